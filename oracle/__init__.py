@@ -12,6 +12,8 @@ Everything here is plain, slow and meant to be read against the pages:
   (flashinfer.gdn_paged, "Page table" and "Slot arguments").
 * ``gdn``   -- the token-by-token fp64 recurrence, the general slot-argument
   prefill/decode and the paged wrappers.
+* ``attention`` -- rotary positions, the append and attention over a paged
+  key/value cache, from their definitions.
 
 Pins (see ``tests/test_oracle_*.py``): the worked examples the pages print,
 closed forms, special cases and brute force on tiny inputs; every function
@@ -22,4 +24,4 @@ by invariants (split invariance, linearity in the start state, decode as a
 one-token prefill) rather than by printed numbers.
 """
 
-from . import csr, slots, gdn  # noqa: F401
+from . import attention, csr, slots, gdn  # noqa: F401

@@ -5,6 +5,15 @@ The compute runs in hand-written HIP kernels in ``libgdn_paged.so`` (C ABI:
 Build the library with ``python -m paged_recurrent_state_amd.build``.
 """
 
+from ._attention import (  # noqa: F401
+    attention_decode_paged,
+    attention_prefill_paged,
+    attention_workspace_size,
+    kv_append_paged,
+    rope,
+    rope_backward,
+    rope_table,
+)
 from ._lib import (  # noqa: F401
     DecodeSlots,
     GDNError,

@@ -65,6 +65,35 @@ class _DecodeSlotsC(C.Structure):
     _fields_ = [("initial_state_indices", C.c_void_p), ("output_state_indices", C.c_void_p)]
 
 
+# include/gdn_attention.h
+class _RowsC(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class _CacheC(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("page_stride", C.c_int64),
+                ("token_stride", C.c_int64), ("head_stride", C.c_int64), ("page_size", C.c_int32),
+                ("num_seqs", C.c_int32), ("page_indices", C.c_void_p), ("page_indptr", C.c_void_p),
+                ("last_page_len", C.c_void_p)]
+
+
+class _RopeC(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("table_rows", C.c_int64), ("rot_dim", C.c_int32),
+                ("interleaved", C.c_int32), ("transposed", C.c_int32)]
+
+
+class _ScalingC(C.Structure):
+    _fields_ = [("scaling", C.c_int32), ("base", C.c_double), ("factor", C.c_double),
+                ("original", C.c_double), ("low_turns", C.c_double), ("high_turns", C.c_double),
+                ("magnitude", C.c_double)]
+
+
+class _AttentionC(C.Structure):
+    _fields_ = [("num_q_heads", C.c_int32), ("num_kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("dtype", C.c_int32), ("scale", C.c_float), ("softcap", C.c_float),
+                ("window", C.c_int32), ("causal", C.c_int32)]
+
+
 class PrefillSlots(NamedTuple):
     """Per-sequence pool rows of a paged prefill batch, all [num_seqs] int32."""
     state_indices: torch.Tensor
@@ -96,7 +125,8 @@ def checked(word: torch.Tensor, num_pages: int, **fields) -> Options:
 EXPORTS = ["gdn_check_paged", "gdn_prefill_slots", "gdn_decode_slots", "gdn_prefill_workspace_size",
            "gdn_prefill_paged", "gdn_prefill_paged_noalloc", "gdn_decode_paged", "gdn_prefill", "gdn_decode",
            "gdn_block_table_to_csr", "gdn_csr_to_block_table", "gdn_stream_copy", "gdn_last_error",
-           "gdn_version"]
+           "gdn_version", "gdn_rope_table", "gdn_rope", "gdn_kv_append_paged", "gdn_attention_workspace_size",
+           "gdn_attention_prefill_paged", "gdn_attention_decode_paged"]
 
 
 def lib_path() -> str:
@@ -112,6 +142,7 @@ def load():
         raise RuntimeError(f"{_LIB_PATH} is not built; run `python -m paged_recurrent_state_amd.build`")
     lib = C.CDLL(_LIB_PATH)
     P, I32, I64, SZ = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
+    R, KV, RP, AT = (C.POINTER(x) for x in (_RowsC, _CacheC, _RopeC, _AttentionC))
     sig = {
         "gdn_check_paged": (C.c_int, [P, P, P, P, I32, I32, I32, P, P]),
         "gdn_prefill_slots": (C.c_int, [P, P, P, P, I32, I32, C.POINTER(_PrefillSlotsC), P]),
@@ -131,6 +162,12 @@ def load():
         "gdn_block_table_to_csr": (C.c_int, [P, I64, P, I32, I32, I32, P, P, P, P, P]),
         "gdn_csr_to_block_table": (C.c_int, [P, P, P, I32, I32, I32, P, I64, P, P, P]),
         "gdn_stream_copy": (C.c_int, [P, P, I64, P]),
+        "gdn_rope_table": (C.c_int, [C.POINTER(_ScalingC), P, I64, I32, P]),
+        "gdn_rope": (C.c_int, [RP, I32, I32, I32, I32, I64, P, I32, R, R, R, R, P]),
+        "gdn_kv_append_paged": (C.c_int, [RP, I32, I32, I32, I32, P, I64, R, R, KV, R, R, P]),
+        "gdn_attention_workspace_size": (SZ, [AT, I64, I32]),
+        "gdn_attention_prefill_paged": (C.c_int, [AT, R, P, I64, KV, R, P, P, SZ, P]),
+        "gdn_attention_decode_paged": (C.c_int, [AT, R, KV, R, P, P, SZ, P]),
         "gdn_last_error": (C.c_char_p, []),
         "gdn_version": (C.c_char_p, []),
     }

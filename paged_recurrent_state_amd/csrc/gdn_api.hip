@@ -1,6 +1,7 @@
 // C-ABI entry points: argument checks, workspace carving and launches.
 // Every host-checkable error returns before any launch; nothing here
 // synchronizes with the device or allocates memory.
+#include "gdn_attention.h"
 #include "gdn_paged.h"
 
 #include <algorithm>
@@ -15,9 +16,9 @@
 
 using namespace gdn;
 
-namespace {
+static thread_local std::string g_err;
 
-thread_local std::string g_err;
+namespace gdn {
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -38,6 +39,10 @@ int launched(hipError_t e, const char* what) {
   if (e != hipSuccess) return fail(GDN_ELAUNCH, "%s launch failed: %s", what, hipGetErrorString(e));
   return GDN_OK;
 }
+
+}  // namespace gdn
+
+namespace {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -687,6 +692,286 @@ int gdn_decode(const gdn_dims_t* dims, const void* q, const void* k, const void*
   dp.out_stride = output_row_stride;
   if (int rc = launched(launch_decode(dp, get_opts(dims).dec, stream), "decode kernel")) return rc;
   return ok();
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------ attention layers
+
+namespace {
+
+int check_type(int32_t dtype, bool f32) {
+  if (dtype == GDN_TYPE_BF16 || dtype == GDN_TYPE_F16 || (f32 && dtype == GDN_TYPE_F32)) return GDN_OK;
+  if (dtype == GDN_TYPE_F32) return fail(GDN_EUNSUPPORTED, "attention takes 16-bit types (got GDN_TYPE_F32)");
+  return fail(GDN_EINVAL, "dtype must be GDN_TYPE_BF16, GDN_TYPE_F16%s (got %d)", f32 ? " or GDN_TYPE_F32" : "",
+              dtype);
+}
+
+RowsDev rows_dev(const gdn_rows_t* r) {
+  return r ? RowsDev{(char*)r->data, r->token_stride, r->head_stride} : RowsDev{nullptr, 0, 0};
+}
+
+// whether every row starts at a multiple of 16 bytes (a stride that only one
+// token or head steps over does not matter)
+bool aligned16(const gdn_rows_t* r, int64_t tokens, int32_t heads, int size) {
+  return !r || ((uintptr_t)r->data % 16 == 0 && (tokens < 2 || r->token_stride * size % 16 == 0) &&
+                (heads < 2 || r->head_stride * size % 16 == 0));
+}
+bool aligned16(const gdn_kv_cache_t* c, int32_t heads, int size) {
+  return (uintptr_t)c->k % 16 == 0 && (uintptr_t)c->v % 16 == 0 && c->page_stride * size % 16 == 0 &&
+         (c->page_size < 2 || c->token_stride * size % 16 == 0) && (heads < 2 || c->head_stride * size % 16 == 0);
+}
+
+int check_rows(const gdn_rows_t* r, const char* name, int64_t tokens) {
+  if (!r) return fail(GDN_EINVAL, "%s must not be NULL", name);
+  if (tokens > 0 && !r->data) return fail(GDN_EINVAL, "%s has no data", name);
+  return GDN_OK;
+}
+
+int check_cache(const gdn_kv_cache_t* c) {
+  if (!c) return fail(GDN_EINVAL, "cache is NULL");
+  if (c->num_seqs < 0) return fail(GDN_EINVAL, "num_seqs must be >= 0 (got %d)", c->num_seqs);
+  if (c->page_size < 1) return fail(GDN_EINVAL, "page_size must be >= 1 (got %d)", c->page_size);
+  if (c->num_seqs > 0 && (!c->k || !c->v || !c->page_indices || !c->page_indptr || !c->last_page_len))
+    return fail(GDN_EINVAL, "the cache and its page table must not be NULL");
+  return GDN_OK;
+}
+
+KvDev kv_dev(const gdn_kv_cache_t* c) {
+  return KvDev{(char*)c->k,  (char*)c->v,          c->page_stride, c->token_stride, c->head_stride,
+               fast_div((uint32_t)c->page_size), c->num_seqs,    c->page_indices, c->page_indptr, c->last_page_len};
+}
+
+int check_token_count(int64_t tokens) {
+  if (tokens < 0 || tokens >= (int64_t(1) << 31))
+    return fail(GDN_EINVAL, "the number of tokens must be 0 .. 2^31 - 1 (got %lld)", (long long)tokens);
+  return GDN_OK;
+}
+
+int check_rope(const gdn_rope_t* r, int32_t head_dim) {
+  if (!r->table && r->table_rows > 0) return fail(GDN_EINVAL, "rope.table must not be NULL");
+  if (r->table_rows < 0) return fail(GDN_EINVAL, "rope.table_rows must be >= 0");
+  if (r->rot_dim < 2 || r->rot_dim % 2 || r->rot_dim > head_dim)
+    return fail(GDN_EINVAL, "rope.rot_dim must be even and 2 .. head_dim (got %d of %d)", r->rot_dim, head_dim);
+  return GDN_OK;
+}
+
+int check_heads(int32_t head_dim, int32_t q, int32_t k) {
+  if (head_dim < 1 || head_dim > 65536) return fail(GDN_EINVAL, "head_dim must be 1 .. 65536 (got %d)", head_dim);
+  if (q < 0 || k < 0 || (int64_t)q + 2 * (int64_t)k > 65536)
+    return fail(GDN_EINVAL, "head counts must be >= 0 and at most 65536 together (%d, %d)", q, k);
+  return GDN_OK;
+}
+
+int type_size(int32_t dtype) { return dtype == GDN_TYPE_F32 ? 4 : 2; }
+
+// 16-byte accesses: whole 8-value pieces with their pairs in one thread
+bool rope_vec(const RopeParams& p, const gdn_rope_t* r, int size) {
+  return p.D % 16 == 0 && (!r || (r->rot_dim % 16 == 0 && (uintptr_t)r->table % 16 == 0));
+}
+
+void set_rope(RopeParams& p, const gdn_rope_t* r) {
+  if (!r) return;
+  p.table = r->table;
+  p.table_rows = r->table_rows;
+  p.rot = r->rot_dim;
+  p.sign = r->transposed ? -1.f : 1.f;
+}
+
+int check_attention(const gdn_attention_dims_t* d) {
+  if (!d) return fail(GDN_EINVAL, "dims is NULL");
+  if (d->num_q_heads < 1 || d->num_kv_heads < 1)
+    return fail(GDN_EINVAL, "head counts must be positive (q %d, kv %d)", d->num_q_heads, d->num_kv_heads);
+  if (int rc = check_type(d->dtype, false)) return rc;
+  if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256)
+    return fail(GDN_EUNSUPPORTED, "head_dim must be 64, 128 or 256 (got %d)", d->head_dim);
+  if (d->num_q_heads % d->num_kv_heads || d->num_q_heads > 65535)
+    return fail(GDN_EUNSUPPORTED, "q-heads (%d) must be a multiple of kv-heads (%d), at most 65535",
+                d->num_q_heads, d->num_kv_heads);
+  if (d->window < 0) return fail(GDN_EINVAL, "window must be >= 0 (got %d)", d->window);
+  if (std::isnan(d->scale) || std::isnan(d->softcap) || std::isinf(d->scale) || std::isinf(d->softcap))
+    return fail(GDN_EINVAL, "scale and softcap must be finite");
+  return GDN_OK;
+}
+
+int run_attention(const gdn_attention_dims_t* dims, const gdn_rows_t* q, const int32_t* cu, int64_t T,
+                  const gdn_kv_cache_t* cache, const gdn_rows_t* out, float* lse, void* workspace,
+                  size_t workspace_bytes, hipStream_t stream) {
+  if (T == 0 || cache->num_seqs == 0) return ok();
+  const int32_t group = dims->num_q_heads / dims->num_kv_heads;
+  if (T * group >= (int64_t(1) << 31))
+    return fail(GDN_EINVAL, "query rows of a kv-head (%lld) must stay below 2^31", (long long)(T * group));
+  if (!aligned16(q, T, dims->num_q_heads, 2)) return fail(GDN_EINVAL, "rows of q must be 16-byte aligned");
+  if (!aligned16(out, T, dims->num_q_heads, 2)) return fail(GDN_EINVAL, "rows of out must be 16-byte aligned");
+  if (!aligned16(cache, dims->num_kv_heads, 2))
+    return fail(GDN_EINVAL, "rows of the cache must be 16-byte aligned");
+  const size_t need = gdn_attention_workspace_size(dims, T, cache->num_seqs);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(GDN_EWORKSPACE, "workspace needs %zu bytes, got %zu", need, workspace ? workspace_bytes : 0);
+  AttnParams p{};
+  p.q = rows_dev(q);
+  p.o = rows_dev(out);
+  p.lse = lse;
+  p.cu = cu;
+  p.kv = kv_dev(cache);
+  p.T = T;
+  p.Hq = dims->num_q_heads;
+  p.Hkv = dims->num_kv_heads;
+  p.group = fast_div((uint32_t)group);
+  p.window = dims->window;
+  p.causal = dims->causal != 0;
+  const double scale = dims->scale > 0.f ? dims->scale : 1.0 / std::sqrt((double)dims->head_dim);
+  const double log2e = 1.4426950408889634074;
+  if (dims->softcap > 0.f) {
+    p.scale = (float)(scale / dims->softcap);
+    p.cap = (float)(dims->softcap * log2e);
+  } else {
+    p.scale = (float)(scale * log2e);
+  }
+  if (int rc = launched(launch_attention(p, dims->head_dim, dims->dtype, stream), "attention kernel")) return rc;
+  return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+int gdn_rope_table(const gdn_rope_scaling_t* scaling, float* table, int64_t rows, int32_t rot_dim,
+                   hipStream_t stream) {
+  if (!scaling) return fail(GDN_EINVAL, "scaling is NULL");
+  if (rows < 0 || (rows > 0 && !table)) return fail(GDN_EINVAL, "table must hold rows >= 0 rows");
+  if (rot_dim < 2 || rot_dim % 2 || rot_dim > 1024)
+    return fail(GDN_EINVAL, "rot_dim must be even and 2 .. 1024 (got %d)", rot_dim);
+  const int kind = scaling->scaling;
+  if (kind < GDN_ROPE_PLAIN || kind > GDN_ROPE_BANDS) return fail(GDN_EINVAL, "unknown scaling %d", kind);
+  if (!(scaling->base > 0.0) || std::isinf(scaling->base)) return fail(GDN_EINVAL, "base must be positive");
+  if (!std::isfinite(scaling->magnitude)) return fail(GDN_EINVAL, "magnitude must be finite");
+  const double factor = kind == GDN_ROPE_PLAIN ? 1.0 : scaling->factor;
+  if (!(factor > 0.0) || std::isinf(factor)) return fail(GDN_EINVAL, "factor must be positive");
+  double base = scaling->base;
+  if (kind == GDN_ROPE_BASE) {
+    if (rot_dim == 2) return fail(GDN_EINVAL, "GDN_ROPE_BASE needs rot_dim > 2");
+    base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+  }
+  if (kind == GDN_ROPE_BANDS &&
+      (!(scaling->original > 0.0) || !(scaling->high_turns > scaling->low_turns) || !std::isfinite(scaling->original) ||
+       !std::isfinite(scaling->high_turns) || !std::isfinite(scaling->low_turns)))
+    return fail(GDN_EINVAL, "GDN_ROPE_BANDS needs original > 0 and high_turns > low_turns");
+  if (int rc = launched(launch_rope_table(table, rows, rot_dim, base, kind == GDN_ROPE_BASE ? 1.0 : factor,
+                                          kind == GDN_ROPE_BANDS, scaling->original, scaling->low_turns,
+                                          scaling->high_turns, scaling->magnitude, stream),
+                        "rotary table kernel"))
+    return rc;
+  return ok();
+}
+
+int gdn_rope(const gdn_rope_t* rope, int32_t dtype, int32_t head_dim, int32_t num_q_heads, int32_t num_k_heads,
+             int64_t num_tokens, const void* positions, int32_t index_dtype, const gdn_rows_t* q,
+             const gdn_rows_t* k, const gdn_rows_t* q_out, const gdn_rows_t* k_out, hipStream_t stream) {
+  if (!rope) return fail(GDN_EINVAL, "rope is NULL");
+  if (int rc = check_type(dtype, true)) return rc;
+  if (int rc = check_heads(head_dim, num_q_heads, num_k_heads)) return rc;
+  if (int rc = check_rope(rope, head_dim)) return rc;
+  if (int rc = check_token_count(num_tokens)) return rc;
+  if (index_dtype != GDN_INDEX_INT32 && index_dtype != GDN_INDEX_INT64)
+    return fail(GDN_EINVAL, "index_dtype must be GDN_INDEX_INT32 or GDN_INDEX_INT64");
+  if (num_tokens > 0 && !positions) return fail(GDN_EINVAL, "positions must not be NULL");
+  if (num_q_heads > 0) {
+    if (int rc = check_rows(q, "q", num_tokens)) return rc;
+    if (int rc = check_rows(q_out, "q_out", num_tokens)) return rc;
+  }
+  if (num_k_heads > 0) {
+    if (int rc = check_rows(k, "k", num_tokens)) return rc;
+    if (int rc = check_rows(k_out, "k_out", num_tokens)) return rc;
+  }
+  RopeParams p{};
+  set_rope(p, rope);
+  p.D = head_dim;
+  p.Hq = num_q_heads;
+  p.Hk = num_k_heads;
+  p.q = rows_dev(q);
+  p.k = rows_dev(k);
+  p.q_out = rows_dev(q_out);
+  p.k_out = rows_dev(k_out);
+  p.T = num_tokens;
+  p.pos = positions;
+  p.pos64 = index_dtype == GDN_INDEX_INT64;
+  p.kv.page = fast_div(1);
+  const int sz = type_size(dtype);
+  bool vec = rope_vec(p, rope, sz);
+  if (num_q_heads) vec = vec && aligned16(q, num_tokens, num_q_heads, sz) && aligned16(q_out, num_tokens, num_q_heads, sz);
+  if (num_k_heads) vec = vec && aligned16(k, num_tokens, num_k_heads, sz) && aligned16(k_out, num_tokens, num_k_heads, sz);
+  if (int rc = launched(launch_rope(p, dtype, rope->interleaved != 0, vec, stream), "rotary kernel")) return rc;
+  return ok();
+}
+
+int gdn_kv_append_paged(const gdn_rope_t* rope, int32_t dtype, int32_t head_dim, int32_t num_q_heads,
+                        int32_t num_kv_heads, const int32_t* cu_seqlens, int64_t total_tokens,
+                        const gdn_rows_t* k, const gdn_rows_t* v, const gdn_kv_cache_t* cache,
+                        const gdn_rows_t* q, const gdn_rows_t* q_out, hipStream_t stream) {
+  if (int rc = check_type(dtype, true)) return rc;
+  const int32_t Hq = q ? num_q_heads : 0;
+  if (int rc = check_heads(head_dim, Hq, num_kv_heads)) return rc;
+  if (num_kv_heads < 1) return fail(GDN_EINVAL, "num_kv_heads must be positive (got %d)", num_kv_heads);
+  if (int rc = check_cache(cache)) return rc;
+  if (rope)
+    if (int rc = check_rope(rope, head_dim)) return rc;
+  if (int rc = check_token_count(total_tokens)) return rc;
+  if (!cu_seqlens && total_tokens != cache->num_seqs)
+    return fail(GDN_EINVAL, "without cu_seqlens there is one token per sequence (%lld tokens, %d sequences)",
+                (long long)total_tokens, cache->num_seqs);
+  if (int rc = check_rows(k, "k", total_tokens)) return rc;
+  if (int rc = check_rows(v, "v", total_tokens)) return rc;
+  if (q) {
+    if (int rc = check_rows(q, "q", total_tokens)) return rc;
+    if (int rc = check_rows(q_out, "q_out", total_tokens)) return rc;
+  }
+  if (total_tokens == 0 || cache->num_seqs == 0) return ok();
+  RopeParams p{};
+  set_rope(p, rope);
+  p.D = head_dim;
+  p.Hq = Hq;
+  p.Hk = p.Hv = num_kv_heads;
+  p.q = rows_dev(q);
+  p.k = rows_dev(k);
+  p.v = rows_dev(v);
+  p.q_out = rows_dev(q_out);
+  p.T = total_tokens;
+  p.cu = cu_seqlens;
+  p.kv = kv_dev(cache);
+  const int sz = type_size(dtype);
+  bool vec = rope_vec(p, rope, sz) && aligned16(k, total_tokens, num_kv_heads, sz) &&
+             aligned16(v, total_tokens, num_kv_heads, sz) && aligned16(cache, num_kv_heads, sz);
+  if (q) vec = vec && aligned16(q, total_tokens, Hq, sz) && aligned16(q_out, total_tokens, Hq, sz);
+  if (int rc = launched(launch_rope(p, dtype, rope && rope->interleaved != 0, vec, stream), "append kernel")) return rc;
+  return ok();
+}
+
+size_t gdn_attention_workspace_size(const gdn_attention_dims_t* dims, int64_t total_tokens, int32_t num_seqs) {
+  if (check_attention(dims) || total_tokens < 0 || num_seqs < 0) return 0;
+  return 256;
+}
+
+int gdn_attention_prefill_paged(const gdn_attention_dims_t* dims, const gdn_rows_t* q, const int32_t* cu_seqlens,
+                                int64_t total_tokens, const gdn_kv_cache_t* cache, const gdn_rows_t* out, float* lse,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (int rc = check_attention(dims)) return rc;
+  if (int rc = check_cache(cache)) return rc;
+  if (int rc = check_token_count(total_tokens)) return rc;
+  if (!cu_seqlens) return fail(GDN_EINVAL, "cu_seqlens must not be NULL");
+  if (int rc = check_rows(q, "q", total_tokens)) return rc;
+  if (int rc = check_rows(out, "out", total_tokens)) return rc;
+  return run_attention(dims, q, cu_seqlens, total_tokens, cache, out, lse, workspace, workspace_bytes, stream);
+}
+
+int gdn_attention_decode_paged(const gdn_attention_dims_t* dims, const gdn_rows_t* q, const gdn_kv_cache_t* cache,
+                               const gdn_rows_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                               hipStream_t stream) {
+  if (int rc = check_attention(dims)) return rc;
+  if (int rc = check_cache(cache)) return rc;
+  if (int rc = check_rows(q, "q", cache->num_seqs)) return rc;
+  if (int rc = check_rows(out, "out", cache->num_seqs)) return rc;
+  return run_attention(dims, q, nullptr, cache->num_seqs, cache, out, lse, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -167,6 +167,78 @@ struct DecodeShape {
 };
 hipError_t launch_decode(const DecodeParams& p, const DecodeShape& shape, hipStream_t s);
 
+// Division by a fixed divisor: n / d for 0 <= n < 2^31 and 1 <= d < 2^31, as
+// (n * mul) >> sh with mul = floor(2^sh / d) + 1, sh = 31 + ceil(log2 d).
+// mul < 2^32, and n (mul d - 2^sh) < 2^31 d <= 2^sh, so the floor is exact.
+struct FastDiv {
+  uint32_t d, mul, sh;
+};
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t lg = 0;
+  while ((uint64_t(1) << lg) < d) ++lg;
+  return FastDiv{d, uint32_t((uint64_t(1) << (31 + lg)) / d + 1), 31 + lg};
+}
+
+// Rows [tokens, heads, dim] in device memory (strides in elements).
+struct RowsDev {
+  char* p;
+  int64_t ts, hs;
+};
+
+// A CSR page table and the caches it addresses (strides in elements).
+struct KvDev {
+  char* k;
+  char* v;
+  int64_t ps, ts, hs;
+  FastDiv page;  // tokens per page
+  int B;
+  const int32_t* idx;
+  const int32_t* ptr;
+  const int32_t* lpl;
+};
+
+// Rotary positions (gdn_rope) and the append that rotates on the way.
+struct RopeParams {
+  const float* table;  // null: no rotation
+  int64_t table_rows;
+  int rot;
+  float sign;  // -1: the transposed map
+  int D, Hq, Hk, Hv;  // Hv = Hk for the append, 0 for gdn_rope
+  RowsDev q, k, v, q_out, k_out;
+  int64_t T;
+  const void* pos;  // gdn_rope: positions; null: places in the page table
+  int pos64;
+  const int32_t* cu;  // append: null = one token per sequence
+  KvDev kv;
+  int tokens_per_block;
+  FastDiv heads;       // Hq + Hk + Hv
+  FastDiv row_units;   // threads a row takes
+};
+hipError_t launch_rope(RopeParams p, int dtype, bool interleaved, bool vec, hipStream_t s);
+hipError_t launch_rope_table(float* table, int64_t rows, int rot, double base, double factor, int bands,
+                             double original, double low, double high, double magnitude, hipStream_t s);
+
+// Attention over the paged cache.
+struct AttnParams {
+  RowsDev q, o;
+  float* lse;
+  const int32_t* cu;  // null: one token per sequence
+  KvDev kv;
+  int64_t T;
+  int Hq, Hkv;
+  FastDiv group;  // q-heads per kv-head
+  int window;     // 0: none
+  int causal;
+  float scale;    // of the raw scores, in log2 units (softcap: scale / softcap)
+  float cap;      // softcap in log2 units, 0: none
+};
+hipError_t launch_attention(const AttnParams& p, int D, int dtype, hipStream_t s);
+
+// Errors of the C-ABI layer (gdn_api.hip): the thread's message and a status.
+int fail(int code, const char* fmt, ...);
+int ok();
+int launched(hipError_t e, const char* what);
+
 // Compute units of the current device (queried once per device).
 int device_cus();
 // Index of the current device, or -1 (for per-device caches of size kMaxDevices).
@@ -175,6 +247,25 @@ int current_device();
 
 // ---------------------------------------------------------------- device helpers
 #if defined(__HIP_DEVICE_COMPILE__) || defined(__HIPCC__)
+
+__device__ __forceinline__ uint32_t div_by(uint32_t n, FastDiv f) {
+  return (uint32_t)((uint64_t(n) * f.mul) >> f.sh);
+}
+
+// The sequence of new token t: how many of cu[1 .. B] are <= t (the whole wave
+// searches together, 64 ways a step).
+__device__ __forceinline__ int wave_find_seq(const int32_t* cu, int B, int t) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = B;
+  while (n > 0) {
+    const int step = (n + 63) >> 6;
+    const int64_t at = int64_t(lane + 1) * step;
+    const int c = __popcll(__ballot(at <= n && cu[lo + (at <= n ? at : 1)] <= t));
+    lo += c * step;
+    n = step == 1 ? 0 : min(step - 1, n - c * step);
+  }
+  return lo;
+}
 
 __device__ __forceinline__ float bf2f(u16 b) { return __uint_as_float(uint32_t(b) << 16); }
 
