@@ -828,7 +828,7 @@ int run_attention(const gdn_attention_dims_t* dims, const gdn_rows_t* q, const i
   } else {
     p.scale = (float)(scale * log2e);
   }
-  if (int rc = launched(launch_attention(p, dims->head_dim, dims->dtype, stream), "attention kernel")) return rc;
+  if (int rc = launched(launch_attention(p, dims->head_dim, dims->dtype, workspace, stream), "attention kernel")) return rc;
   return ok();
 }
 
@@ -949,7 +949,7 @@ int gdn_kv_append_paged(const gdn_rope_t* rope, int32_t dtype, int32_t head_dim,
 
 size_t gdn_attention_workspace_size(const gdn_attention_dims_t* dims, int64_t total_tokens, int32_t num_seqs) {
   if (check_attention(dims) || total_tokens < 0 || num_seqs < 0) return 0;
-  return 256;
+  return attention_bytes(dims->head_dim);
 }
 
 int gdn_attention_prefill_paged(const gdn_attention_dims_t* dims, const gdn_rows_t* q, const int32_t* cu_seqlens,

@@ -268,6 +268,444 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
   }
 }
 
+// ------------------------------------------------------------------ decode
+//
+// One token per sequence: the G query rows of a kv-head against every key the
+// sequence holds.  Bound by reading the cache once, so the work is cut by bytes:
+// every (sequence, kv-head) is a run of 128-key tiles, the runs of the batch laid
+// end to end are cut into equal shares, one a workgroup, and a run that crosses
+// shares is joined afterwards from its parts' (m, l, o).
+//
+// The four waves of a workgroup take 32 of a tile's 128 keys each and never wait
+// for each other within a run: a wave loads its keys and values straight into
+// its own ring in LDS, and reads them once they have landed while the next are
+// on the way.  Products on 16x16x32 MFMAs in the same transposed form as above;
+// P enters as the sum of two 16-bit parts (the matrix units idle anyway), so
+// what it adds to the output's own rounding is invisible.
+
+constexpr int kDecKeys = 32;                     // keys of a wave's tile
+constexpr int kDecTile = kDecKeys * kWaves;      // keys of a workgroup's tile
+constexpr int kDecRows = 16;                     // query rows of a workgroup
+constexpr int kDecPages = 1024;                  // page ids staged at a time
+template <int D>
+constexpr int kDecStages = D == 64 ? 2 : 1;      // tiles of keys (and of values) in a wave's ring
+template <int D>
+constexpr int kDecLds = kWaves * kDecStages<D> * 2 * kDecKeys * D * 2;
+
+typedef __attribute__((address_space(3))) char* lds_ptr;
+
+__device__ __forceinline__ uint32_t lds_of(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
+// One 16-byte global->LDS load a lane: lane l's bytes land at byte 16 l of the
+// 1 KiB block at `lds`.  In assembly, so that the compiler neither drains every
+// LDS read for it nor counts it; its completion is awaited explicitly.  (One wait
+// state between the M0 write and the load that reads it.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+template <bool NT>
+__device__ __forceinline__ void dma16(uint32_t lds, const void* src) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane(lds);
+  if constexpr (NT)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" ::"s"(at), "v"(src)
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src)
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+__device__ const u32x4 g_zero = {0u, 0u, 0u, 0u};  // read in place of keys outside a run
+
+template <class E>
+__device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c);
+template <>
+__device__ __forceinline__ f32x4 mfma16<Bf>(u32x4 a, u32x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                 0, 0);
+}
+template <>
+__device__ __forceinline__ f32x4 mfma16<Hf>(u32x4 a, u32x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                0);
+}
+
+// Two weights as hi + lo in the element type: hi cut off, not rounded, so that lo
+// is not negative, and lo at least a trace of the weight: an infinite value that a
+// row sees then reaches its output as that infinity, never as 0 * inf.
+template <class E>
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo);
+template <>
+__device__ __forceinline__ void split2<Bf>(float a, float b, uint32_t& hi, uint32_t& lo) {
+  const uint32_t x = __float_as_uint(a) & 0xffff0000u, y = __float_as_uint(b) & 0xffff0000u;
+  hi = (x >> 16) | y;
+  lo = f2bf2(fmaxf(a - __uint_as_float(x), a * 0x1p-20f), fmaxf(b - __uint_as_float(y), b * 0x1p-20f));
+}
+template <>
+__device__ __forceinline__ void split2<Hf>(float a, float b, uint32_t& hi, uint32_t& lo) {
+  const f16x2 h = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_pkrtz(a, b));
+  hi = __builtin_bit_cast(uint32_t, h);
+  lo = Hf::pack(fmaxf(a - (float)h[0], fminf(a, 0x1p-24f)), fmaxf(b - (float)h[1], fminf(b, 0x1p-24f)));
+}
+
+// Tokens sequence b holds, and the first its (only) query sees.
+struct Span {
+  int first_page, len, begin;
+};
+__device__ __forceinline__ Span dec_span(const AttnParams& p, int b) {
+  const int f = p.kv.ptr[b], pages = p.kv.ptr[b + 1] - f;
+  const int len = pages > 0 ? (pages - 1) * (int)p.kv.page.d + p.kv.lpl[b] : 0;
+  return Span{f, len, p.window > 0 ? max(0, len - p.window) : 0};
+}
+// its 128-key tiles, counted from the one that holds `begin`
+__device__ __forceinline__ int dec_tiles(const Span& s) {
+  return s.len <= s.begin ? 0 : (s.len + kDecTile - 1) / kDecTile - s.begin / kDecTile;
+}
+
+// Score in log2 units.
+template <bool CAP>
+__device__ __forceinline__ float score(const AttnParams& p, float x) {
+  x *= p.scale;
+  if constexpr (CAP) x = p.cap * tanhf(x);
+  return x;
+}
+
+template <class E, int D, bool CAP>
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(AttnParams p) {
+  constexpr int NS = kDecStages<D>;
+  constexpr int kSlot = kDecKeys * D * 2;     // bytes of 32 keys
+  constexpr int kLoads = kSlot / 1024;        // load instructions of 32 keys
+  constexpr int kRowsPerLoad = 512 / D;
+  constexpr int kSteps = D / 32, kBlocks = D / 16;
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  __shared__ int page_ids[kDecPages];
+  __shared__ int s_where[3];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, grp = lane >> 4, col = lane & 15;
+  const int G = (int)p.group.d, vh = (G + kDecRows - 1) / kDecRows;  // row blocks of a kv-head
+  const int heads = p.Hkv * vh, B = p.kv.B;
+
+  // sequences without a token: zeros
+  for (int b = blockIdx.x; b < B; b += gridDim.x)
+    if (dec_span(p, b).len <= 0) {
+      for (int x = tid; x < p.Hq * (D / 8); x += 64 * kWaves)
+        *(u32x4*)((u16*)p.o.p + (int64_t)b * p.o.ts + (int64_t)(x / (D / 8)) * p.o.hs + 8 * (x % (D / 8))) =
+            u32x4{0u, 0u, 0u, 0u};
+      if (p.lse)
+        for (int h = tid; h < p.Hq; h += 64 * kWaves) p.lse[(int64_t)b * p.Hq + h] = -INFINITY;
+    }
+
+  // this workgroup's share: units first .. end of the runs laid end to end
+  const int per = (B + 64 * kWaves - 1) / (64 * kWaves);
+  int mine = 0;
+  for (int b = tid * per; b < min(B, (tid + 1) * per); ++b) mine += dec_tiles(dec_span(p, b));
+  int total;
+  const int before = block_exclusive_scan(mine, &total);
+  const int64_t units = (int64_t)total * heads;
+  const int64_t share = (units + gridDim.x - 1) / gridDim.x;
+  const int64_t first = (int64_t)blockIdx.x * share, end = min(units, first + share);
+  int* tail = p.parts + 2 * blockIdx.x;  // {item, parts} of the run this share leaves unfinished
+  if (first >= end) {
+    if (tid == 0) tail[0] = -1;
+    return;
+  }
+  if (first >= (int64_t)before * heads && first < (int64_t)(before + mine) * heads) {
+    int64_t at = (int64_t)before * heads;
+    int b = tid * per;
+    for (;; ++b) {
+      const int64_t n = (int64_t)dec_tiles(dec_span(p, b)) * heads;
+      if (first < at + n) break;
+      at += n;
+    }
+    s_where[0] = b;
+    s_where[1] = (int)((first - at) / dec_tiles(dec_span(p, b)));
+    s_where[2] = (int)((first - at) % dec_tiles(dec_span(p, b)));
+  }
+  __syncthreads();
+  int b = s_where[0], h = s_where[1], t = s_where[2];
+  bool left = false;  // an unfinished run
+
+  char* ring = smem + wave * (2 * NS * kSlot);
+  for (int64_t u = first; u < end;) {
+    const Span sp = dec_span(p, b);
+    const int tiles = dec_tiles(sp);
+    if (tiles == 0) {
+      ++b;
+      continue;
+    }
+    const int todo = (int)min((int64_t)(tiles - t), end - u);  // tiles of this run taken here
+    const int hk = h / vh, row0 = (h - hk * vh) * kDecRows, rows = min(kDecRows, G - row0);
+
+    u32x4 q[kSteps];
+    {
+      const u16* src = (const u16*)p.q.p + (int64_t)b * p.q.ts + (int64_t)(hk * G + row0 + min(col, rows - 1)) * p.q.hs;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) q[s] = *(const u32x4*)(src + 32 * s + 8 * grp);
+    }
+    f32x4 o[kBlocks];
+    float m = kNoScore, l = 0.f;
+#pragma unroll
+    for (int d = 0; d < kBlocks; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    const int key_a = (sp.begin / kDecTile + t) * kDecTile;           // keys of this part
+    const int key_b = min(sp.len, key_a + todo * kDecTile);
+    const char* kbase = p.kv.k + 2 * (int64_t)hk * p.kv.hs;
+    const int64_t vdiff = p.kv.v - p.kv.k;
+
+    // as many tiles at a time as the staged page ids reach
+    for (int a0 = max(key_a, sp.begin); a0 < key_b;) {
+      const int page0 = (int)div_by(a0, p.kv.page);
+      const int64_t reach = (int64_t)(page0 + kDecPages) * p.kv.page.d;  // first key past the staged pages
+      // (whole tiles; kDecPages pages are more than a tile's keys)
+      const int a1 = reach >= key_b ? key_b : (int)reach / kDecTile * kDecTile;
+      __syncthreads();
+      {
+        const int last = (int)div_by(a1 - 1, p.kv.page);
+        for (int i = tid; i <= last - page0; i += 64 * kWaves) page_ids[i] = p.kv.idx[sp.first_page + page0 + i];
+      }
+      __syncthreads();
+      const int start = a0 / kDecTile * kDecTile + wave * kDecKeys;   // this wave's first tile
+      const int n = (a1 - a0 / kDecTile * kDecTile + kDecTile - 1) / kDecTile;
+
+      // values (V) or keys of tile i into their slot
+      auto load = [&](int i, bool V) {
+        const uint32_t dst = lds_of(ring + (V ? NS * kSlot : 0) + (i % NS) * kSlot);
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x) {
+          const int r = x * kRowsPerLoad + lane / (D / 8), slot = lane % (D / 8);
+          // the piece that belongs at this lane's place: the turning is its own inverse
+          const int c = V ? (slot ^ (D == 64 ? ((r >> 1) & 1) << 2 : (r & 3) << 2))
+                          : (slot ^ (D == 64 ? (r >> 1) & 7 : r & 15));
+          const int key = start + i * kDecTile + r;
+          const char* src = (const char*)&g_zero;
+          if (key >= a0 && key < a1 && i < n) {
+            const int pg = (int)div_by(key, p.kv.page);
+            src = kbase + 2 * ((int64_t)page_ids[pg - page0] * p.kv.ps + (int64_t)(key - pg * (int)p.kv.page.d) * p.kv.ts +
+                               8 * c) + (V ? vdiff : 0);
+          }
+          dma16<true>(dst + x * 1024, src);
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        load(i, false);
+        load(i, true);
+      }
+      for (int i = 0; i < n; ++i) {
+        const char* sk = ring + (i % NS) * kSlot;
+        const char* sv = ring + NS * kSlot + (i % NS) * kSlot;
+        // outstanding after the keys of tile i: its values and NS - 1 whole tiles
+        wait_vm<(2 * NS - 1) * kLoads>();
+        f32x4 s[2];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          s[kb] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int x = 0; x < kSteps; ++x)
+            s[kb] = mfma16<E>(*(const u32x4*)(sk + k_at<D>(kb * 16 + col, 4 * x + grp)), q[x], s[kb]);
+        }
+        wait_lds();
+        load(i + NS, false);
+        float x[8], top = -INFINITY;
+        const int key = start + i * kDecTile + 4 * grp;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int k = key + 16 * (e >> 2) + (e & 3);
+          x[e] = k >= a0 && k < a1 ? score<CAP>(p, s[e >> 2][e & 3]) : -INFINITY;
+          top = fmaxf(top, x[e]);
+        }
+        if (__any(top > m + (E::kBias + E::kSlack))) {
+          top = fmaxf(top, __shfl_xor(top, 16, 64));
+          top = fmaxf(top, __shfl_xor(top, 32, 64)) - E::kBias;
+          const float to = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - to);
+          m = to;
+          l *= f;
+#pragma unroll
+          for (int d = 0; d < kBlocks; ++d) o[d] *= f;
+        }
+        u32x4 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float a = __builtin_amdgcn_exp2f(x[e] - m), c = __builtin_amdgcn_exp2f(x[e + 1] - m);
+          l += a + c;
+          uint32_t wh, wl;
+          split2<E>(a, c, wh, wl);
+          hi[e >> 1] = wh;
+          lo[e >> 1] = wl;
+        }
+        // outstanding after the values of tile i: NS - 1 tiles and the keys just asked for
+        wait_vm<(2 * NS - 1) * kLoads>();
+#pragma unroll
+        for (int d = 0; d < kBlocks; ++d) {
+          // keys 4 grp + 0..3 and 16 more, in the order S left them
+          const int kr = 4 * grp + (col >> 2), dim = 16 * d + 4 * (lane & 3), sub = (dim & 7) * 2;
+          const s16x4 wl = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(sv + v_at<D>(kr, dim >> 3) + sub));
+          const s16x4 wh = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(sv + v_at<D>(kr + 16, dim >> 3) + sub));
+          const u32x2 a = __builtin_bit_cast(u32x2, wl), c = __builtin_bit_cast(u32x2, wh);
+          const u32x4 vf{a[0], a[1], c[0], c[1]};
+          o[d] = mfma16<E>(vf, lo, o[d]);
+          o[d] = mfma16<E>(vf, hi, o[d]);
+        }
+        wait_lds();
+        load(i + NS, true);
+      }
+      wait_vm<0>();
+      a0 = a1;
+    }
+
+    // join the four waves
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+    float* mo = (float*)smem;
+    __syncthreads();
+    __shared__ float ml[kWaves][kDecRows][2];
+#pragma unroll
+    for (int d = 0; d < kBlocks; ++d) *(f32x4*)(mo + (wave * kDecRows + col) * D + 16 * d + 4 * grp) = o[d];
+    if (grp == 0) {
+      ml[wave][col][0] = m;
+      ml[wave][col][1] = l;
+    }
+    __syncthreads();
+    const bool whole = t == 0 && todo == tiles;
+    const bool head = t > 0;  // a part that continues a run: slot 0, one that starts it: slot 1
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (head ? 0 : 1);
+    for (int x = tid; x < rows * (D / 4); x += 64 * kWaves) {
+      const int r = x / (D / 4), d = 4 * (x % (D / 4));
+      float top = ml[0][r][0];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, ml[w][r][0]);
+      float sum = 0.f;
+      f32x4 acc{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = __builtin_amdgcn_exp2f(ml[w][r][0] - top);
+        sum += f * ml[w][r][1];
+        acc += f * *(const f32x4*)(mo + (w * kDecRows + r) * D + d);
+      }
+      if (whole) {
+        const int64_t hq = (int64_t)hk * G + row0 + r;
+        acc *= 1.f / sum;
+        *(u32x2*)((u16*)p.o.p + (int64_t)b * p.o.ts + hq * p.o.hs + d) =
+            u32x2{E::pack(acc[0], acc[1]), E::pack(acc[2], acc[3])};
+        if (p.lse && d == 0) p.lse[(int64_t)b * p.Hq + hq] = (top + __builtin_amdgcn_logf(sum)) * kLn2;
+      } else {
+        *(f32x4*)(p.part_o + (slot * kDecRows + r) * D + d) = acc;
+        if (d == 0) {
+          p.part_ml[(slot * kDecRows + r) * 2] = top;
+          p.part_ml[(slot * kDecRows + r) * 2 + 1] = sum;
+        }
+      }
+    }
+    if (!whole && !head) {
+      left = true;
+      if (tid == 0) {
+        tail[0] = b * heads + h;
+        tail[1] = (int)((u + (tiles - t) - 1) / share) - (int)blockIdx.x + 1;
+      }
+    }
+    u += todo;
+    t += todo;
+    if (t == tiles) {
+      t = 0;
+      if (++h == heads) {
+        h = 0;
+        ++b;
+      }
+    }
+    __syncthreads();
+  }
+  if (!left && tid == 0) tail[0] = -1;
+}
+
+// Joins the parts of the runs that cross shares: workgroup (w, r) takes row r of
+// the run that share w leaves unfinished; its parts are slot 1 of w and slot 0 of
+// the shares after it.
+template <class E, int D>
+__global__ __launch_bounds__(256) void decode_join_kernel(AttnParams p) {
+  constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
+  const int w = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, d = 4 * (tid % kLanes), g = tid / kLanes;
+  const int item = p.parts[2 * w], parts = p.parts[2 * w + 1];
+  if (item < 0) return;
+  const int G = (int)p.group.d, vh = (G + kDecRows - 1) / kDecRows, heads = p.Hkv * vh;
+  const int b = item / heads, h = item - b * heads, hk = h / vh, row0 = (h - hk * vh) * kDecRows;
+  if (row0 + r >= G) return;
+  auto row = [&](int i) { return (int64_t)(i == 0 ? 2 * w + 1 : 2 * (w + i)) * kDecRows + r; };
+  __shared__ float red[256 / 64];
+  __shared__ f32x4 acc_s[256];
+  __shared__ float sum_s[256];
+  float top = kNoScore;
+  for (int i = tid; i < parts; i += 256) top = fmaxf(top, p.part_ml[row(i) * 2]);
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x, 64));
+  if ((tid & 63) == 0) red[tid >> 6] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  f32x4 acc{0.f, 0.f, 0.f, 0.f};
+  float sum = 0.f;
+  for (int i = g; i < parts; i += kGroups) {
+    const float f = __builtin_amdgcn_exp2f(p.part_ml[row(i) * 2] - top);
+    sum += f * p.part_ml[row(i) * 2 + 1];
+    acc += f * *(const f32x4*)(p.part_o + row(i) * D + d);
+  }
+  acc_s[tid] = acc;
+  sum_s[tid] = sum;
+  __syncthreads();
+  if (g) return;
+  for (int i = 1; i < kGroups; ++i) {
+    acc += acc_s[tid + i * kLanes];
+    sum += sum_s[tid + i * kLanes];
+  }
+  acc *= 1.f / sum;
+  const int64_t hq = (int64_t)hk * G + row0 + r;
+  *(u32x2*)((u16*)p.o.p + (int64_t)b * p.o.ts + hq * p.o.hs + d) =
+      u32x2{E::pack(acc[0], acc[1]), E::pack(acc[2], acc[3])};
+  if (p.lse && d == 0) p.lse[(int64_t)b * p.Hq + hq] = (top + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+// Workgroups of a decode: as many as the compute units hold at once.
+template <int D>
+int decode_shares() {
+  return device_cus() * (D == 256 ? 1 : 2);
+}
+
+template <class E, int D, bool CAP>
+hipError_t launch_decode_cap(const AttnParams& p, hipStream_t s) {
+  static std::atomic<bool> raised[kMaxDevices];
+  const int dev = current_device();
+  if (dev < 0 || dev >= kMaxDevices || !raised[dev].load(std::memory_order_acquire)) {
+    const hipError_t e = hipFuncSetAttribute((const void*)decode_kernel<E, D, CAP>,
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, kDecLds<D>);
+    if (e != hipSuccess) return e;
+    if (dev >= 0 && dev < kMaxDevices) raised[dev].store(true, std::memory_order_release);
+  }
+  const int shares = decode_shares<D>();
+  decode_kernel<E, D, CAP><<<dim3(shares), dim3(64 * kWaves), kDecLds<D>, s>>>(p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  decode_join_kernel<E, D><<<dim3(shares, std::min<int>(kDecRows, (int)p.group.d)), dim3(256), 0, s>>>(p);
+  return hipGetLastError();
+}
+
+template <class E, int D>
+hipError_t launch_dec(AttnParams p, void* workspace, hipStream_t s) {
+  const int shares = decode_shares<D>();
+  p.part_o = (float*)workspace;
+  p.part_ml = p.part_o + (int64_t)2 * shares * kDecRows * D;
+  p.parts = (int*)(p.part_ml + (int64_t)2 * shares * kDecRows * 2);
+  return p.cap > 0.f ? launch_decode_cap<E, D, true>(p, s) : launch_decode_cap<E, D, false>(p, s);
+}
+
+template <int D>
+size_t decode_bytes() {
+  return (size_t)decode_shares<D>() * (2 * kDecRows * (D + 2) * sizeof(float) + 2 * sizeof(int));
+}
+
 template <class E, int D, int NQ>
 hipError_t launch_chunk(const AttnParams& p, hipStream_t s) {
   constexpr int kRows = 32 * NQ * kWaves;
@@ -281,7 +719,12 @@ hipError_t launch_chunk(const AttnParams& p, hipStream_t s) {
 }
 
 template <class E>
-hipError_t launch_type(const AttnParams& p, int D, hipStream_t s) {
+hipError_t launch_type(const AttnParams& p, int D, void* workspace, hipStream_t s) {
+  if (!p.cu) {
+    if (D == 64) return launch_dec<E, 64>(p, workspace, s);
+    if (D == 128) return launch_dec<E, 128>(p, workspace, s);
+    return launch_dec<E, 256>(p, workspace, s);
+  }
   if (D == 64) return launch_chunk<E, 64, 2>(p, s);
   if (D == 128) return launch_chunk<E, 128, 2>(p, s);
   return launch_chunk<E, 256, 1>(p, s);
@@ -289,9 +732,13 @@ hipError_t launch_type(const AttnParams& p, int D, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_attention(const AttnParams& p, int D, int dtype, hipStream_t s) {
+hipError_t launch_attention(const AttnParams& p, int D, int dtype, void* workspace, hipStream_t s) {
   if (p.T == 0 || p.kv.B == 0) return hipSuccess;
-  return dtype == 0 ? launch_type<Bf>(p, D, s) : launch_type<Hf>(p, D, s);
+  return dtype == 0 ? launch_type<Bf>(p, D, workspace, s) : launch_type<Hf>(p, D, workspace, s);
+}
+
+size_t attention_bytes(int D) {
+  return D == 64 ? decode_bytes<64>() : D == 128 ? decode_bytes<128>() : decode_bytes<256>();
 }
 
 }  // namespace gdn

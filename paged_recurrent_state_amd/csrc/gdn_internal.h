@@ -231,8 +231,13 @@ struct AttnParams {
   int causal;
   float scale;    // of the raw scores, in log2 units (softcap: scale / softcap)
   float cap;      // softcap in log2 units, 0: none
+  // workspace: parts of the runs that are cut between workgroups
+  float* part_o;   // [2 * shares][rows][D]
+  float* part_ml;  // [2 * shares][rows][2]: reference and sum
+  int* parts;      // [shares][2]: the run a share leaves unfinished (-1: none), and its parts
 };
-hipError_t launch_attention(const AttnParams& p, int D, int dtype, hipStream_t s);
+hipError_t launch_attention(const AttnParams& p, int D, int dtype, void* workspace, hipStream_t s);
+size_t attention_bytes(int D);  // workspace of launch_attention
 
 // Errors of the C-ABI layer (gdn_api.hip): the thread's message and a status.
 int fail(int code, const char* fmt, ...);
