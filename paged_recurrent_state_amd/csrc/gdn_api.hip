@@ -799,8 +799,8 @@ int run_attention(const gdn_attention_dims_t* dims, const gdn_rows_t* q, const i
                   size_t workspace_bytes, hipStream_t stream) {
   if (T == 0 || cache->num_seqs == 0) return ok();
   const int32_t group = dims->num_q_heads / dims->num_kv_heads;
-  if (T * group >= (int64_t(1) << 31))
-    return fail(GDN_EINVAL, "query rows of a kv-head (%lld) must stay below 2^31", (long long)(T * group));
+  if (T * group >= (int64_t(1) << 31) - 4096)  // (32-bit row numbers, to the end of the last tile)
+    return fail(GDN_EINVAL, "query rows of a kv-head (%lld) must stay below 2^31 - 4096", (long long)(T * group));
   if (!aligned16(q, T, dims->num_q_heads, 2)) return fail(GDN_EINVAL, "rows of q must be 16-byte aligned");
   if (!aligned16(out, T, dims->num_q_heads, 2)) return fail(GDN_EINVAL, "rows of out must be 16-byte aligned");
   if (!aligned16(cache, dims->num_kv_heads, 2))
@@ -949,7 +949,7 @@ int gdn_kv_append_paged(const gdn_rope_t* rope, int32_t dtype, int32_t head_dim,
 
 size_t gdn_attention_workspace_size(const gdn_attention_dims_t* dims, int64_t total_tokens, int32_t num_seqs) {
   if (check_attention(dims) || total_tokens < 0 || num_seqs < 0) return 0;
-  return attention_bytes(dims->head_dim);
+  return attention_bytes(dims->head_dim, total_tokens, num_seqs, dims->num_q_heads / dims->num_kv_heads);
 }
 
 int gdn_attention_prefill_paged(const gdn_attention_dims_t* dims, const gdn_rows_t* q, const int32_t* cu_seqlens,

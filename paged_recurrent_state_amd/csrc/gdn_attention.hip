@@ -34,7 +34,6 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kKeys = 64;        // keys of a tile
 constexpr int kWaves = 4;
 constexpr float kNoScore = -3.0e38f;  // reference before the first score
 constexpr float kLog2e = 1.4426950408889634f;
@@ -82,218 +81,6 @@ __device__ __forceinline__ int v_at(int r, int c) {
   return r * (2 * D) + ((c ^ (D == 64 ? ((r >> 1) & 1) << 2 : (r & 3) << 2)) << 4);
 }
 
-template <class E, int D, int NQ, bool CAP>
-__global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
-  constexpr int kRows = 32 * NQ * kWaves;  // query rows of a tile
-  constexpr int kPieces = D / 8;           // 16-byte pieces of a row
-  constexpr int kSteps = D / 16;           // MFMA steps over D
-  constexpr int kBlocks = D / 32;          // 32-wide blocks of the output
-  __shared__ __attribute__((aligned(16))) char sk[kKeys * D * 2];
-  __shared__ __attribute__((aligned(16))) char sv[kKeys * D * 2];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5, col = lane & 31;
-  const int G = (int)p.group.d;
-  const int hk = blockIdx.y;
-
-  // which sequence and which of its tiles
-  int b = -1, tile = 0, tok0 = 0, n = 0;
-  {
-    int before = 0;
-    for (int b0 = 0; b0 < p.kv.B && b < 0; b0 += 64) {
-      const int i = b0 + lane;
-      int c0 = 0, c1 = 0;
-      if (i < p.kv.B) {
-        c0 = p.cu ? p.cu[i] : i;
-        c1 = p.cu ? p.cu[i + 1] : i + 1;
-      }
-      const int t = (int)(((int64_t)(c1 - c0) * G + kRows - 1) / kRows);
-      int incl = t;
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const int y = __shfl_up(incl, off, 64);
-        if (lane >= off) incl += y;
-      }
-      const uint64_t hit = __ballot(before + incl > (int)blockIdx.x);
-      if (hit) {
-        const int src = __ffsll((unsigned long long)hit) - 1;
-        b = b0 + src;
-        tile = (int)blockIdx.x - before - __shfl(incl - t, src, 64);
-        tok0 = __shfl(c0, src, 64);
-        n = __shfl(c1 - c0, src, 64);
-      }
-      before += __shfl(incl, 63, 64);
-    }
-    if (b < 0) return;
-  }
-  const int first_page = p.kv.ptr[b], pages = p.kv.ptr[b + 1] - first_page;
-  const int len = pages > 0 ? (pages - 1) * (int)p.kv.page.d + p.kv.lpl[b] : 0;
-  const int past = len - n;
-
-  // this lane's rows
-  int lim[NQ], low[NQ];  // keys low .. lim
-  u32x4 q[NQ][kSteps];
-#pragma unroll
-  for (int a = 0; a < NQ; ++a) {
-    const int row = tile * kRows + wave * 32 * NQ + a * 32 + col;
-    const int tok = (int)div_by(row, p.group), g = row - tok * G;
-    const bool real = tok < n;
-    lim[a] = real ? (p.causal ? min(past + tok, len - 1) : len - 1) : -1;
-    low[a] = real && p.window > 0 ? max(0, past + tok - p.window + 1) : 0;
-    const u16* src = (const u16*)p.q.p + (int64_t)(tok0 + (real ? tok : 0)) * p.q.ts +
-                     (int64_t)(hk * G + (real ? g : 0)) * p.q.hs + 8 * half;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) q[a][s] = *(const u32x4*)(src + 16 * s);
-  }
-  // the tile's keys
-  const int last_tok = min(n - 1, (int)div_by(tile * kRows + kRows - 1, p.group));
-  const int first_tok = (int)div_by(tile * kRows, p.group);
-  const int key_end = p.causal ? min(past + last_tok + 1, len) : len;
-  const int key_begin = p.window > 0 ? max(0, past + first_tok - p.window + 1) : 0;
-
-  f32x16 o[NQ][kBlocks];
-  float m[NQ], l[NQ];
-#pragma unroll
-  for (int a = 0; a < NQ; ++a) {
-    m[a] = kNoScore;
-    l[a] = 0.f;
-#pragma unroll
-    for (int d = 0; d < kBlocks; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[a][d][i] = 0.f;
-  }
-
-  const u32x4 zero{0u, 0u, 0u, 0u};
-  for (int key0 = key_begin & ~(kKeys - 1); key0 < key_end; key0 += kKeys) {
-    __syncthreads();
-    constexpr int kLoads = kKeys * kPieces / (64 * kWaves);
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int x = i * 64 * kWaves + threadIdx.x, r = x / kPieces, c = x % kPieces;
-      const int key = key0 + r;
-      u32x4 wk = zero, wv = zero;
-      if (key < len) {
-        const int pg = (int)div_by(key, p.kv.page);
-        const int64_t at = (int64_t)p.kv.idx[first_page + pg] * p.kv.ps +
-                           (int64_t)(key - pg * (int)p.kv.page.d) * p.kv.ts + hk * p.kv.hs + 8 * c;
-        wk = *(const u32x4*)((const u16*)p.kv.k + at);
-        wv = *(const u32x4*)((const u16*)p.kv.v + at);
-      }
-      *(u32x4*)(sk + k_at<D>(r, c)) = wk;
-      *(u32x4*)(sv + v_at<D>(r, c)) = wv;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kb = 0; kb < kKeys / 32; ++kb) {
-      f32x16 s[NQ];
-#pragma unroll
-      for (int a = 0; a < NQ; ++a)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[a][i] = 0.f;
-#pragma unroll
-      for (int t = 0; t < kSteps; ++t) {
-        const u32x4 kf = *(const u32x4*)(sk + k_at<D>(kb * 32 + col, 2 * t + half));
-#pragma unroll
-        for (int a = 0; a < NQ; ++a) s[a] = E::mfma(kf, q[a][t], s[a]);
-      }
-      u32x4 pt[NQ][2];
-#pragma unroll
-      for (int a = 0; a < NQ; ++a) {
-        // this lane's keys: base + 8 (i / 4) + i % 4
-        const int base = key0 + kb * 32 + 4 * half;
-        float x[16], top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int key = base + 8 * (i >> 2) + (i & 3);
-          x[i] = s[a][i] * p.scale;
-          if constexpr (CAP) x[i] = p.cap * tanhf(x[i]);
-          if (key > lim[a] || key < low[a]) x[i] = -INFINITY;
-          top = fmaxf(top, x[i]);
-        }
-        if (__any(top > m[a] + (E::kBias + E::kSlack))) {
-          top = fmaxf(top, other_half(top)) - E::kBias;
-          const float to = fmaxf(m[a], top), f = __builtin_amdgcn_exp2f(m[a] - to);
-          m[a] = to;
-          l[a] *= f;
-#pragma unroll
-          for (int d = 0; d < kBlocks; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[a][d][i] *= f;
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          x[i] = __builtin_amdgcn_exp2f(x[i] - m[a]);
-          l[a] += x[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) pt[a][i >> 2][i & 3] = E::pack(x[2 * i], x[2 * i + 1]);
-      }
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int d = 0; d < kBlocks; ++d) {
-          // keys 16 t + 4 half + 0..3 and 8 more; lane i of a 16-lane group points
-          // at 4 values of key i / 4 and receives value i of the four keys
-          const int key = kb * 32 + 16 * t + 4 * half + ((lane & 15) >> 2);
-          const int dim = 32 * d + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-          const int sub = (dim & 7) * 2;
-          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(sv + v_at<D>(key, dim >> 3) + sub));
-          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(sv + v_at<D>(key + 8, dim >> 3) + sub));
-          const u32x2 wl = __builtin_bit_cast(u32x2, lo), wh = __builtin_bit_cast(u32x2, hi);
-          const u32x4 vf{wl[0], wl[1], wh[0], wh[1]};
-#pragma unroll
-          for (int a = 0; a < NQ; ++a) o[a][d] = E::mfma(vf, pt[a][t], o[a][d]);
-        }
-    }
-  }
-
-#pragma unroll
-  for (int a = 0; a < NQ; ++a) {
-    const float sum = l[a] + other_half(l[a]);
-    const int row = tile * kRows + wave * 32 * NQ + a * 32 + col;
-    const int tok = (int)div_by(row, p.group), g = row - tok * G;
-    if (tok >= n) continue;
-    const float inv = lim[a] < low[a] ? 0.f : 1.f / sum;
-    const int64_t h = (int64_t)hk * G + g;
-    u16* dst = (u16*)p.o.p + (int64_t)(tok0 + tok) * p.o.ts + h * p.o.hs;
-#pragma unroll
-    for (int d = 0; d < kBlocks; ++d)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x16& x = o[a][d];
-        *(u32x2*)(dst + 32 * d + 8 * i + 4 * half) = u32x2{E::pack(x[4 * i] * inv, x[4 * i + 1] * inv),
-                                                           E::pack(x[4 * i + 2] * inv, x[4 * i + 3] * inv)};
-      }
-    if (p.lse && half == 0)
-      p.lse[(int64_t)(tok0 + tok) * p.Hq + h] =
-          lim[a] < low[a] ? -INFINITY : (m[a] + __builtin_amdgcn_logf(sum)) * kLn2;
-  }
-}
-
-// ------------------------------------------------------------------ decode
-//
-// One token per sequence: the G query rows of a kv-head against every key the
-// sequence holds.  Bound by reading the cache once, so the work is cut by bytes:
-// every (sequence, kv-head) is a run of 128-key tiles, the runs of the batch laid
-// end to end are cut into equal shares, one a workgroup, and a run that crosses
-// shares is joined afterwards from its parts' (m, l, o).
-//
-// The four waves of a workgroup take 32 of a tile's 128 keys each and never wait
-// for each other within a run: a wave loads its keys and values straight into
-// its own ring in LDS, and reads them once they have landed while the next are
-// on the way.  Products on 16x16x32 MFMAs in the same transposed form as above;
-// P enters as the sum of two 16-bit parts (the matrix units idle anyway), so
-// what it adds to the output's own rounding is invisible.
-
-constexpr int kDecKeys = 32;                     // keys of a wave's tile
-constexpr int kDecTile = kDecKeys * kWaves;      // keys of a workgroup's tile
-constexpr int kDecRows = 16;                     // query rows of a workgroup
-constexpr int kDecPages = 1024;                  // page ids staged at a time
-template <int D>
-constexpr int kDecStages = D == 64 ? 2 : 1;      // tiles of keys (and of values) in a wave's ring
-template <int D>
-constexpr int kDecLds = kWaves * kDecStages<D> * 2 * kDecKeys * D * 2;
-
-typedef __attribute__((address_space(3))) char* lds_ptr;
-
 __device__ __forceinline__ uint32_t lds_of(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
@@ -323,6 +110,563 @@ __device__ __forceinline__ void wait_vm() {
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 __device__ const u32x4 g_zero = {0u, 0u, 0u, 0u};  // read in place of keys outside a run
+
+// tanh by one exponential: 1 - 2 / (e^{2y} + 1), within 2^-22 of it.
+__device__ __forceinline__ float tanh_of(float y) {
+  const float e = __builtin_amdgcn_exp2f(y * (2.f * kLog2e));
+  return 1.f - 2.f * __builtin_amdgcn_rcpf(e + 1.f);
+}
+
+// Score in log2 units.
+template <bool CAP>
+__device__ __forceinline__ float score(const AttnParams& p, float x) {
+  x *= p.scale;
+  if constexpr (CAP) x = p.cap * tanh_of(x);
+  return x;
+}
+
+// ------------------------------------------------------------------ chunks
+//
+// The tiles of kRows query rows, each against its own run of key tiles, are
+// listed by plan_kernel with the running total of their key tiles.  The total
+// over all kv-heads is cut into equal shares, one a workgroup and one workgroup a
+// compute unit, so the chip is full and even whatever the batch: a run that
+// crosses shares is joined afterwards from its parts' (m, l, o).
+//
+// A workgroup is four waves, one a SIMD, with 32 NQ rows each; at NQ = 2 a K or V
+// fragment read from LDS feeds two products, which keeps the LDS reads at half
+// the matrix time.  Nothing else runs on the SIMD, so a wave overlaps its own
+// work: while the exponentials of tile i are computed, the matrix unit works on
+// the scores of tile i + 1, and then on tile i's product with V.  Tiles arrive by
+// global->LDS loads two tiles ahead, through a ring of kSlots tiles of K (one
+// ahead) and of V, with one barrier a tile.
+
+// Sizes of the chunk kernel.
+template <int D>
+struct Chunk {
+  static constexpr int kNQ = D == 256 ? 1 : 2;      // 32-row blocks of a wave
+  static constexpr int kRows = 32 * kNQ * kWaves;   // query rows of a tile
+  static constexpr int kKeys = D == 256 ? 32 : 64;  // keys of a tile
+  static constexpr int kSlotsK = 4, kSlotsV = 3;    // tiles of K and of V in LDS
+  static constexpr int kPages = 4096;               // page ids staged at a time
+  static constexpr int kSlot = kKeys * D * 2;       // bytes of a tile
+  static constexpr int kLds = (kSlotsK + kSlotsV) * kSlot + kPages * 4;
+};
+
+// A tile of query rows (plan_kernel): sequence, place in it, keys it sees.
+struct TileRec {
+  int b, tile, key_begin, key_end;
+};
+
+// One workgroup: lists every sequence's tiles, and the running total of their key
+// tiles (of one kv-head), [tiles + 1].
+__global__ __launch_bounds__(1024) void plan_kernel(AttnParams p, int rows, int keys) {
+  const int B = p.kv.B, G = (int)p.group.d;
+  // tiles before each sequence
+  const int per = (B + 1023) / 1024;
+  const int b0 = min(B, (int)threadIdx.x * per), b1 = min(B, b0 + per);
+  auto count = [&](int b) { return (int)(((int64_t)max(0, p.cu[b + 1] - p.cu[b]) * G + rows - 1) / rows); };
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) mine += count(b);
+  int total;
+  int at = block_exclusive_scan(mine, &total);
+  for (int b = b0; b < b1; ++b) {
+    p.seq_before[b] = at;
+    at += count(b);
+  }
+  if (threadIdx.x == 0) p.num_tiles[0] = total;
+  __syncthreads();
+  int64_t run = 0;
+  for (int i0 = 0; i0 < total; i0 += 1024) {
+    const int i = i0 + (int)threadIdx.x;
+    int x = 0;
+    if (i < total) {
+      int lo = 0, hi = B - 1;  // the last sequence with seq_before <= i has tile i
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.seq_before[mid] <= i)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      const int tokens = p.cu[lo + 1] - p.cu[lo], pages = p.kv.ptr[lo + 1] - p.kv.ptr[lo];
+      const int len = pages > 0 ? (pages - 1) * (int)p.kv.page.d + p.kv.lpl[lo] : 0;
+      const int past = len - tokens;
+      TileRec r;
+      r.b = lo;
+      r.tile = i - p.seq_before[lo];
+      const int first = (int)div_by((uint32_t)r.tile * rows, p.group);
+      const int last = min(tokens - 1, (int)div_by((uint32_t)r.tile * rows + rows - 1, p.group));
+      r.key_end = p.causal ? max(0, min(past + last + 1, len)) : len;
+      r.key_begin = p.window > 0 ? min(r.key_end, max(0, past + first - p.window + 1) / keys * keys) : 0;
+      ((TileRec*)p.tiles)[i] = r;
+      x = max(1, (r.key_end - r.key_begin + keys - 1) / keys);  // a tile without keys still writes its rows
+    }
+    int sum;
+    const int before = block_exclusive_scan(x, &sum);
+    if (i < total) p.before[i] = run + before;
+    run += sum;
+  }
+  if (threadIdx.x == 0) p.before[total] = run;
+}
+
+// The last tile whose running total is at most x (the whole wave searches).
+__device__ __forceinline__ int find_tile(const int64_t* before, int tiles, int64_t x) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = tiles - 1;  // among before[1 .. tiles - 1]
+  while (n > 0) {
+    const int step = (n + 63) >> 6;
+    const int64_t at = int64_t(lane + 1) * step;
+    const int c = __popcll(__ballot(at <= n && before[lo + (at <= n ? at : 1)] <= x));
+    lo += c * step;
+    n = step == 1 ? 0 : min(step - 1, n - c * step);
+  }
+  return lo;
+}
+
+template <class E, int D, bool CAP>
+__global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
+  typedef Chunk<D> C;
+  constexpr int NQ = C::kNQ, NSK = C::kSlotsK, NSV = C::kSlotsV, KB = C::kKeys / 32;
+  constexpr int kSteps = D / 16;   // MFMA steps over D
+  constexpr int kBlocks = D / 32;  // 32-wide blocks of the output
+  constexpr int kLoads = C::kSlot / 1024 / kWaves;  // load instructions of a wave for a tile of K or V
+  constexpr int kLoadRows = C::kKeys / kWaves;      // rows they cover
+  constexpr int kRowsPerLoad = 512 / D;
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  int* page_ids = (int*)(smem + (NSK + NSV) * C::kSlot);
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, col = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int G = (int)p.group.d;
+
+  const int num_tiles = p.num_tiles[0];
+  const int64_t per_head = p.before[num_tiles], units = per_head * p.Hkv;
+  const int64_t share = (units + gridDim.x - 1) / gridDim.x;
+  // neighbouring shares on one XCD (workgroup x runs on XCD x % 8)
+  const int shares8 = gridDim.x >> 3;
+  const int me = (gridDim.x & 7) ? blockIdx.x : (blockIdx.x & 7) * shares8 + (blockIdx.x >> 3);
+  const int64_t first = (int64_t)me * share, end = min(units, first + share);
+  int* tail = p.parts + 2 * me;
+  if (first >= end) {
+    if (tid == 0) tail[0] = -1;
+    return;
+  }
+  int hk = (int)(first / per_head);
+  int ti = find_tile(p.before, num_tiles, first - hk * per_head);
+  int done = (int)(first - hk * per_head - p.before[ti]);  // key tiles of it already taken by the share before
+  bool left = false;
+
+  for (int64_t u = first; u < end;) {
+    const TileRec rec = ((const TileRec*)p.tiles)[ti];
+    const int tiles = (int)(p.before[ti + 1] - p.before[ti]);
+    const int todo = (int)min((int64_t)(tiles - done), end - u);
+    const int tok0 = p.cu[rec.b], n = p.cu[rec.b + 1] - tok0;
+    const int first_page = p.kv.ptr[rec.b], pages = p.kv.ptr[rec.b + 1] - first_page;
+    const int len = pages > 0 ? (pages - 1) * (int)p.kv.page.d + p.kv.lpl[rec.b] : 0;
+    const int past = len - n;
+
+    // this lane's rows
+    int lim[NQ], low[NQ];  // keys low .. lim
+    u32x4 q[NQ][kSteps];
+#pragma unroll
+    for (int a = 0; a < NQ; ++a) {
+      const int row = rec.tile * C::kRows + wave * 32 * NQ + a * 32 + col;
+      const int tok = (int)div_by(row, p.group), g = row - tok * G;
+      const bool real = tok < n;
+      lim[a] = real ? (p.causal ? min(past + tok, len - 1) : len - 1) : -1;
+      low[a] = real && p.window > 0 ? max(0, past + tok - p.window + 1) : 0;
+      const u16* src = (const u16*)p.q.p + (int64_t)(tok0 + (real ? tok : 0)) * p.q.ts +
+                       (int64_t)(hk * G + (real ? g : 0)) * p.q.hs + 8 * half;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) q[a][s] = *(const u32x4*)(src + 16 * s);
+    }
+    // keys all_low .. all_lim are seen by every row of the wave and need no mask
+    int all_lim = 0x7fffffff, all_low = 0;
+#pragma unroll
+    for (int a = 0; a < NQ; ++a) {
+      const int row = rec.tile * C::kRows + wave * 32 * NQ + a * 32 + col;
+      if ((int)div_by(row, p.group) < n) all_lim = min(all_lim, lim[a]);
+      all_low = max(all_low, low[a]);
+    }
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) {
+      all_lim = min(all_lim, __shfl_xor(all_lim, x, 64));
+      all_low = max(all_low, __shfl_xor(all_low, x, 64));
+    }
+    all_lim = __builtin_amdgcn_readfirstlane(all_lim);
+    all_low = __builtin_amdgcn_readfirstlane(all_low);
+
+    f32x16 o[NQ][kBlocks];
+    float m[NQ], l[NQ];
+#pragma unroll
+    for (int a = 0; a < NQ; ++a) {
+      m[a] = kNoScore;
+      l[a] = 0.f;
+#pragma unroll
+      for (int d = 0; d < kBlocks; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[a][d][i] = 0.f;
+    }
+
+    const int key_a = rec.key_begin + done * C::kKeys;
+    const int key_b = min(rec.key_end, key_a + todo * C::kKeys);
+    const char* kbase = p.kv.k + 2 * (int64_t)hk * p.kv.hs;
+    const int64_t vdiff = p.kv.v - p.kv.k;
+
+    // as many tiles at a time as the staged page ids reach
+    for (int a0 = key_a; a0 < key_b;) {
+      const int page0 = (int)div_by(a0, p.kv.page);
+      const int64_t reach = (int64_t)(page0 + C::kPages) * p.kv.page.d;  // first key past the staged pages
+      // (whole tiles; kPages pages are more than a tile's keys)
+      const int a1 = reach >= key_b ? key_b : (int)reach / C::kKeys * C::kKeys;
+      const int count = (a1 - a0 + C::kKeys - 1) / C::kKeys;
+      __syncthreads();
+      {
+        const int last = (int)div_by(a1 - 1, p.kv.page);
+        for (int i = tid; i <= last - page0; i += 64 * kWaves) page_ids[i] = p.kv.idx[first_page + page0 + i];
+      }
+      __syncthreads();
+
+      // this wave's rows of tile i (of keys, or V: of values) into its slot
+      auto load = [&](int i, bool V) __attribute__((always_inline)) {
+        const uint32_t dst = lds_of(smem) + (V ? NSK + i % NSV : i % NSK) * C::kSlot + wave * (kLoads * 1024);
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x) {
+          const int r = wave * kLoadRows + x * kRowsPerLoad + lane / (D / 8), slot = lane % (D / 8);
+          // the piece that belongs at this lane's place: the turning is its own inverse
+          const int c = V ? (slot ^ (D == 64 ? ((r >> 1) & 1) << 2 : (r & 3) << 2))
+                          : (slot ^ (D == 64 ? (r >> 1) & 7 : r & 15));
+          const int key = a0 + i * C::kKeys + r;
+          const char* src = (const char*)&g_zero;
+          if (key < a1) {
+            const int pg = (int)div_by(key, p.kv.page);
+            src = kbase + 2 * ((int64_t)page_ids[pg - page0] * p.kv.ps + (int64_t)(key - pg * (int)p.kv.page.d) * p.kv.ts +
+                               8 * c) + (V ? vdiff : 0);
+          }
+          dma16<false>(dst + x * 1024, src);
+        }
+      };
+      // tile i's values and tile i + 1's keys are in LDS, and every wave is done with tile i - 1
+      auto arrive = [&]() __attribute__((always_inline)) {
+        wait_vm<2 * kLoads>();
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      };
+
+      f32x16 s[NQ];
+      // scores of block kb (32 keys) of tile i
+      auto scores = [&](int i, int kb) __attribute__((always_inline)) {
+        const char* sk = smem + (i % NSK) * C::kSlot;
+#pragma unroll
+        for (int a = 0; a < NQ; ++a)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[a][e] = 0.f;
+#pragma unroll
+        for (int t = 0; t < kSteps; ++t) {
+          const u32x4 kf = *(const u32x4*)(sk + k_at<D>(kb * 32 + col, 2 * t + half));
+#pragma unroll
+          for (int a = 0; a < NQ; ++a) s[a] = E::mfma(kf, q[a][t], s[a]);
+        }
+      };
+      // their masks, and the running reference
+      auto settle = [&](int i, int kb) __attribute__((always_inline)) {
+        const int key0 = a0 + i * C::kKeys + kb * 32;
+        if constexpr (CAP) {
+#pragma unroll
+          for (int a = 0; a < NQ; ++a)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[a][e] = score<true>(p, s[a][e]);
+        }
+        if (key0 + 31 > min(all_lim, a1 - 1) || key0 < all_low) {
+#pragma unroll
+          for (int a = 0; a < NQ; ++a) {
+            // this lane's keys: 4 half + 8 (e / 4) + e % 4
+            const int hi = min(lim[a], a1 - 1) - key0 - 4 * half, lo = low[a] - key0 - 4 * half;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int key = 8 * (e >> 2) + (e & 3);
+              if (key > hi || key < lo) s[a][e] = -INFINITY;
+              if (e % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // (the comparisons' masks would fill the scalar registers)
+            }
+          }
+        }
+        const float scale = CAP ? 1.f : p.scale;
+        float top[NQ];
+        bool move = false;
+#pragma unroll
+        for (int a = 0; a < NQ; ++a) {
+          top[a] = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) top[a] = fmaxf(top[a], fmaxf(s[a][e], s[a][e + 1]));
+          top[a] *= scale;
+          move = move || top[a] > m[a] + (E::kBias + E::kSlack);
+        }
+        if (__any(move)) {
+#pragma unroll
+          for (int a = 0; a < NQ; ++a) {
+            const float up = fmaxf(top[a], other_half(top[a])) - E::kBias;
+            const float to = fmaxf(m[a], up), f = __builtin_amdgcn_exp2f(m[a] - to);
+            m[a] = to;
+            l[a] *= f;
+#pragma unroll
+            for (int d = 0; d < kBlocks; ++d)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[a][d][e] *= f;
+          }
+        }
+      };
+      u32x4 pt[NQ][2];
+      auto weights = [&](const f32x16 (&x)[NQ]) __attribute__((always_inline)) {
+        const float scale = CAP ? 1.f : p.scale;
+#pragma unroll
+        for (int a = 0; a < NQ; ++a)
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[a][e], scale, -m[a]));
+            const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[a][e + 1], scale, -m[a]));
+            l[a] += w0;
+            l[a] += w1;
+            pt[a][e >> 3][(e >> 1) & 3] = E::pack(w0, w1);
+          }
+      };
+      auto product = [&](int i, int kb) __attribute__((always_inline)) {
+        const char* sv = smem + (NSK + i % NSV) * C::kSlot;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int d = 0; d < kBlocks; ++d) {
+            // keys 16 t + 4 half + 0..3 and 8 more; lane i of a 16-lane group points at 4 values
+            // of key i / 4 and receives value i of the four keys
+            const int key = kb * 32 + 16 * t + 4 * half + ((lane & 15) >> 2);
+            const int dim = 32 * d + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+            const int sub = (dim & 7) * 2;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(sv + v_at<D>(key, dim >> 3) + sub));
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(sv + v_at<D>(key + 8, dim >> 3) + sub));
+            const u32x2 wl = __builtin_bit_cast(u32x2, lo), wh = __builtin_bit_cast(u32x2, hi);
+            const u32x4 vf{wl[0], wl[1], wh[0], wh[1]};
+#pragma unroll
+            for (int a = 0; a < NQ; ++a) o[a][d] = E::mfma(vf, pt[a][t], o[a][d]);
+          }
+      };
+      // one block: its weights and product, and the next block's scores beside them
+      auto block = [&](int i, int kb) __attribute__((always_inline)) {
+        f32x16 x[NQ];
+#pragma unroll
+        for (int a = 0; a < NQ; ++a) x[a] = s[a];
+        const int ni = kb + 1 < KB ? i : i + 1, nkb = kb + 1 < KB ? kb + 1 : 0;
+        scores(ni, nkb);
+        weights(x);
+        product(i, kb);
+        settle(ni, nkb);
+      };
+
+      load(0, false);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        load(x, true);
+        load(x + 1, false);
+      }
+      wait_vm<4 * kLoads>();
+      asm volatile("s_barrier" ::: "memory");
+      scores(0, 0);
+      settle(0, 0);
+      // (the last block's "next" is a block of zeros, masked)
+      for (int i = 0; i < count; ++i) {
+        arrive();
+        load(i + 2, true);
+        load(i + 3, false);
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) block(i, kb);
+      }
+      wait_vm<0>();
+      a0 = a1;
+    }
+
+    const bool whole = done == 0 && todo == tiles;
+    const bool head = done > 0;  // a part that continues a run: slot 0, one that starts it: slot 1
+    const int64_t part = (2 * (int64_t)me + (head ? 0 : 1)) * p.part_rows;
+#pragma unroll
+    for (int a = 0; a < NQ; ++a) {
+      const float sum = l[a] + other_half(l[a]);
+      const int in_tile = wave * 32 * NQ + a * 32 + col;
+      const int row = rec.tile * C::kRows + in_tile;
+      const int tok = (int)div_by(row, p.group), g = row - tok * G;
+      if (tok >= n) continue;
+      if (whole) {
+        const bool none = lim[a] < low[a];
+        const float inv = none ? 0.f : 1.f / sum;
+        const int64_t h = (int64_t)hk * G + g;
+        u16* dst = (u16*)p.o.p + (int64_t)(tok0 + tok) * p.o.ts + h * p.o.hs;
+#pragma unroll
+        for (int d = 0; d < kBlocks; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f32x16& x = o[a][d];
+            *(u32x2*)(dst + 32 * d + 8 * i + 4 * half) = u32x2{E::pack(x[4 * i] * inv, x[4 * i + 1] * inv),
+                                                               E::pack(x[4 * i + 2] * inv, x[4 * i + 3] * inv)};
+          }
+        if (p.lse && half == 0)
+          p.lse[(int64_t)(tok0 + tok) * p.Hq + h] = none ? -INFINITY : (m[a] + __builtin_amdgcn_logf(sum)) * kLn2;
+      } else {
+        float* dst = p.part_o + (part + in_tile) * D;
+#pragma unroll
+        for (int d = 0; d < kBlocks; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f32x16& x = o[a][d];
+            *(f32x4*)(dst + 32 * d + 8 * i + 4 * half) = f32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
+          }
+        if (half == 0) {
+          p.part_ml[(part + in_tile) * 2] = m[a];
+          p.part_ml[(part + in_tile) * 2 + 1] = sum;
+        }
+      }
+    }
+    if (!whole && !head) {
+      left = true;
+      if (tid == 0) {
+        tail[0] = hk * num_tiles + ti;
+        tail[1] = (int)((u + (tiles - done) - 1) / share) - me + 1;
+      }
+    }
+    u += todo;
+    done += todo;
+    if (done == tiles) {
+      done = 0;
+      if (++ti == num_tiles) {
+        ti = 0;
+        ++hk;
+      }
+    }
+  }
+  if (!left && tid == 0) tail[0] = -1;
+}
+
+// Joins the parts of the tiles that cross shares: workgroup (w, y) takes kGroups
+// rows of the tile that share w leaves unfinished; its parts are slot 1 of w and
+// slot 0 of the shares after it.
+template <class E, int D>
+__global__ __launch_bounds__(256) void chunk_join_kernel(AttnParams p) {
+  constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
+  const int w = blockIdx.x, d = 4 * (threadIdx.x % kLanes), in_tile = blockIdx.y * kGroups + threadIdx.x / kLanes;
+  const int item = p.parts[2 * w], parts = p.parts[2 * w + 1];
+  if (item < 0) return;
+  const int num_tiles = p.num_tiles[0], hk = item / num_tiles;
+  const TileRec rec = ((const TileRec*)p.tiles)[item - hk * num_tiles];
+  const int tok0 = p.cu[rec.b], n = p.cu[rec.b + 1] - tok0, row = rec.tile * Chunk<D>::kRows + in_tile;
+  const int tok = (int)div_by(row, p.group), g = row - tok * (int)p.group.d;
+  if (tok >= n) return;
+  auto at = [&](int i) { return (int64_t)(i == 0 ? 2 * w + 1 : 2 * (w + i)) * p.part_rows + in_tile; };
+  float top = kNoScore;
+  for (int i = 0; i < parts; ++i) top = fmaxf(top, p.part_ml[at(i) * 2]);
+  f32x4 acc{0.f, 0.f, 0.f, 0.f};
+  float sum = 0.f;
+  for (int i = 0; i < parts; ++i) {
+    const float f = __builtin_amdgcn_exp2f(p.part_ml[at(i) * 2] - top);
+    sum += f * p.part_ml[at(i) * 2 + 1];
+    acc += f * *(const f32x4*)(p.part_o + at(i) * D + d);
+  }
+  // a row that saw nothing in any part
+  const bool none = sum == 0.f;
+  acc *= none ? 0.f : 1.f / sum;
+  const int64_t h = (int64_t)hk * p.group.d + g;
+  *(u32x2*)((u16*)p.o.p + (int64_t)(tok0 + tok) * p.o.ts + h * p.o.hs + d) =
+      u32x2{E::pack(acc[0], acc[1]), E::pack(acc[2], acc[3])};
+  if (p.lse && d == 0)
+    p.lse[(int64_t)(tok0 + tok) * p.Hq + h] = none ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+size_t align16(size_t x) { return (x + 15) & ~size_t(15); }
+
+// Workspace of a chunk call: the plan, and two parts a share.
+struct ChunkWs {
+  int64_t tiles, part_rows;
+  size_t recs, before, seqs, count, parts, ml, o, total;
+};
+template <int D>
+ChunkWs chunk_ws(int64_t T, int64_t B, int64_t G) {
+  ChunkWs w;
+  const int64_t shares = device_cus();
+  w.tiles = T * G / Chunk<D>::kRows + B;  // sum over the sequences of ceil(n G / kRows)
+  w.part_rows = std::min<int64_t>(Chunk<D>::kRows, T * G);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t x = at;
+    at += align16(bytes);
+    return x;
+  };
+  w.recs = take((w.tiles + 1) * sizeof(TileRec));
+  w.before = take((w.tiles + 1) * sizeof(int64_t));
+  w.seqs = take(B * sizeof(int));
+  w.count = take(sizeof(int));
+  w.parts = take(shares * 2 * sizeof(int));
+  w.ml = take(2 * shares * w.part_rows * 2 * sizeof(float));
+  w.o = take(2 * shares * w.part_rows * D * sizeof(float));
+  w.total = at;
+  return w;
+}
+
+template <class Kernel>
+hipError_t allow_lds(Kernel* k, int bytes, std::atomic<bool> (&raised)[kMaxDevices]) {
+  const int dev = current_device();
+  if (dev >= 0 && dev < kMaxDevices && raised[dev].load(std::memory_order_acquire)) return hipSuccess;
+  const hipError_t e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess && dev >= 0 && dev < kMaxDevices) raised[dev].store(true, std::memory_order_release);
+  return e;
+}
+
+template <class E, int D, bool CAP>
+hipError_t launch_chunk_cap(const AttnParams& p, hipStream_t s) {
+  static std::atomic<bool> raised[kMaxDevices];
+  hipError_t e = allow_lds(chunk_kernel<E, D, CAP>, Chunk<D>::kLds, raised);
+  if (e != hipSuccess) return e;
+  const int shares = device_cus();
+  plan_kernel<<<dim3(1), dim3(1024), 0, s>>>(p, Chunk<D>::kRows, Chunk<D>::kKeys);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  chunk_kernel<E, D, CAP><<<dim3(shares), dim3(64 * kWaves), Chunk<D>::kLds, s>>>(p);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  const int groups = 256 / (D / 4);
+  chunk_join_kernel<E, D><<<dim3(shares, (p.part_rows + groups - 1) / groups), dim3(256), 0, s>>>(p);
+  return hipGetLastError();
+}
+
+template <class E, int D>
+hipError_t launch_chunk(AttnParams p, void* workspace, hipStream_t s) {
+  const ChunkWs w = chunk_ws<D>(p.T, p.kv.B, p.group.d);
+  char* base = (char*)workspace;
+  p.tiles = base + w.recs;
+  p.before = (int64_t*)(base + w.before);
+  p.seq_before = (int*)(base + w.seqs);
+  p.num_tiles = (int*)(base + w.count);
+  p.parts = (int*)(base + w.parts);
+  p.part_ml = (float*)(base + w.ml);
+  p.part_o = (float*)(base + w.o);
+  p.part_rows = (int)w.part_rows;
+  return p.cap > 0.f ? launch_chunk_cap<E, D, true>(p, s) : launch_chunk_cap<E, D, false>(p, s);
+}
+
+// ------------------------------------------------------------------ decode
+//
+// One token per sequence: the G query rows of a kv-head against every key the
+// sequence holds.  Bound by reading the cache once, so the work is cut by bytes:
+// every (sequence, kv-head) is a run of 128-key tiles, the runs of the batch laid
+// end to end are cut into equal shares, one a workgroup, and a run that crosses
+// shares is joined afterwards from its parts' (m, l, o).
+//
+// The four waves of a workgroup take 32 of a tile's 128 keys each and never wait
+// for each other within a run: a wave loads its keys and values straight into
+// its own ring in LDS, and reads them once they have landed while the next are
+// on the way.  Products on 16x16x32 MFMAs in the same transposed form as above;
+// P enters as the sum of two 16-bit parts (the matrix units idle anyway), so
+// what it adds to the output's own rounding is invisible.
+
+constexpr int kDecKeys = 32;                     // keys of a wave's tile
+constexpr int kDecTile = kDecKeys * kWaves;      // keys of a workgroup's tile
+constexpr int kDecRows = 16;                     // query rows of a workgroup
+constexpr int kDecPages = 1024;                  // page ids staged at a time
+template <int D>
+constexpr int kDecStages = D == 64 ? 2 : 1;      // tiles of keys (and of values) in a wave's ring
+template <int D>
+constexpr int kDecLds = kWaves * kDecStages<D> * 2 * kDecKeys * D * 2;
 
 template <class E>
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c);
@@ -367,14 +711,6 @@ __device__ __forceinline__ Span dec_span(const AttnParams& p, int b) {
 // its 128-key tiles, counted from the one that holds `begin`
 __device__ __forceinline__ int dec_tiles(const Span& s) {
   return s.len <= s.begin ? 0 : (s.len + kDecTile - 1) / kDecTile - s.begin / kDecTile;
-}
-
-// Score in log2 units.
-template <bool CAP>
-__device__ __forceinline__ float score(const AttnParams& p, float x) {
-  x *= p.scale;
-  if constexpr (CAP) x = p.cap * tanhf(x);
-  return x;
 }
 
 template <class E, int D, bool CAP>
@@ -677,17 +1013,11 @@ int decode_shares() {
 template <class E, int D, bool CAP>
 hipError_t launch_decode_cap(const AttnParams& p, hipStream_t s) {
   static std::atomic<bool> raised[kMaxDevices];
-  const int dev = current_device();
-  if (dev < 0 || dev >= kMaxDevices || !raised[dev].load(std::memory_order_acquire)) {
-    const hipError_t e = hipFuncSetAttribute((const void*)decode_kernel<E, D, CAP>,
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, kDecLds<D>);
-    if (e != hipSuccess) return e;
-    if (dev >= 0 && dev < kMaxDevices) raised[dev].store(true, std::memory_order_release);
-  }
+  hipError_t e = allow_lds(decode_kernel<E, D, CAP>, kDecLds<D>, raised);
+  if (e != hipSuccess) return e;
   const int shares = decode_shares<D>();
   decode_kernel<E, D, CAP><<<dim3(shares), dim3(64 * kWaves), kDecLds<D>, s>>>(p);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if ((e = hipGetLastError()) != hipSuccess) return e;
   decode_join_kernel<E, D><<<dim3(shares, std::min<int>(kDecRows, (int)p.group.d)), dim3(256), 0, s>>>(p);
   return hipGetLastError();
 }
@@ -706,18 +1036,6 @@ size_t decode_bytes() {
   return (size_t)decode_shares<D>() * (2 * kDecRows * (D + 2) * sizeof(float) + 2 * sizeof(int));
 }
 
-template <class E, int D, int NQ>
-hipError_t launch_chunk(const AttnParams& p, hipStream_t s) {
-  constexpr int kRows = 32 * NQ * kWaves;
-  const int64_t tiles = p.cu ? p.T * (int64_t)p.group.d / kRows + p.kv.B : p.kv.B * (int64_t)((p.group.d + kRows - 1) / kRows);
-  const dim3 grid((uint32_t)tiles, (uint32_t)p.Hkv), blk(64 * kWaves);
-  if (p.cap > 0.f)
-    chunk_kernel<E, D, NQ, true><<<grid, blk, 0, s>>>(p);
-  else
-    chunk_kernel<E, D, NQ, false><<<grid, blk, 0, s>>>(p);
-  return hipGetLastError();
-}
-
 template <class E>
 hipError_t launch_type(const AttnParams& p, int D, void* workspace, hipStream_t s) {
   if (!p.cu) {
@@ -725,9 +1043,9 @@ hipError_t launch_type(const AttnParams& p, int D, void* workspace, hipStream_t 
     if (D == 128) return launch_dec<E, 128>(p, workspace, s);
     return launch_dec<E, 256>(p, workspace, s);
   }
-  if (D == 64) return launch_chunk<E, 64, 2>(p, s);
-  if (D == 128) return launch_chunk<E, 128, 2>(p, s);
-  return launch_chunk<E, 256, 1>(p, s);
+  if (D == 64) return launch_chunk<E, 64>(p, workspace, s);
+  if (D == 128) return launch_chunk<E, 128>(p, workspace, s);
+  return launch_chunk<E, 256>(p, workspace, s);
 }
 
 }  // namespace
@@ -737,8 +1055,10 @@ hipError_t launch_attention(const AttnParams& p, int D, int dtype, void* workspa
   return dtype == 0 ? launch_type<Bf>(p, D, workspace, s) : launch_type<Hf>(p, D, workspace, s);
 }
 
-size_t attention_bytes(int D) {
-  return D == 64 ? decode_bytes<64>() : D == 128 ? decode_bytes<128>() : decode_bytes<256>();
+size_t attention_bytes(int D, int64_t T, int64_t B, int64_t G) {
+  if (D == 64) return std::max(decode_bytes<64>(), chunk_ws<64>(T, B, G).total);
+  if (D == 128) return std::max(decode_bytes<128>(), chunk_ws<128>(T, B, G).total);
+  return std::max(decode_bytes<256>(), chunk_ws<256>(T, B, G).total);
 }
 
 }  // namespace gdn

@@ -235,9 +235,15 @@ struct AttnParams {
   float* part_o;   // [2 * shares][rows][D]
   float* part_ml;  // [2 * shares][rows][2]: reference and sum
   int* parts;      // [shares][2]: the run a share leaves unfinished (-1: none), and its parts
+  int part_rows;   // chunks: rows of a part
+  // chunks: the list of query tiles (plan_kernel)
+  void* tiles;
+  int64_t* before;  // [tiles + 1]: key tiles of the tiles before
+  int* seq_before;  // [B]: tiles before each sequence's
+  int* num_tiles;
 };
 hipError_t launch_attention(const AttnParams& p, int D, int dtype, void* workspace, hipStream_t s);
-size_t attention_bytes(int D);  // workspace of launch_attention
+size_t attention_bytes(int D, int64_t T, int64_t B, int64_t group);  // workspace of launch_attention
 
 // Errors of the C-ABI layer (gdn_api.hip): the thread's message and a status.
 int fail(int code, const char* fmt, ...);
