@@ -101,7 +101,18 @@ __device__ __forceinline__ void dma16(uint32_t lds, const void* src) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src)
                  : "memory", "m0");
 }
+// The same from a wave-uniform address and a 32-bit byte offset of each lane.
+__device__ __forceinline__ void dma16_at(uint32_t lds, const void* base, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
+}
 #pragma clang diagnostic pop
+
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
 
 template <int N>
 __device__ __forceinline__ void wait_vm() {
@@ -256,6 +267,18 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
   int done = (int)(first - hk * per_head - p.before[ti]);  // key tiles of it already taken by the share before
   bool left = false;
 
+  // What each lane loads of a row: the piece that belongs at its place in LDS (k_at, v_at: the
+  // turning is its own inverse), and where that is from the first row of the wave's part of a tile
+  uint32_t piece_k[kLoads], piece_v[kLoads], off_k[kLoads], off_v[kLoads];
+#pragma unroll
+  for (int x = 0; x < kLoads; ++x) {
+    const int r = x * kRowsPerLoad + lane / (D / 8), tr = wave * kLoadRows + r, slot = lane % (D / 8);
+    piece_k[x] = 16 * (slot ^ (D == 64 ? (tr >> 1) & 7 : tr & 15));
+    piece_v[x] = 16 * (slot ^ (D == 64 ? ((tr >> 1) & 1) << 2 : (tr & 3) << 2));
+    off_k[x] = (uint32_t)(2 * r * p.kv.ts) + piece_k[x];
+    off_v[x] = (uint32_t)(2 * r * p.kv.ts) + piece_v[x];
+  }
+
   for (int64_t u = first; u < end;) {
     const TileRec rec = ((const TileRec*)p.tiles)[ti];
     const int tiles = (int)(p.before[ti + 1] - p.before[ti]);
@@ -311,7 +334,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
     const int key_a = rec.key_begin + done * C::kKeys;
     const int key_b = min(rec.key_end, key_a + todo * C::kKeys);
     const char* kbase = p.kv.k + 2 * (int64_t)hk * p.kv.hs;
-    const int64_t vdiff = p.kv.v - p.kv.k;
+    const char* vbase = p.kv.v + 2 * (int64_t)hk * p.kv.hs;
 
     // as many tiles at a time as the staged page ids reach
     for (int a0 = key_a; a0 < key_b;) {
@@ -327,23 +350,46 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
       }
       __syncthreads();
 
-      // this wave's rows of tile i (of keys, or V: of values) into its slot
+      // Where this wave's rows of a tile lie in the caches, in bytes from the start of its kv-head:
+      // one place for all of them when they lie in one page and are all there, otherwise each
+      // lane's own (-1: past the end, zeros).  A tile's keys and, an iteration later, its values
+      // go by the same places.
+      bool one;
+      int64_t at;
+      int64_t lane_at[kLoads];
+      auto page_of = [&](int i) __attribute__((always_inline)) {
+        const int key = min(a0 + i * C::kKeys + wave * kLoadRows, a1 - 1);
+        return page_ids[(int)div_by(key, p.kv.page) - page0];
+      };
+      auto place = [&](int i, int id) __attribute__((always_inline)) {
+        const int key0 = a0 + i * C::kKeys + wave * kLoadRows;
+        one = p.even_pages && key0 + kLoadRows <= a1;
+        if (one) {
+          const int off = key0 - (int)div_by(key0, p.kv.page) * (int)p.kv.page.d;
+          at = 2 * ((int64_t)__builtin_amdgcn_readfirstlane(id) * p.kv.ps + (int64_t)off * p.kv.ts);
+        } else {
+#pragma unroll
+          for (int x = 0; x < kLoads; ++x) {
+            const int key = key0 + x * kRowsPerLoad + lane / (D / 8), k = min(key, a1 - 1);
+            const int pg = (int)div_by(k, p.kv.page);
+            const int64_t to = 2 * ((int64_t)page_ids[pg - page0] * p.kv.ps + (int64_t)(k - pg * (int)p.kv.page.d) * p.kv.ts);
+            lane_at[x] = key < a1 ? to : -1;
+          }
+        }
+      };
+      // the placed tile's keys (or V: values) into the slot of tile i
       auto load = [&](int i, bool V) __attribute__((always_inline)) {
         const uint32_t dst = lds_of(smem) + (V ? NSK + i % NSV : i % NSK) * C::kSlot + wave * (kLoads * 1024);
+        if (one) {
+          const char* base = (V ? vbase : kbase) + at;
 #pragma unroll
-        for (int x = 0; x < kLoads; ++x) {
-          const int r = wave * kLoadRows + x * kRowsPerLoad + lane / (D / 8), slot = lane % (D / 8);
-          // the piece that belongs at this lane's place: the turning is its own inverse
-          const int c = V ? (slot ^ (D == 64 ? ((r >> 1) & 1) << 2 : (r & 3) << 2))
-                          : (slot ^ (D == 64 ? (r >> 1) & 7 : r & 15));
-          const int key = a0 + i * C::kKeys + r;
-          const char* src = (const char*)&g_zero;
-          if (key < a1) {
-            const int pg = (int)div_by(key, p.kv.page);
-            src = kbase + 2 * ((int64_t)page_ids[pg - page0] * p.kv.ps + (int64_t)(key - pg * (int)p.kv.page.d) * p.kv.ts +
-                               8 * c) + (V ? vdiff : 0);
+          for (int x = 0; x < kLoads; ++x) dma16_at(dst + x * 1024, base, V ? off_v[x] : off_k[x]);
+        } else {
+#pragma unroll
+          for (int x = 0; x < kLoads; ++x) {
+            const char* src = (V ? vbase : kbase) + lane_at[x] + (V ? piece_v[x] : piece_k[x]);
+            dma16<false>(dst + x * 1024, lane_at[x] < 0 ? (const char*)&g_zero : src);
           }
-          dma16<false>(dst + x * 1024, src);
         }
       };
       // tile i's values and tile i + 1's keys are in LDS, and every wave is done with tile i - 1
@@ -459,12 +505,15 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
         settle(ni, nkb);
       };
 
+      place(0, page_of(0));
       load(0, false);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         load(x, true);
+        place(x + 1, page_of(x + 1));
         load(x + 1, false);
       }
+      int id = page_of(3);
       wait_vm<4 * kLoads>();
       asm volatile("s_barrier" ::: "memory");
       scores(0, 0);
@@ -473,7 +522,9 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
       for (int i = 0; i < count; ++i) {
         arrive();
         load(i + 2, true);
+        place(i + 3, id);
         load(i + 3, false);
+        id = page_of(i + 4);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) block(i, kb);
       }
@@ -641,6 +692,9 @@ hipError_t launch_chunk(AttnParams p, void* workspace, hipStream_t s) {
   p.part_ml = (float*)(base + w.ml);
   p.part_o = (float*)(base + w.o);
   p.part_rows = (int)w.part_rows;
+  // a wave's rows of a tile start at a multiple of 16 (or 8) keys; their offsets from the first
+  // must fit 32 bits
+  p.even_pages = p.kv.page.d % 16 == 0 && p.kv.ts >= 0 && p.kv.ts < (int64_t(1) << 26);
   return p.cap > 0.f ? launch_chunk_cap<E, D, true>(p, s) : launch_chunk_cap<E, D, false>(p, s);
 }
 

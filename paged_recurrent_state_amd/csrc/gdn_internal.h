@@ -236,6 +236,7 @@ struct AttnParams {
   float* part_ml;  // [2 * shares][rows][2]: reference and sum
   int* parts;      // [shares][2]: the run a share leaves unfinished (-1: none), and its parts
   int part_rows;   // chunks: rows of a part
+  int even_pages;  // chunks: every 16 keys from a multiple of 16 lie in one page
   // chunks: the list of query tiles (plan_kernel)
   void* tiles;
   int64_t* before;  // [tiles + 1]: key tiles of the tiles before
