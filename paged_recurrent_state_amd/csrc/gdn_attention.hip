@@ -39,11 +39,12 @@ constexpr float kNoScore = -3.0e38f;  // reference before the first score
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Element types.  kBias: a new reference lies this far under the row's maximum,
-// which puts 2^{x - m} where a half still holds small weights to full precision;
-// kSlack more and the reference moves (2^(kBias + kSlack) stays in range).
+// Element types.  Chunks take references kUp above a row's maximum (see weigh);
+// fp16, whose small weights lose bits below 2^-14, stays closer.  Decode takes
+// them kBias below it, and new ones when a score exceeds them by kSlack more
+// (2^(kBias + kSlack) stays in fp16's range).
 struct Bf {
-  static constexpr float kBias = 0.f, kSlack = 8.f;
+  static constexpr float kUp = 7.f, kBias = 0.f, kSlack = 8.f;
   static __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
                                                    0, 0, 0);
@@ -51,7 +52,7 @@ struct Bf {
   static __device__ __forceinline__ uint32_t pack(float a, float b) { return f2bf2(a, b); }
 };
 struct Hf {
-  static constexpr float kBias = 7.f, kSlack = 8.f;
+  static constexpr float kUp = 3.f, kBias = 7.f, kSlack = 8.f;
   static __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
                                                   0, 0);
@@ -67,6 +68,7 @@ __device__ __forceinline__ float other_half(float x) {
 }
 
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+typedef __attribute__((address_space(3))) const u32x4* lds_u32x4;
 
 // Where piece c (8 values, 16 bytes) of row r of a K or V tile lies in LDS.
 // K fragments read one piece of 16 consecutive rows at a time, V fragments four
@@ -158,7 +160,10 @@ struct Chunk {
   static constexpr int kNQ = D == 256 ? 1 : 2;      // 32-row blocks of a wave
   static constexpr int kRows = 32 * kNQ * kWaves;   // query rows of a tile
   static constexpr int kKeys = D == 256 ? 32 : 64;  // keys of a tile
-  static constexpr int kSlotsK = 4, kSlotsV = 3;    // tiles of K and of V in LDS
+  // tiles the loads of K run ahead (those of V: one less): the K fragments of a block are read from
+  // LDS two blocks before its weights are formed, so one tile more where a tile is one block
+  static constexpr int kAhead = kKeys == 32 ? 4 : 3;
+  static constexpr int kSlotsK = kAhead, kSlotsV = kAhead;  // tiles of K and of V in LDS
   static constexpr int kPages = 4096;               // page ids staged at a time
   static constexpr int kSlot = kKeys * D * 2;       // bytes of a tile
   static constexpr int kLds = (kSlotsK + kSlotsV) * kSlot + kPages * 4;
@@ -279,6 +284,16 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
     off_v[x] = (uint32_t)(2 * r * p.kv.ts) + piece_v[x];
   }
 
+  // and where its fragments start in a slot: of K's step t, and of V's 32-wide block d (lane i of a
+  // 16-lane group points at 4 values of key i / 4 and receives value i of four keys)
+  uint32_t frag_k[kSteps], frag_v[kBlocks];
+#pragma unroll
+  for (int t = 0; t < kSteps; ++t) frag_k[t] = lds_of(smem) + k_at<D>(col, 2 * t + half);
+#pragma unroll
+  for (int d = 0; d < kBlocks; ++d)
+    frag_v[d] = lds_of(smem) + NSK * C::kSlot + 8 * (lane & 1) +
+                v_at<D>(4 * half + ((lane & 15) >> 2), 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1));
+
   for (int64_t u = first; u < end;) {
     const TileRec rec = ((const TileRec*)p.tiles)[ti];
     const int tiles = (int)(p.before[ti + 1] - p.before[ti]);
@@ -392,37 +407,50 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
           }
         }
       };
-      // tile i's values and tile i + 1's keys are in LDS, and every wave is done with tile i - 1
+      // tile i's values and the keys that its blocks read fragments of are in LDS, and every wave is
+      // done with what the loads that follow overwrite
       auto arrive = [&]() __attribute__((always_inline)) {
         wait_vm<2 * kLoads>();
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
       };
 
+      // K fragments of block kb (32 keys) of tile i
+      u32x4 kf[kSteps];
+      auto read_k = [&](int i, int kb) __attribute__((always_inline)) {
+        const uint32_t slot = (i % NSK) * C::kSlot;
+#pragma unroll
+        for (int t = 0; t < kSteps; ++t) kf[t] = *(lds_u32x4)(frag_k[t] + slot + kb * 32 * 2 * D);
+      };
+      // V fragments of block kb of tile i: keys 16 t + 4 half + 0..3, and 8 more
+      u32x2 vf[2][kBlocks][2];
+      auto read_v = [&](int i, int kb) __attribute__((always_inline)) {
+        const uint32_t slot = (i % NSV) * C::kSlot;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int d = 0; d < kBlocks; ++d)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              vf[t][d][x] = __builtin_bit_cast(
+                  u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                             (lds_s16x4)(frag_v[d] + slot + (kb * 32 + 16 * t + 8 * x) * 2 * D)));
+      };
       f32x16 s[NQ];
-      // scores of block kb (32 keys) of tile i
-      auto scores = [&](int i, int kb) __attribute__((always_inline)) {
-        const char* sk = smem + (i % NSK) * C::kSlot;
+      auto scores = [&]() __attribute__((always_inline)) {
 #pragma unroll
         for (int a = 0; a < NQ; ++a)
 #pragma unroll
           for (int e = 0; e < 16; ++e) s[a][e] = 0.f;
 #pragma unroll
-        for (int t = 0; t < kSteps; ++t) {
-          const u32x4 kf = *(const u32x4*)(sk + k_at<D>(kb * 32 + col, 2 * t + half));
+        for (int t = 0; t < kSteps; ++t)
 #pragma unroll
-          for (int a = 0; a < NQ; ++a) s[a] = E::mfma(kf, q[a][t], s[a]);
-        }
+          for (int a = 0; a < NQ; ++a) s[a] = E::mfma(kf[t], q[a][t], s[a]);
       };
-      // their masks, and the running reference
+      // their masks
       auto settle = [&](int i, int kb) __attribute__((always_inline)) {
         const int key0 = a0 + i * C::kKeys + kb * 32;
-        if constexpr (CAP) {
-#pragma unroll
-          for (int a = 0; a < NQ; ++a)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) s[a][e] = score<true>(p, s[a][e]);
-        }
         if (key0 + 31 > min(all_lim, a1 - 1) || key0 < all_low) {
+          asm volatile("");  // a branch: as selects the masks would cost every block
 #pragma unroll
           for (int a = 0; a < NQ; ++a) {
             // this lane's keys: 4 half + 8 (e / 4) + e % 4
@@ -435,22 +463,37 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
             }
           }
         }
-        const float scale = CAP ? 1.f : p.scale;
-        float top[NQ];
-        bool move = false;
+      };
+      u32x4 pt[NQ][2];
+      float w[NQ][16];
+      const float scale = CAP ? 1.f : p.scale;
+      auto weights = [&](const f32x16 (&x)[NQ]) __attribute__((always_inline)) {
+        uint32_t over = 0;
 #pragma unroll
-        for (int a = 0; a < NQ; ++a) {
-          top[a] = -INFINITY;
+        for (int a = 0; a < NQ; ++a)
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) top[a] = fmaxf(top[a], fmaxf(s[a][e], s[a][e + 1]));
-          top[a] *= scale;
-          move = move || top[a] > m[a] + (E::kBias + E::kSlack);
-        }
-        if (__any(move)) {
+          for (int e = 0; e < 16; e += 2) {
+            w[a][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[a][e], scale, -m[a]));
+            w[a][e + 1] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[a][e + 1], scale, -m[a]));
+            const uint32_t both = E::pack(w[a][e], w[a][e + 1]);
+            pt[a][e >> 3][(e >> 1) & 3] = both;
+            over |= both;
+          }
+        return over;
+      };
+      // The weights against the reference so far.  A weight of 2 or more, a NaN or an infinity has
+      // the top bit of its exponent set, in either 16-bit type: one such and the wave takes new
+      // references, kUp above its rows' maxima, so that this happens again only for a score that
+      // exceeds them by kUp + 1.
+      auto weigh = [&](const f32x16 (&x)[NQ]) __attribute__((always_inline)) {
+        if (__any((weights(x) & 0x40004000u) != 0)) {
 #pragma unroll
           for (int a = 0; a < NQ; ++a) {
-            const float up = fmaxf(top[a], other_half(top[a])) - E::kBias;
-            const float to = fmaxf(m[a], up), f = __builtin_amdgcn_exp2f(m[a] - to);
+            float top = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top = fmaxf(top, x[a][e]);
+            top = fmaxf(top, other_half(top)) * scale + E::kUp;
+            const float to = fmaxf(m[a], top), f = __builtin_amdgcn_exp2f(m[a] - to);
             m[a] = to;
             l[a] *= f;
 #pragma unroll
@@ -458,73 +501,71 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[a][d][e] *= f;
           }
+          weights(x);
         }
       };
-      u32x4 pt[NQ][2];
-      auto weights = [&](const f32x16 (&x)[NQ]) __attribute__((always_inline)) {
-        const float scale = CAP ? 1.f : p.scale;
-#pragma unroll
-        for (int a = 0; a < NQ; ++a)
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[a][e], scale, -m[a]));
-            const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[a][e + 1], scale, -m[a]));
-            l[a] += w0;
-            l[a] += w1;
-            pt[a][e >> 3][(e >> 1) & 3] = E::pack(w0, w1);
-          }
-      };
-      auto product = [&](int i, int kb) __attribute__((always_inline)) {
-        const char* sv = smem + (NSK + i % NSV) * C::kSlot;
+      auto product = [&]() __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int d = 0; d < kBlocks; ++d) {
-            // keys 16 t + 4 half + 0..3 and 8 more; lane i of a 16-lane group points at 4 values
-            // of key i / 4 and receives value i of the four keys
-            const int key = kb * 32 + 16 * t + 4 * half + ((lane & 15) >> 2);
-            const int dim = 32 * d + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-            const int sub = (dim & 7) * 2;
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(sv + v_at<D>(key, dim >> 3) + sub));
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(sv + v_at<D>(key + 8, dim >> 3) + sub));
-            const u32x2 wl = __builtin_bit_cast(u32x2, lo), wh = __builtin_bit_cast(u32x2, hi);
-            const u32x4 vf{wl[0], wl[1], wh[0], wh[1]};
+            const u32x4 f{vf[t][d][0][0], vf[t][d][0][1], vf[t][d][1][0], vf[t][d][1][1]};
 #pragma unroll
-            for (int a = 0; a < NQ; ++a) o[a][d] = E::mfma(vf, pt[a][t], o[a][d]);
+            for (int a = 0; a < NQ; ++a) o[a][d] = E::mfma(f, pt[a][t], o[a][d]);
           }
       };
-      // one block: its weights and product, and the next block's scores beside them
+      // one block: its weights and product; beside the weights the next block's scores, beside the
+      // product the reads of the fragments of the block after that
       auto block = [&](int i, int kb) __attribute__((always_inline)) {
         f32x16 x[NQ];
 #pragma unroll
         for (int a = 0; a < NQ; ++a) x[a] = s[a];
-        const int ni = kb + 1 < KB ? i : i + 1, nkb = kb + 1 < KB ? kb + 1 : 0;
-        scores(ni, nkb);
-        weights(x);
-        product(i, kb);
-        settle(ni, nkb);
+        read_v(i, kb);
+        scores();
+        weigh(x);
+        read_k(i + (KB == 1 ? 2 : 1), kb);
+        product();
+#pragma unroll
+        for (int a = 0; a < NQ; ++a)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            l[a] += w[a][e];
+            if constexpr (CAP) s[a][e] = score<true>(p, s[a][e]);
+          }
+        settle(kb + 1 < KB ? i : i + 1, kb + 1 < KB ? kb + 1 : 0);
       };
 
-      place(0, page_of(0));
-      load(0, false);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        load(x, true);
-        place(x + 1, page_of(x + 1));
-        load(x + 1, false);
+      for (int x = 0; x < C::kAhead; ++x) {
+        place(x, page_of(x));
+        load(x, false);
+        if (x < C::kAhead - 1) load(x, true);
       }
-      int id = page_of(3);
+      int id = page_of(C::kAhead);
       wait_vm<4 * kLoads>();
       asm volatile("s_barrier" ::: "memory");
-      scores(0, 0);
+      read_k(0, 0);
+      scores();
+      read_k(KB == 1 ? 1 : 0, KB == 1 ? 0 : 1);
+      if constexpr (CAP) {
+#pragma unroll
+        for (int a = 0; a < NQ; ++a)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[a][e] = score<true>(p, s[a][e]);
+      }
       settle(0, 0);
       // (the last block's "next" is a block of zeros, masked)
       for (int i = 0; i < count; ++i) {
+        // (the queries stay in accumulation registers, which the products read directly)
+#pragma unroll
+        for (int a = 0; a < NQ; ++a)
+#pragma unroll
+          for (int t = 0; t < kSteps; ++t) asm volatile("" : "+a"(q[a][t]));
         arrive();
-        load(i + 2, true);
-        place(i + 3, id);
-        load(i + 3, false);
-        id = page_of(i + 4);
+        load(i + C::kAhead - 1, true);
+        place(i + C::kAhead, id);
+        load(i + C::kAhead, false);
+        id = page_of(i + C::kAhead + 1);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) block(i, kb);
       }
