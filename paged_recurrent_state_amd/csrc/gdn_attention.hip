@@ -103,17 +103,31 @@ __device__ __forceinline__ void dma16(uint32_t lds, const void* src) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src)
                  : "memory", "m0");
 }
-// The same from a wave-uniform address and a 32-bit byte offset of each lane.
+// The same to `lds` (wave-uniform) + N from a wave-uniform address and a 32-bit byte offset of each lane.
+template <int N>
 __device__ __forceinline__ void dma16_at(uint32_t lds, const void* base, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
-               : "memory", "m0");
+  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base),
+               "n"(N)
+               : "memory", "m0", "scc");
 }
 #pragma clang diagnostic pop
 
+// A value that every lane of the wave holds, in a scalar register.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
   const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
   return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+// Loads into blocks S bytes apart.
+template <int S, int L>
+__device__ __forceinline__ void load_blocks(uint32_t lds, const void* base, const uint32_t (&off)[L]) {
+  dma16_at<0>(lds, base, off[0]);
+  if constexpr (L > 1) dma16_at<S>(lds, base, off[1]);
+  if constexpr (L > 2) dma16_at<2 * S>(lds, base, off[2]);
+  if constexpr (L > 3) dma16_at<3 * S>(lds, base, off[3]);
+  static_assert(L <= 4, "one line a load");
 }
 
 template <int N>
@@ -164,9 +178,27 @@ struct Chunk {
   // LDS two blocks before its weights are formed, so one tile more where a tile is one block
   static constexpr int kAhead = kKeys == 32 ? 4 : 3;
   static constexpr int kSlotsK = kAhead, kSlotsV = kAhead;  // tiles of K and of V in LDS
-  static constexpr int kPages = 4096;               // page ids staged at a time
-  static constexpr int kSlot = kKeys * D * 2;       // bytes of a tile
-  static constexpr int kLds = (kSlotsK + kSlotsV) * kSlot + kPages * 4;
+  static constexpr int kPlaces = 2048;              // places of rows staged at a time (see `places`)
+  // A load instruction brings kLoadRows rows into one block of 1 KiB.  In a block of K a row's 16-byte
+  // pieces stay in order, but for the lowest bits of their number, turned by the row's; blocks lie
+  // kPadK bytes further apart than 1 KiB: 16 rows of one piece then touch every bank once, and a
+  // fragment's address is one of kTurnsK registers and an immediate.  In a block of V the 64-byte
+  // quarter-, half- or eighth-rows that one product takes lie together, row by row, so that the
+  // transposed read of four rows covers 256 bytes in one piece.
+  static constexpr int kLoadRows = 512 / D;
+  static constexpr int kTurnsK = D == 256 ? 1 : 2;
+  static constexpr int kBlockK = 1024 + (D == 256 ? 32 : 64), kBlockV = 1024 + (D == 256 ? 128 : 0);
+  static constexpr int kBlocks = kKeys / kLoadRows;  // of a tile
+  static constexpr int kSlotK = kBlocks * kBlockK, kSlotV = kBlocks * kBlockV;  // bytes of a tile
+  static __device__ __forceinline__ int turn_k(int r) { return D == 64 ? (r >> 1) & 3 : D == 128 ? r & 3 : r & 1; }
+  // piece c of row r of a tile
+  static __device__ __forceinline__ int k_at(int r, int c) {
+    return r / kLoadRows * kBlockK + r % kLoadRows * 2 * D + ((c ^ turn_k(r)) << 4);
+  }
+  static __device__ __forceinline__ int v_at(int r, int c) {
+    return r / kLoadRows * kBlockV + (c >> 2) * (64 * kLoadRows) + r % kLoadRows * 64 + ((c & 3) << 4);
+  }
+  static constexpr int kLds = kSlotsK * kSlotK + kSlotsV * kSlotV + kPlaces * 8;
 };
 
 // A tile of query rows (plan_kernel): sequence, place in it, keys it sees.
@@ -246,17 +278,18 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
   constexpr int NQ = C::kNQ, NSK = C::kSlotsK, NSV = C::kSlotsV, KB = C::kKeys / 32;
   constexpr int kSteps = D / 16;   // MFMA steps over D
   constexpr int kBlocks = D / 32;  // 32-wide blocks of the output
-  constexpr int kLoads = C::kSlot / 1024 / kWaves;  // load instructions of a wave for a tile of K or V
-  constexpr int kLoadRows = C::kKeys / kWaves;      // rows they cover
-  constexpr int kRowsPerLoad = 512 / D;
+  constexpr int kLoads = C::kBlocks / kWaves;  // load instructions of a wave for a tile of K or V
+  constexpr int kRowsW = C::kKeys / kWaves;    // rows they cover
   extern __shared__ __attribute__((aligned(1024))) char smem[];
-  int* page_ids = (int*)(smem + (NSK + NSV) * C::kSlot);
+  // Where rows of the run's keys lie in the caches, in bytes from the start of their kv-head: of every
+  // kRowsW-th row, or of every row when pages may end between them
+  int64_t* places = (int64_t*)(smem + NSK * C::kSlotK + NSV * C::kSlotV);
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, col = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int G = (int)p.group.d;
 
-  const int num_tiles = p.num_tiles[0];
-  const int64_t per_head = p.before[num_tiles], units = per_head * p.Hkv;
+  const int num_tiles = uniform(p.num_tiles[0]);
+  const int64_t per_head = uniform64(p.before[num_tiles]), units = per_head * p.Hkv;
   const int64_t share = (units + gridDim.x - 1) / gridDim.x;
   // neighbouring shares on one XCD (workgroup x runs on XCD x % 8)
   const int shares8 = gridDim.x >> 3;
@@ -267,40 +300,41 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
     if (tid == 0) tail[0] = -1;
     return;
   }
-  int hk = (int)(first / per_head);
-  int ti = find_tile(p.before, num_tiles, first - hk * per_head);
-  int done = (int)(first - hk * per_head - p.before[ti]);  // key tiles of it already taken by the share before
+  int hk = uniform((int)(first / per_head));
+  int ti = uniform(find_tile(p.before, num_tiles, first - hk * per_head));
+  int done = (int)(first - hk * per_head - uniform64(p.before[ti]));  // key tiles of it already taken by the share before
   bool left = false;
 
-  // What each lane loads of a row: the piece that belongs at its place in LDS (k_at, v_at: the
-  // turning is its own inverse), and where that is from the first row of the wave's part of a tile
-  uint32_t piece_k[kLoads], piece_v[kLoads], off_k[kLoads], off_v[kLoads];
+  // What each lane loads (the piece that belongs at its place in the block), and where that is from
+  // the first row of the wave's part of a tile
+  const int kr = lane / (D / 8), vr = (lane >> 2) % C::kLoadRows;
+  const uint32_t piece_v = 16 * ((lane >> 2) / C::kLoadRows * 4 + (lane & 3));
+  uint32_t piece_k[kLoads], off_k[kLoads], off_v[kLoads];
 #pragma unroll
   for (int x = 0; x < kLoads; ++x) {
-    const int r = x * kRowsPerLoad + lane / (D / 8), tr = wave * kLoadRows + r, slot = lane % (D / 8);
-    piece_k[x] = 16 * (slot ^ (D == 64 ? (tr >> 1) & 7 : tr & 15));
-    piece_v[x] = 16 * (slot ^ (D == 64 ? ((tr >> 1) & 1) << 2 : (tr & 3) << 2));
-    off_k[x] = (uint32_t)(2 * r * p.kv.ts) + piece_k[x];
-    off_v[x] = (uint32_t)(2 * r * p.kv.ts) + piece_v[x];
+    const int r = x * C::kLoadRows;
+    piece_k[x] = 16 * ((lane % (D / 8)) ^ C::turn_k(wave * kRowsW + r + kr));
+    off_k[x] = (uint32_t)(2 * (r + kr) * p.kv.ts) + piece_k[x];
+    off_v[x] = (uint32_t)(2 * (r + vr) * p.kv.ts) + piece_v;
   }
+  // and where its fragments start in a slot: of K's first steps, and of V (lane i of a 16-lane group
+  // points at 4 values of key i / 4 and receives value i of four keys)
+  uint32_t frag_k[C::kTurnsK];
+#pragma unroll
+  for (int t = 0; t < C::kTurnsK; ++t) frag_k[t] = lds_of(smem) + C::k_at(col, 2 * t + half);
+  const uint32_t frag_v = lds_of(smem) + NSK * C::kSlotK + 8 * (lane & 1) +
+                          C::v_at(4 * half + ((lane & 15) >> 2), 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1));
 
-  // and where its fragments start in a slot: of K's step t, and of V's 32-wide block d (lane i of a
-  // 16-lane group points at 4 values of key i / 4 and receives value i of four keys)
-  uint32_t frag_k[kSteps], frag_v[kBlocks];
-#pragma unroll
-  for (int t = 0; t < kSteps; ++t) frag_k[t] = lds_of(smem) + k_at<D>(col, 2 * t + half);
-#pragma unroll
-  for (int d = 0; d < kBlocks; ++d)
-    frag_v[d] = lds_of(smem) + NSK * C::kSlot + 8 * (lane & 1) +
-                v_at<D>(4 * half + ((lane & 15) >> 2), 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1));
+  const uint32_t token_bytes = (uint32_t)(2 * p.kv.ts);
 
   for (int64_t u = first; u < end;) {
-    const TileRec rec = ((const TileRec*)p.tiles)[ti];
-    const int tiles = (int)(p.before[ti + 1] - p.before[ti]);
+    TileRec rec = ((const TileRec*)p.tiles)[ti];
+    rec = TileRec{uniform(rec.b), uniform(rec.tile), uniform(rec.key_begin), uniform(rec.key_end)};
+    const int tiles = uniform((int)(p.before[ti + 1] - p.before[ti]));
     const int todo = (int)min((int64_t)(tiles - done), end - u);
-    const int tok0 = p.cu[rec.b], n = p.cu[rec.b + 1] - tok0;
-    const int first_page = p.kv.ptr[rec.b], pages = p.kv.ptr[rec.b + 1] - first_page;
-    const int len = pages > 0 ? (pages - 1) * (int)p.kv.page.d + p.kv.lpl[rec.b] : 0;
+    const int tok0 = uniform(p.cu[rec.b]), n = uniform(p.cu[rec.b + 1]) - tok0;
+    const int first_page = uniform(p.kv.ptr[rec.b]), pages = uniform(p.kv.ptr[rec.b + 1]) - first_page;
+    const int len = pages > 0 ? (pages - 1) * (int)p.kv.page.d + uniform(p.kv.lpl[rec.b]) : 0;
     const int past = len - n;
 
     // this lane's rows
@@ -351,59 +385,53 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
     const char* kbase = p.kv.k + 2 * (int64_t)hk * p.kv.hs;
     const char* vbase = p.kv.v + 2 * (int64_t)hk * p.kv.hs;
 
-    // as many tiles at a time as the staged page ids reach
+    // as many tiles at a time as the staged places reach
+    const int step = p.even_pages ? kRowsW : 1;
     for (int a0 = key_a; a0 < key_b;) {
-      const int page0 = (int)div_by(a0, p.kv.page);
-      const int64_t reach = (int64_t)(page0 + C::kPages) * p.kv.page.d;  // first key past the staged pages
-      // (whole tiles; kPages pages are more than a tile's keys)
-      const int a1 = reach >= key_b ? key_b : (int)reach / C::kKeys * C::kKeys;
+      const int a1 = (int)min((int64_t)key_b, a0 + (int64_t)C::kPlaces * step);
       const int count = (a1 - a0 + C::kKeys - 1) / C::kKeys;
       __syncthreads();
-      {
-        const int last = (int)div_by(a1 - 1, p.kv.page);
-        for (int i = tid; i <= last - page0; i += 64 * kWaves) page_ids[i] = p.kv.idx[first_page + page0 + i];
+      for (int x = tid; a0 + x * step < a1; x += 64 * kWaves) {
+        const int key = a0 + x * step, pg = (int)div_by(key, p.kv.page);
+        places[x] = 2 * ((int64_t)p.kv.idx[first_page + pg] * p.kv.ps + (int64_t)(key - pg * (int)p.kv.page.d) * p.kv.ts);
       }
       __syncthreads();
 
-      // Where this wave's rows of a tile lie in the caches, in bytes from the start of its kv-head:
-      // one place for all of them when they lie in one page and are all there, otherwise each
-      // lane's own (-1: past the end, zeros).  A tile's keys and, an iteration later, its values
-      // go by the same places.
+      // This wave's rows of a tile: one place when they lie in one page and are all there, otherwise
+      // each lane's own (-1: past the end, zeros).  A tile's keys and, an iteration later, its values
+      // go by the same places; `next` is read from LDS a tile ahead.
       bool one;
-      int64_t at;
-      int64_t lane_at[kLoads];
-      auto page_of = [&](int i) __attribute__((always_inline)) {
-        const int key = min(a0 + i * C::kKeys + wave * kLoadRows, a1 - 1);
-        return page_ids[(int)div_by(key, p.kv.page) - page0];
-      };
-      auto place = [&](int i, int id) __attribute__((always_inline)) {
-        const int key0 = a0 + i * C::kKeys + wave * kLoadRows;
-        one = p.even_pages && key0 + kLoadRows <= a1;
-        if (one) {
-          const int off = key0 - (int)div_by(key0, p.kv.page) * (int)p.kv.page.d;
-          at = 2 * ((int64_t)__builtin_amdgcn_readfirstlane(id) * p.kv.ps + (int64_t)off * p.kv.ts);
-        } else {
+      int64_t at, next = places[wave];
+      int64_t lane_at[kLoads][2];
+      auto place = [&](int i) __attribute__((always_inline)) {
+        const int key0 = a0 + i * C::kKeys + wave * kRowsW;
+        one = p.even_pages && key0 + kRowsW <= a1;
+        at = uniform64(next);
+        if (!one) {
 #pragma unroll
-          for (int x = 0; x < kLoads; ++x) {
-            const int key = key0 + x * kRowsPerLoad + lane / (D / 8), k = min(key, a1 - 1);
-            const int pg = (int)div_by(k, p.kv.page);
-            const int64_t to = 2 * ((int64_t)page_ids[pg - page0] * p.kv.ps + (int64_t)(k - pg * (int)p.kv.page.d) * p.kv.ts);
-            lane_at[x] = key < a1 ? to : -1;
+          for (int x = 0; x < 2 * kLoads; ++x) {
+            const int r = x / 2 * C::kLoadRows + (x & 1 ? vr : kr);
+            const int64_t to = p.even_pages ? at + r * (int64_t)token_bytes : places[min(key0 + r, a1 - 1) - a0];
+            lane_at[x / 2][x & 1] = key0 + r < a1 ? to : -1;
           }
         }
+        next = places[min((i + 1) * kWaves + wave, C::kPlaces - 1)];
       };
       // the placed tile's keys (or V: values) into the slot of tile i
       auto load = [&](int i, bool V) __attribute__((always_inline)) {
-        const uint32_t dst = lds_of(smem) + (V ? NSK + i % NSV : i % NSK) * C::kSlot + wave * (kLoads * 1024);
+        const uint32_t dst = lds_of(smem) + (V ? NSK * C::kSlotK + i % NSV * C::kSlotV : i % NSK * C::kSlotK) +
+                             wave * (kLoads * (V ? C::kBlockV : C::kBlockK));
         if (one) {
           const char* base = (V ? vbase : kbase) + at;
-#pragma unroll
-          for (int x = 0; x < kLoads; ++x) dma16_at(dst + x * 1024, base, V ? off_v[x] : off_k[x]);
+          if (V)
+            load_blocks<C::kBlockV>(dst, base, off_v);
+          else
+            load_blocks<C::kBlockK>(dst, base, off_k);
         } else {
 #pragma unroll
           for (int x = 0; x < kLoads; ++x) {
-            const char* src = (V ? vbase : kbase) + lane_at[x] + (V ? piece_v[x] : piece_k[x]);
-            dma16<false>(dst + x * 1024, lane_at[x] < 0 ? (const char*)&g_zero : src);
+            const char* src = (V ? vbase : kbase) + lane_at[x][V] + (V ? piece_v : piece_k[x]);
+            dma16<false>(dst + x * (V ? C::kBlockV : C::kBlockK), lane_at[x][V] < 0 ? (const char*)&g_zero : src);
           }
         }
       };
@@ -417,14 +445,22 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
       // K fragments of block kb (32 keys) of tile i
       u32x4 kf[kSteps];
       auto read_k = [&](int i, int kb) __attribute__((always_inline)) {
-        const uint32_t slot = (i % NSK) * C::kSlot;
+        uint32_t from[C::kTurnsK];
 #pragma unroll
-        for (int t = 0; t < kSteps; ++t) kf[t] = *(lds_u32x4)(frag_k[t] + slot + kb * 32 * 2 * D);
+        for (int t = 0; t < C::kTurnsK; ++t) {
+          from[t] = frag_k[t] + i % NSK * C::kSlotK;
+          asm("" : "+v"(from[t]));  // (so that the rest goes into the reads' immediates)
+        }
+#pragma unroll
+        for (int t = 0; t < kSteps; ++t)
+          kf[t] = *(lds_u32x4)(from[t % C::kTurnsK] + t / C::kTurnsK * (32 * C::kTurnsK) +
+                               kb * 32 / C::kLoadRows * C::kBlockK);
       };
       // V fragments of block kb of tile i: keys 16 t + 4 half + 0..3, and 8 more
       u32x2 vf[2][kBlocks][2];
       auto read_v = [&](int i, int kb) __attribute__((always_inline)) {
-        const uint32_t slot = (i % NSV) * C::kSlot;
+        uint32_t from = frag_v + i % NSV * C::kSlotV;
+        asm("" : "+v"(from));
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -433,7 +469,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
             for (int x = 0; x < 2; ++x)
               vf[t][d][x] = __builtin_bit_cast(
                   u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                             (lds_s16x4)(frag_v[d] + slot + (kb * 32 + 16 * t + 8 * x) * 2 * D)));
+                             (lds_s16x4)(from + (kb * 32 + 16 * t + 8 * x) / C::kLoadRows * C::kBlockV +
+                                         d * (64 * C::kLoadRows))));
       };
       f32x16 s[NQ];
       auto scores = [&]() __attribute__((always_inline)) {
@@ -464,8 +501,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
           }
         }
       };
-      u32x4 pt[NQ][2];
-      float w[NQ][16];
+      u32x4 pt[NQ][2], pw[NQ][2];
+      float sum[NQ];
       const float scale = CAP ? 1.f : p.scale;
       auto weights = [&](const f32x16 (&x)[NQ]) __attribute__((always_inline)) {
         uint32_t over = 0;
@@ -473,36 +510,32 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
         for (int a = 0; a < NQ; ++a)
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
-            w[a][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[a][e], scale, -m[a]));
-            w[a][e + 1] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[a][e + 1], scale, -m[a]));
-            const uint32_t both = E::pack(w[a][e], w[a][e + 1]);
-            pt[a][e >> 3][(e >> 1) & 3] = both;
+            const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[a][e], scale, -m[a]));
+            const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[a][e + 1], scale, -m[a]));
+            sum[a] = e == 0 ? w0 + w1 : sum[a] + w0 + w1;
+            const uint32_t both = E::pack(w0, w1);
+            pw[a][e >> 3][(e >> 1) & 3] = both;
             over |= both;
           }
         return over;
       };
-      // The weights against the reference so far.  A weight of 2 or more, a NaN or an infinity has
-      // the top bit of its exponent set, in either 16-bit type: one such and the wave takes new
-      // references, kUp above its rows' maxima, so that this happens again only for a score that
-      // exceeds them by kUp + 1.
-      auto weigh = [&](const f32x16 (&x)[NQ]) __attribute__((always_inline)) {
-        if (__any((weights(x) & 0x40004000u) != 0)) {
+      // New references, kUp above the rows' maxima, and the weights against them.
+      auto move = [&](const f32x16 (&x)[NQ]) __attribute__((always_inline)) {
 #pragma unroll
-          for (int a = 0; a < NQ; ++a) {
-            float top = -INFINITY;
+        for (int a = 0; a < NQ; ++a) {
+          float top = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) top = fmaxf(top, x[a][e]);
-            top = fmaxf(top, other_half(top)) * scale + E::kUp;
-            const float to = fmaxf(m[a], top), f = __builtin_amdgcn_exp2f(m[a] - to);
-            m[a] = to;
-            l[a] *= f;
+          for (int e = 0; e < 16; ++e) top = fmaxf(top, x[a][e]);
+          top = fmaxf(top, other_half(top)) * scale + E::kUp;
+          const float to = fmaxf(m[a], top), f = __builtin_amdgcn_exp2f(m[a] - to);
+          m[a] = to;
+          l[a] *= f;
 #pragma unroll
-            for (int d = 0; d < kBlocks; ++d)
+          for (int d = 0; d < kBlocks; ++d)
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[a][d][e] *= f;
-          }
-          weights(x);
+            for (int e = 0; e < 16; ++e) o[a][d][e] *= f;
         }
+        weights(x);
       };
       auto product = [&]() __attribute__((always_inline)) {
 #pragma unroll
@@ -514,34 +547,48 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
             for (int a = 0; a < NQ; ++a) o[a][d] = E::mfma(f, pt[a][t], o[a][d]);
           }
       };
-      // one block: its weights and product; beside the weights the next block's scores, beside the
-      // product the reads of the fragments of the block after that
+      // One block: its weights, and beside them the product of the block before and the scores of the
+      // block after.  The weights are formed against the reference so far.  A weight of 2 or more, a
+      // NaN or an infinity has the top bit of its exponent set, in either 16-bit type: one such and
+      // the wave takes new references, kUp above its rows' maxima, so that this happens again only
+      // for a score that exceeds them by kUp + 1.
       auto block = [&](int i, int kb) __attribute__((always_inline)) {
         f32x16 x[NQ];
 #pragma unroll
         for (int a = 0; a < NQ; ++a) x[a] = s[a];
+        product();
         read_v(i, kb);
         scores();
-        weigh(x);
         read_k(i + (KB == 1 ? 2 : 1), kb);
-        product();
+        const uint32_t over = weights(x);
 #pragma unroll
-        for (int a = 0; a < NQ; ++a)
+        for (int t = 0; t < kSteps * NQ + 2 * kBlocks * NQ; ++t) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+        }
+        if (__any((over & 0x40004000u) != 0)) move(x);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            l[a] += w[a][e];
-            if constexpr (CAP) s[a][e] = score<true>(p, s[a][e]);
-          }
+        for (int a = 0; a < NQ; ++a) {
+          l[a] += sum[a];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) pt[a][t] = pw[a][t];
+        }
+        if constexpr (CAP) {
+#pragma unroll
+          for (int a = 0; a < NQ; ++a)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[a][e] = score<true>(p, s[a][e]);
+        }
         settle(kb + 1 < KB ? i : i + 1, kb + 1 < KB ? kb + 1 : 0);
       };
 
 #pragma unroll
       for (int x = 0; x < C::kAhead; ++x) {
-        place(x, page_of(x));
+        place(x);
         load(x, false);
         if (x < C::kAhead - 1) load(x, true);
       }
-      int id = page_of(C::kAhead);
       wait_vm<4 * kLoads>();
       asm volatile("s_barrier" ::: "memory");
       read_k(0, 0);
@@ -554,6 +601,13 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
           for (int e = 0; e < 16; ++e) s[a][e] = score<true>(p, s[a][e]);
       }
       settle(0, 0);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int a = 0; a < NQ; ++a) pt[a][t] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int d = 0; d < kBlocks; ++d) vf[t][d][0] = vf[t][d][1] = u32x2{0u, 0u};
+      }
       // (the last block's "next" is a block of zeros, masked)
       for (int i = 0; i < count; ++i) {
         // (the queries stay in accumulation registers, which the products read directly)
@@ -563,12 +617,12 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
           for (int t = 0; t < kSteps; ++t) asm volatile("" : "+a"(q[a][t]));
         arrive();
         load(i + C::kAhead - 1, true);
-        place(i + C::kAhead, id);
+        place(i + C::kAhead);
         load(i + C::kAhead, false);
-        id = page_of(i + C::kAhead + 1);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) block(i, kb);
       }
+      product();
       wait_vm<0>();
       a0 = a1;
     }
@@ -733,9 +787,9 @@ hipError_t launch_chunk(AttnParams p, void* workspace, hipStream_t s) {
   p.part_ml = (float*)(base + w.ml);
   p.part_o = (float*)(base + w.o);
   p.part_rows = (int)w.part_rows;
-  // a wave's rows of a tile start at a multiple of 16 (or 8) keys; their offsets from the first
-  // must fit 32 bits
-  p.even_pages = p.kv.page.d % 16 == 0 && p.kv.ts >= 0 && p.kv.ts < (int64_t(1) << 26);
+  // a wave's rows of a tile start at a multiple of 16 (or 8) keys; their offsets in a page must fit
+  // 32 bits
+  p.even_pages = p.kv.page.d % 16 == 0 && p.kv.ts >= 0 && p.kv.ts * p.kv.page.d < (int64_t(1) << 30);
   return p.cap > 0.f ? launch_chunk_cap<E, D, true>(p, s) : launch_chunk_cap<E, D, false>(p, s);
 }
 
