@@ -22,6 +22,7 @@
 // workgroup's tile (row = token * group + head): K and V are read once for them.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "gdn_internal.h"
 
@@ -39,12 +40,15 @@ constexpr float kNoScore = -3.0e38f;  // reference before the first score
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Element types.  Chunks take references kUp above a row's maximum (see weigh);
-// fp16, whose small weights lose bits below 2^-14, stays closer.  Decode takes
-// them kBias below it, and new ones when a score exceeds them by kSlack more
-// (2^(kBias + kSlack) stays in fp16's range).
+// Element types.  Decode takes references kBias below a row's maximum, and new
+// ones when a score exceeds them by kSlack more (2^(kBias + kSlack) stays in
+// fp16's range).  Chunks take them kUp above the maximum of the first block a row
+// sees, and keep them while the row's weights sum to at most kHigh and nothing
+// overflows (fp16: later scores up to 20 above that maximum).  kOne is 1 in the
+// type, kExp and kCarry find values that are not finite in a packed pair.
 struct Bf {
-  static constexpr float kUp = 7.f, kBias = 0.f, kSlack = 8.f;
+  static constexpr float kBias = 0.f, kSlack = 8.f, kUp = 0.f, kHigh = 0x1p100f;
+  static constexpr uint32_t kOne = 0x3f80u, kExp = 0x7f807f80u, kCarry = 0x00800080u;
   static __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
                                                    0, 0, 0);
@@ -52,7 +56,8 @@ struct Bf {
   static __device__ __forceinline__ uint32_t pack(float a, float b) { return f2bf2(a, b); }
 };
 struct Hf {
-  static constexpr float kUp = 3.f, kBias = 7.f, kSlack = 8.f;
+  static constexpr float kBias = 7.f, kSlack = 8.f, kUp = 4.f, kHigh = 0x1p100f;
+  static constexpr uint32_t kOne = 0x3c00u, kExp = 0x7c007c00u, kCarry = 0x04000400u;
   static __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
                                                   0, 0);
@@ -103,12 +108,10 @@ __device__ __forceinline__ void dma16(uint32_t lds, const void* src) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src)
                  : "memory", "m0");
 }
-// The same to `lds` (wave-uniform) + N from a wave-uniform address and a 32-bit byte offset of each lane.
-template <int N>
+// The same from a wave-uniform address and a 32-bit byte offset of each lane.
 __device__ __forceinline__ void dma16_at(uint32_t lds, const void* base, uint32_t off) {
-  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base),
-               "n"(N)
-               : "memory", "m0", "scc");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
 }
 #pragma clang diagnostic pop
 
@@ -118,16 +121,6 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
   const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
   return (int64_t)(((uint64_t)hi << 32) | lo);
-}
-
-// Loads into blocks S bytes apart.
-template <int S, int L>
-__device__ __forceinline__ void load_blocks(uint32_t lds, const void* base, const uint32_t (&off)[L]) {
-  dma16_at<0>(lds, base, off[0]);
-  if constexpr (L > 1) dma16_at<S>(lds, base, off[1]);
-  if constexpr (L > 2) dma16_at<2 * S>(lds, base, off[2]);
-  if constexpr (L > 3) dma16_at<3 * S>(lds, base, off[3]);
-  static_assert(L <= 4, "one line a load");
 }
 
 template <int N>
@@ -174,10 +167,9 @@ struct Chunk {
   static constexpr int kNQ = D == 256 ? 1 : 2;      // 32-row blocks of a wave
   static constexpr int kRows = 32 * kNQ * kWaves;   // query rows of a tile
   static constexpr int kKeys = D == 256 ? 32 : 64;  // keys of a tile
-  // tiles the loads of K run ahead (those of V: one less): the K fragments of a block are read from
-  // LDS two blocks before its weights are formed, so one tile more where a tile is one block
-  static constexpr int kAhead = kKeys == 32 ? 4 : 3;
-  static constexpr int kSlotsK = kAhead, kSlotsV = kAhead;  // tiles of K and of V in LDS
+  // tiles of K and of V in LDS: K's loads run three tiles ahead, V's two; the keys of a tile's later
+  // blocks are still read while its first is worked on
+  static constexpr int kSlotsK = kKeys == 32 ? 3 : 4, kSlotsV = 3;
   static constexpr int kPlaces = 2048;              // places of rows staged at a time (see `places`)
   // A load instruction brings kLoadRows rows into one block of 1 KiB.  In a block of K a row's 16-byte
   // pieces stay in order, but for the lowest bits of their number, turned by the row's; blocks lie
@@ -206,9 +198,12 @@ struct TileRec {
   int b, tile, key_begin, key_end;
 };
 
+constexpr int kTileCost = 512;  // what starting and ending a tile costs, in keys
+constexpr int kMinShare = 2;  // key tiles of a share at least: fewer parts to join
+
 // One workgroup: lists every sequence's tiles, and the running total of their key
 // tiles (of one kv-head), [tiles + 1].
-__global__ __launch_bounds__(1024) void plan_kernel(AttnParams p, int rows, int keys) {
+__global__ __launch_bounds__(1024) void plan_kernel(AttnParams p, int rows, int keys, int shares) {
   const int B = p.kv.B, G = (int)p.group.d;
   // tiles before each sequence
   const int per = (B + 1023) / 1024;
@@ -255,21 +250,60 @@ __global__ __launch_bounds__(1024) void plan_kernel(AttnParams p, int rows, int 
     if (i < total) p.before[i] = run + before;
     run += sum;
   }
-  if (threadIdx.x == 0) p.before[total] = run;
+  if (threadIdx.x == 0) {
+    p.before[total] = run;
+    // a tile costs as many key tiles more than it has, or less where shares are small
+    p.num_tiles[1] = (int)min((int64_t)(kTileCost / keys), run * p.Hkv / (4 * (int64_t)shares));
+  }
 }
 
-// The last tile whose running total is at most x (the whole wave searches).
-__device__ __forceinline__ int find_tile(const int64_t* before, int tiles, int64_t x) {
+// The last tile that starts at most x in, each `cost` more than its key tiles (the whole wave searches).
+__device__ __forceinline__ int find_tile(const int64_t* before, int tiles, int cost, int64_t x) {
   const int lane = threadIdx.x & 63;
   int lo = 0, n = tiles - 1;  // among before[1 .. tiles - 1]
   while (n > 0) {
     const int step = (n + 63) >> 6;
     const int64_t at = int64_t(lane + 1) * step;
-    const int c = __popcll(__ballot(at <= n && before[lo + (at <= n ? at : 1)] <= x));
+    const int64_t i = lo + (at <= n ? at : 1);
+    const int c = __popcll(__ballot(at <= n && before[i] + i * cost <= x));
     lo += c * step;
     n = step == 1 ? 0 : min(step - 1, n - c * step);
   }
   return lo;
+}
+
+// A lane's column of output (row in_tile of the tile, half of its values): the
+// finished row, or, into part `part` >= 0, what the join needs.
+template <class E, int D>
+__device__ __forceinline__ void store_rows(const AttnParams& p, const TileRec& rec, int hk, int tok0, int n, int in_tile,
+                                           int64_t part, const f32x16 (&o)[D / 32], float m, float sum, bool none) {
+  const int half = (threadIdx.x & 63) >> 5, row = rec.tile * Chunk<D>::kRows + in_tile;
+  const int tok = (int)div_by(row, p.group), g = row - tok * (int)p.group.d;
+  if (tok >= n) return;
+  if (part < 0) {
+    const float inv = none ? 0.f : 1.f / sum;
+    const int64_t h = (int64_t)hk * p.group.d + g;
+    u16* dst = (u16*)p.o.p + (int64_t)(tok0 + tok) * p.o.ts + h * p.o.hs;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *(u32x2*)(dst + 32 * d + 8 * i + 4 * half) = u32x2{E::pack(o[d][4 * i] * inv, o[d][4 * i + 1] * inv),
+                                                           E::pack(o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv)};
+    if (p.lse && half == 0)
+      p.lse[(int64_t)(tok0 + tok) * p.Hq + h] = none ? -INFINITY : (m + __builtin_amdgcn_logf(sum)) * kLn2;
+  } else {
+    float* dst = p.part_o + (part * p.part_rows + in_tile) * D;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *(f32x4*)(dst + 32 * d + 8 * i + 4 * half) = f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+    if (half == 0) {
+      p.part_ml[(part * p.part_rows + in_tile) * 2] = m;
+      p.part_ml[(part * p.part_rows + in_tile) * 2 + 1] = sum;
+    }
+  }
 }
 
 template <class E, int D, bool CAP>
@@ -288,9 +322,9 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int G = (int)p.group.d;
 
-  const int num_tiles = uniform(p.num_tiles[0]);
-  const int64_t per_head = uniform64(p.before[num_tiles]), units = per_head * p.Hkv;
-  const int64_t share = (units + gridDim.x - 1) / gridDim.x;
+  const int num_tiles = uniform(p.num_tiles[0]), cost = uniform(p.num_tiles[1]);
+  const int64_t per_head = uniform64(p.before[num_tiles]) + (int64_t)num_tiles * cost, units = per_head * p.Hkv;
+  const int64_t share = max((int64_t)kMinShare, (units + gridDim.x - 1) / gridDim.x);
   // neighbouring shares on one XCD (workgroup x runs on XCD x % 8)
   const int shares8 = gridDim.x >> 3;
   const int me = (gridDim.x & 7) ? blockIdx.x : (blockIdx.x & 7) * shares8 + (blockIdx.x >> 3);
@@ -300,9 +334,9 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
     if (tid == 0) tail[0] = -1;
     return;
   }
+  bool off = false;
   int hk = uniform((int)(first / per_head));
-  int ti = uniform(find_tile(p.before, num_tiles, first - hk * per_head));
-  int done = (int)(first - hk * per_head - uniform64(p.before[ti]));  // key tiles of it already taken by the share before
+  int ti = uniform(find_tile(p.before, num_tiles, cost, first - hk * per_head));
   bool left = false;
 
   // What each lane loads (the piece that belongs at its place in the block), and where that is from
@@ -327,11 +361,15 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
 
   const uint32_t token_bytes = (uint32_t)(2 * p.kv.ts);
 
-  for (int64_t u = first; u < end;) {
+  for (;;) {
     TileRec rec = ((const TileRec*)p.tiles)[ti];
     rec = TileRec{uniform(rec.b), uniform(rec.tile), uniform(rec.key_begin), uniform(rec.key_end)};
+    // this share's part of the tile's key tiles: from `done` on (those before are the share before's)
+    const int64_t start = hk * per_head + uniform64(p.before[ti]) + (int64_t)ti * cost;
     const int tiles = uniform((int)(p.before[ti + 1] - p.before[ti]));
-    const int todo = (int)min((int64_t)(tiles - done), end - u);
+    const int done = (int)max((int64_t)0, first - start - cost);
+    const int todo = (int)min((int64_t)tiles, end - start - cost) - done;
+    if (todo > 0) {
     const int tok0 = uniform(p.cu[rec.b]), n = uniform(p.cu[rec.b + 1]) - tok0;
     const int first_page = uniform(p.kv.ptr[rec.b]), pages = uniform(p.kv.ptr[rec.b + 1]) - first_page;
     const int len = pages > 0 ? (pages - 1) * (int)p.kv.page.d + uniform(p.kv.lpl[rec.b]) : 0;
@@ -368,11 +406,19 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
     all_lim = __builtin_amdgcn_readfirstlane(all_lim);
     all_low = __builtin_amdgcn_readfirstlane(all_low);
 
+    const int key_a = rec.key_begin + done * C::kKeys;
+    const int key_b = min(rec.key_end, key_a + todo * C::kKeys);
+    const char* kbase = p.kv.k + 2 * (int64_t)hk * p.kv.hs;
+    const char* vbase = p.kv.v + 2 * (int64_t)hk * p.kv.hs;
+
     f32x16 o[NQ][kBlocks];
     float m[NQ], l[NQ];
+    const float scale = CAP ? 1.f : p.scale;
+    const int step = p.even_pages ? kRowsW : 1;
+
 #pragma unroll
     for (int a = 0; a < NQ; ++a) {
-      m[a] = kNoScore;
+      m[a] = lim[a] < 0 ? 0.f : kNoScore;
       l[a] = 0.f;
 #pragma unroll
       for (int d = 0; d < kBlocks; ++d)
@@ -380,13 +426,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
         for (int i = 0; i < 16; ++i) o[a][d][i] = 0.f;
     }
 
-    const int key_a = rec.key_begin + done * C::kKeys;
-    const int key_b = min(rec.key_end, key_a + todo * C::kKeys);
-    const char* kbase = p.kv.k + 2 * (int64_t)hk * p.kv.hs;
-    const char* vbase = p.kv.v + 2 * (int64_t)hk * p.kv.hs;
-
     // as many tiles at a time as the staged places reach
-    const int step = p.even_pages ? kRowsW : 1;
     for (int a0 = key_a; a0 < key_b;) {
       const int a1 = (int)min((int64_t)key_b, a0 + (int64_t)C::kPlaces * step);
       const int count = (a1 - a0 + C::kKeys - 1) / C::kKeys;
@@ -400,13 +440,18 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
       // This wave's rows of a tile: one place when they lie in one page and are all there, otherwise
       // each lane's own (-1: past the end, zeros).  A tile's keys and, an iteration later, its values
       // go by the same places; `next` is read from LDS a tile ahead.
+      const int last_place = p.even_pages ? (a1 - a0 - 1) / C::kKeys : 0;
       bool one;
       int64_t at, next = places[wave];
       int64_t lane_at[kLoads][2];
+      auto advance = [&](int i) __attribute__((always_inline)) {
+        at = uniform64(next);
+        next = places[min(i + 1, last_place) * kWaves + wave];
+      };
       auto place = [&](int i) __attribute__((always_inline)) {
         const int key0 = a0 + i * C::kKeys + wave * kRowsW;
         one = p.even_pages && key0 + kRowsW <= a1;
-        at = uniform64(next);
+        advance(i);
         if (!one) {
 #pragma unroll
           for (int x = 0; x < 2 * kLoads; ++x) {
@@ -415,36 +460,37 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
             lane_at[x / 2][x & 1] = key0 + r < a1 ? to : -1;
           }
         }
-        next = places[min((i + 1) * kWaves + wave, C::kPlaces - 1)];
       };
-      // the placed tile's keys (or V: values) into the slot of tile i
-      auto load = [&](int i, bool V) __attribute__((always_inline)) {
+      // load x of the placed tile's keys (or V: values) into the slot of tile i, from one place
+      auto load_one = [&](int i, bool V, int x) __attribute__((always_inline)) {
         const uint32_t dst = lds_of(smem) + (V ? NSK * C::kSlotK + i % NSV * C::kSlotV : i % NSK * C::kSlotK) +
-                             wave * (kLoads * (V ? C::kBlockV : C::kBlockK));
+                             (wave * kLoads + x) * (V ? C::kBlockV : C::kBlockK);
+        dma16_at(dst, (V ? vbase : kbase) + at, V ? off_v[x] : off_k[x]);
+      };
+      auto load = [&](int i, bool V) __attribute__((always_inline)) {
         if (one) {
-          const char* base = (V ? vbase : kbase) + at;
-          if (V)
-            load_blocks<C::kBlockV>(dst, base, off_v);
-          else
-            load_blocks<C::kBlockK>(dst, base, off_k);
+#pragma unroll
+          for (int x = 0; x < kLoads; ++x) load_one(i, V, x);
         } else {
+          const uint32_t dst = lds_of(smem) + (V ? NSK * C::kSlotK + i % NSV * C::kSlotV : i % NSK * C::kSlotK);
 #pragma unroll
           for (int x = 0; x < kLoads; ++x) {
             const char* src = (V ? vbase : kbase) + lane_at[x][V] + (V ? piece_v : piece_k[x]);
-            dma16<false>(dst + x * (V ? C::kBlockV : C::kBlockK), lane_at[x][V] < 0 ? (const char*)&g_zero : src);
+            dma16<false>(dst + (wave * kLoads + x) * (V ? C::kBlockV : C::kBlockK),
+                         lane_at[x][V] < 0 ? (const char*)&g_zero : src);
           }
         }
       };
-      // tile i's values and the keys that its blocks read fragments of are in LDS, and every wave is
-      // done with what the loads that follow overwrite
+      // tile i's values and tile i + 1's keys are in LDS, and every wave is done with tile i - 1's values
+      // and keys
       auto arrive = [&]() __attribute__((always_inline)) {
         wait_vm<2 * kLoads>();
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
       };
 
-      // K fragments of block kb (32 keys) of tile i
+      // K fragments t0 .. t1 of block kb (32 keys) of tile i
       u32x4 kf[kSteps];
-      auto read_k = [&](int i, int kb) __attribute__((always_inline)) {
+      auto read_k = [&](int i, int kb, int t0, int t1) __attribute__((always_inline)) {
         uint32_t from[C::kTurnsK];
 #pragma unroll
         for (int t = 0; t < C::kTurnsK; ++t) {
@@ -453,154 +499,157 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
         }
 #pragma unroll
         for (int t = 0; t < kSteps; ++t)
-          kf[t] = *(lds_u32x4)(from[t % C::kTurnsK] + t / C::kTurnsK * (32 * C::kTurnsK) +
-                               kb * 32 / C::kLoadRows * C::kBlockK);
+          if (t >= t0 && t < t1)
+            kf[t] = *(lds_u32x4)(from[t % C::kTurnsK] + t / C::kTurnsK * (32 * C::kTurnsK) +
+                                 kb * 32 / C::kLoadRows * C::kBlockK);
       };
-      // V fragments of block kb of tile i: keys 16 t + 4 half + 0..3, and 8 more
+      // V fragments of half t of block kb of tile i: keys 16 t + 4 half + 0..3, and 8 more
       u32x2 vf[2][kBlocks][2];
-      auto read_v = [&](int i, int kb) __attribute__((always_inline)) {
+      auto read_v = [&](int i, int kb, int t) __attribute__((always_inline)) {
         uint32_t from = frag_v + i % NSV * C::kSlotV;
         asm("" : "+v"(from));
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int d = 0; d < kBlocks; ++d)
 #pragma unroll
-          for (int d = 0; d < kBlocks; ++d)
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-              vf[t][d][x] = __builtin_bit_cast(
-                  u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                             (lds_s16x4)(from + (kb * 32 + 16 * t + 8 * x) / C::kLoadRows * C::kBlockV +
-                                         d * (64 * C::kLoadRows))));
+          for (int x = 0; x < 2; ++x)
+            vf[t][d][x] = __builtin_bit_cast(
+                u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                           (lds_s16x4)(from + (kb * 32 + 16 * t + 8 * x) / C::kLoadRows * C::kBlockV +
+                                       d * (64 * C::kLoadRows))));
       };
       f32x16 s[NQ];
-      auto scores = [&]() __attribute__((always_inline)) {
-#pragma unroll
-        for (int a = 0; a < NQ; ++a)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) s[a][e] = 0.f;
-#pragma unroll
-        for (int t = 0; t < kSteps; ++t)
-#pragma unroll
-          for (int a = 0; a < NQ; ++a) s[a] = E::mfma(kf[t], q[a][t], s[a]);
-      };
-      // their masks
-      auto settle = [&](int i, int kb) __attribute__((always_inline)) {
-        const int key0 = a0 + i * C::kKeys + kb * 32;
-        if (key0 + 31 > min(all_lim, a1 - 1) || key0 < all_low) {
-          asm volatile("");  // a branch: as selects the masks would cost every block
-#pragma unroll
-          for (int a = 0; a < NQ; ++a) {
-            // this lane's keys: 4 half + 8 (e / 4) + e % 4
-            const int hi = min(lim[a], a1 - 1) - key0 - 4 * half, lo = low[a] - key0 - 4 * half;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int key = 8 * (e >> 2) + (e & 3);
-              if (key > hi || key < lo) s[a][e] = -INFINITY;
-              if (e % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // (the comparisons' masks would fill the scalar registers)
-            }
-          }
-        }
-      };
-      u32x4 pt[NQ][2], pw[NQ][2];
-      float sum[NQ];
-      const float scale = CAP ? 1.f : p.scale;
-      auto weights = [&](const f32x16 (&x)[NQ]) __attribute__((always_inline)) {
-        uint32_t over = 0;
-#pragma unroll
-        for (int a = 0; a < NQ; ++a)
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[a][e], scale, -m[a]));
-            const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[a][e + 1], scale, -m[a]));
-            sum[a] = e == 0 ? w0 + w1 : sum[a] + w0 + w1;
-            const uint32_t both = E::pack(w0, w1);
-            pw[a][e >> 3][(e >> 1) & 3] = both;
-            over |= both;
-          }
-        return over;
-      };
-      // New references, kUp above the rows' maxima, and the weights against them.
-      auto move = [&](const f32x16 (&x)[NQ]) __attribute__((always_inline)) {
-#pragma unroll
-        for (int a = 0; a < NQ; ++a) {
-          float top = -INFINITY;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) top = fmaxf(top, x[a][e]);
-          top = fmaxf(top, other_half(top)) * scale + E::kUp;
-          const float to = fmaxf(m[a], top), f = __builtin_amdgcn_exp2f(m[a] - to);
-          m[a] = to;
-          l[a] *= f;
-#pragma unroll
-          for (int d = 0; d < kBlocks; ++d)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[a][d][e] *= f;
-        }
-        weights(x);
-      };
-      auto product = [&]() __attribute__((always_inline)) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int d = 0; d < kBlocks; ++d) {
-            const u32x4 f{vf[t][d][0][0], vf[t][d][0][1], vf[t][d][1][0], vf[t][d][1][1]};
-#pragma unroll
-            for (int a = 0; a < NQ; ++a) o[a][d] = E::mfma(f, pt[a][t], o[a][d]);
-          }
-      };
-      // One block: its weights, and beside them the product of the block before and the scores of the
-      // block after.  The weights are formed against the reference so far.  A weight of 2 or more, a
-      // NaN or an infinity has the top bit of its exponent set, in either 16-bit type: one such and
-      // the wave takes new references, kUp above its rows' maxima, so that this happens again only
-      // for a score that exceeds them by kUp + 1.
-      auto block = [&](int i, int kb) __attribute__((always_inline)) {
-        f32x16 x[NQ];
-#pragma unroll
-        for (int a = 0; a < NQ; ++a) x[a] = s[a];
-        product();
-        read_v(i, kb);
-        scores();
-        read_k(i + (KB == 1 ? 2 : 1), kb);
-        const uint32_t over = weights(x);
-#pragma unroll
-        for (int t = 0; t < kSteps * NQ + 2 * kBlocks * NQ; ++t) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
-        }
-        if (__any((over & 0x40004000u) != 0)) move(x);
-#pragma unroll
-        for (int a = 0; a < NQ; ++a) {
-          l[a] += sum[a];
-#pragma unroll
-          for (int t = 0; t < 2; ++t) pt[a][t] = pw[a][t];
-        }
-        if constexpr (CAP) {
+      auto scores = [&](int t0, int t1) __attribute__((always_inline)) {
+        if (t0 == 0) {
 #pragma unroll
           for (int a = 0; a < NQ; ++a)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s[a][e] = score<true>(p, s[a][e]);
+            for (int e = 0; e < 16; ++e) s[a][e] = 0.f;
         }
-        settle(kb + 1 < KB ? i : i + 1, kb + 1 < KB ? kb + 1 : 0);
-      };
-
 #pragma unroll
-      for (int x = 0; x < C::kAhead; ++x) {
-        place(x);
-        load(x, false);
-        if (x < C::kAhead - 1) load(x, true);
-      }
-      wait_vm<4 * kLoads>();
-      asm volatile("s_barrier" ::: "memory");
-      read_k(0, 0);
-      scores();
-      read_k(KB == 1 ? 1 : 0, KB == 1 ? 0 : 1);
-      if constexpr (CAP) {
+        for (int t = 0; t < kSteps; ++t)
+          if (t >= t0 && t < t1) {
+#pragma unroll
+            for (int a = 0; a < NQ; ++a) s[a] = E::mfma(kf[t], q[a][t], s[a]);
+          }
+      };
+      // value e of row block a of the block of keys from key0: bounded, in units of 1 / scale, and
+      // (MASK) -inf where the row does not see the key; this lane's keys are 4 half + 8 (e / 4) + e % 4
+      auto seen = [&](int a, int e, int key0) __attribute__((always_inline)) {
+        const int key = key0 + 4 * half + 8 * (e >> 2) + (e & 3);
+        return key <= min(lim[a], a1 - 1) && key >= low[a];
+      };
+      auto value = [&](const f32x16 (&x)[NQ], int a, int e) __attribute__((always_inline)) {
+        return CAP ? score<true>(p, x[a][e]) : x[a][e];
+      };
+      u32x4 pt[NQ][2], pw[NQ][2];
+      float sum[NQ];
+      // weights of values v0 .. v1 of a lane's 16 NQ
+      auto weights = [&](auto mask, const f32x16 (&x)[NQ], int v0, int v1, int key0) __attribute__((always_inline)) {
 #pragma unroll
         for (int a = 0; a < NQ; ++a)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) s[a][e] = score<true>(p, s[a][e]);
+          for (int e = 0; e < 16; e += 2)
+            if (16 * a + e >= v0 && 16 * a + e < v1) {
+              float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(value(x, a, e), scale, -m[a]));
+              float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(value(x, a, e + 1), scale, -m[a]));
+              if constexpr (decltype(mask)::value) {
+                w0 = seen(a, e, key0) ? w0 : 0.f;
+                w1 = seen(a, e + 1, key0) ? w1 : 0.f;
+                if (e % 4 == 2) __builtin_amdgcn_sched_barrier(0);  // (the comparisons' masks would fill the scalar registers)
+              }
+              sum[a] = e == 0 ? w0 + w1 : sum[a] + w0 + w1;
+              pw[a][e >> 3][(e >> 1) & 3] = E::pack(w0, w1);
+            }
+      };
+      auto product = [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+        for (int d = 0; d < kBlocks; ++d) {
+          const u32x4 f{vf[t][d][0][0], vf[t][d][0][1], vf[t][d][1][0], vf[t][d][1][1]};
+#pragma unroll
+          for (int a = 0; a < NQ; ++a) o[a][d] = E::mfma(f, pt[a][t], o[a][d]);
+        }
+      };
+      // References for the rows that have none yet: the highest score that the row sees in the block of
+      // scores at hand, lowered weights kUp below 1 leaving room above.
+      auto refer = [&](const f32x16 (&x)[NQ], int key0) __attribute__((always_inline)) {
+        bool none = false;
+#pragma unroll
+        for (int a = 0; a < NQ; ++a) none = none || m[a] == kNoScore;
+        if (__any(none)) {
+#pragma unroll
+          for (int a = 0; a < NQ; ++a) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top = fmaxf(top, seen(a, e, key0) ? value(x, a, e) * scale : -INFINITY);
+            top = fmaxf(top, other_half(top));
+            if (m[a] == kNoScore && top > kNoScore) m[a] = top + E::kUp;
+          }
+        }
+      };
+
+      // One tile, block by block: the weights of a block, and beside them the product of the block
+      // before with V and the scores of the block after, in four parts that each take their share of
+      // the products, of the fragment reads for the next ones, of the weights and of the loads.
+      // `inner`: a tile that every row of the wave sees whole, as the next one, all there and from
+      // one place, so that nothing is asked inside it.
+      auto tile = [&](auto inner, int i) __attribute__((always_inline)) {
+        constexpr bool kInner = decltype(inner)::value;
+        // (the queries stay in accumulation registers, which the products read directly)
+#pragma unroll
+        for (int a = 0; a < NQ; ++a)
+#pragma unroll
+          for (int t = 0; t < kSteps; ++t) asm volatile("" : "+a"(q[a][t]));
+        arrive();
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          f32x16 x[NQ];
+#pragma unroll
+          for (int a = 0; a < NQ; ++a) x[a] = s[a];
+          const int ni = kb + 1 < KB ? i : i + 1, nkb = kb + 1 < KB ? kb + 1 : 0;
+          if constexpr (!kInner) refer(x, a0 + i * C::kKeys + kb * 32);
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            if (g < 2) {
+              product(g);
+              read_k(ni, nkb, g * kSteps / 2, (g + 1) * kSteps / 2);
+            } else {
+              scores((g - 2) * kSteps / 2, (g - 1) * kSteps / 2);
+              read_v(i, kb, g - 2);
+            }
+            weights(std::bool_constant<!kInner>(), x, g * 4 * NQ, (g + 1) * 4 * NQ, a0 + i * C::kKeys + kb * 32);
+            const int part = kb * 4 + g;
+            if constexpr (kInner) {
+              if (part == 2 * KB) advance(i + 3);
+#pragma unroll
+              for (int y = part * 2 * kLoads / (4 * KB); y < (part + 1) * 2 * kLoads / (4 * KB); ++y)
+                y < kLoads ? load_one(i + 2, true, y) : load_one(i + 3, false, y - kLoads);
+              __builtin_amdgcn_sched_barrier(0);
+            } else {
+              if (part == 0) load(i + 2, true);
+              if (part == 2 * KB) {
+                place(i + 3);
+                load(i + 3, false);
+              }
+            }
+          }
+#pragma unroll
+          for (int a = 0; a < NQ; ++a) {
+            l[a] += sum[a];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) pt[a][t] = pw[a][t];
+          }
+        }
+      };
+#pragma unroll
+      for (int x = 0; x < 3; ++x) {
+        place(x);
+        load(x, false);
+        if (x < 2) load(x, true);
       }
-      settle(0, 0);
+      wait_vm<4 * kLoads>();
+      asm volatile("s_barrier" ::: "memory");
+      read_k(0, 0, 0, kSteps);
+      scores(0, kSteps);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
 #pragma unroll
@@ -608,83 +657,200 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
 #pragma unroll
         for (int d = 0; d < kBlocks; ++d) vf[t][d][0] = vf[t][d][1] = u32x2{0u, 0u};
       }
-      // (the last block's "next" is a block of zeros, masked)
-      for (int i = 0; i < count; ++i) {
-        // (the queries stay in accumulation registers, which the products read directly)
-#pragma unroll
-        for (int a = 0; a < NQ; ++a)
-#pragma unroll
-          for (int t = 0; t < kSteps; ++t) asm volatile("" : "+a"(q[a][t]));
-        arrive();
-        load(i + C::kAhead - 1, true);
-        place(i + C::kAhead);
-        load(i + C::kAhead, false);
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) block(i, kb);
-      }
-      product();
+      refer(s, a0);
+      // Tiles inner0 .. inner1 are seen whole by every row of the wave, and every row has its reference
+      // (those that see the first block have it now, the others from the tile that `all_low` lies in);
+      // the loads they ask for are of whole tiles or of none.
+      const int full = (a1 - a0) / C::kKeys;
+      const int inner0 = all_low <= a0 ? 0 : min(count, (all_low - a0) / C::kKeys + 1);
+      const int inner1 = p.even_pages ? min(full < count ? full - 3 : full, (min(all_lim, a1 - 1) - a0 + 1) / C::kKeys) : 0;
+      int i = 0;
+      for (; i < inner0; ++i) tile(std::false_type(), i);
+      for (; i < inner1; ++i) tile(std::true_type(), i);
+      // (the scores after the last block are of zeros, and nobody's)
+      for (; i < count; ++i) tile(std::false_type(), i);
+      product(0);
+      product(1);
       wait_vm<0>();
       a0 = a1;
     }
 
     const bool whole = done == 0 && todo == tiles;
     const bool head = done > 0;  // a part that continues a run: slot 0, one that starts it: slot 1
-    const int64_t part = (2 * (int64_t)me + (head ? 0 : 1)) * p.part_rows;
+    const int64_t part = whole ? -1 : 2 * (int64_t)me + (head ? 0 : 1);
+    // a row whose weights overflowed, or whose outputs are not finite: the share is computed again
+
 #pragma unroll
     for (int a = 0; a < NQ; ++a) {
-      const float sum = l[a] + other_half(l[a]);
-      const int in_tile = wave * 32 * NQ + a * 32 + col;
-      const int row = rec.tile * C::kRows + in_tile;
-      const int tok = (int)div_by(row, p.group), g = row - tok * G;
-      if (tok >= n) continue;
-      if (whole) {
-        const bool none = lim[a] < low[a];
-        const float inv = none ? 0.f : 1.f / sum;
-        const int64_t h = (int64_t)hk * G + g;
-        u16* dst = (u16*)p.o.p + (int64_t)(tok0 + tok) * p.o.ts + h * p.o.hs;
+      l[a] += other_half(l[a]);
+      float z = 0.f;
 #pragma unroll
-        for (int d = 0; d < kBlocks; ++d)
+      for (int d = 0; d < kBlocks; ++d)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const f32x16& x = o[a][d];
-            *(u32x2*)(dst + 32 * d + 8 * i + 4 * half) = u32x2{E::pack(x[4 * i] * inv, x[4 * i + 1] * inv),
-                                                               E::pack(x[4 * i + 2] * inv, x[4 * i + 3] * inv)};
-          }
-        if (p.lse && half == 0)
-          p.lse[(int64_t)(tok0 + tok) * p.Hq + h] = none ? -INFINITY : (m[a] + __builtin_amdgcn_logf(sum)) * kLn2;
-      } else {
-        float* dst = p.part_o + (part + in_tile) * D;
-#pragma unroll
-        for (int d = 0; d < kBlocks; ++d)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const f32x16& x = o[a][d];
-            *(f32x4*)(dst + 32 * d + 8 * i + 4 * half) = f32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
-          }
-        if (half == 0) {
-          p.part_ml[(part + in_tile) * 2] = m[a];
-          p.part_ml[(part + in_tile) * 2 + 1] = sum;
-        }
-      }
+        for (int e = 0; e < 16; ++e) z = __builtin_fmaf(o[a][d][e], 0.f, z);
+      if (lim[a] >= 0) off = off || !(l[a] <= E::kHigh) || z != 0.f;
     }
+#pragma unroll
+    for (int a = 0; a < NQ; ++a)
+      store_rows<E, D>(p, rec, hk, tok0, n, wave * 32 * NQ + a * 32 + col, part, o[a], m[a], l[a], lim[a] < low[a]);
     if (!whole && !head) {
       left = true;
       if (tid == 0) {
         tail[0] = hk * num_tiles + ti;
-        tail[1] = (int)((u + (tiles - done) - 1) / share) - me + 1;
+        tail[1] = (int)((start + cost + tiles - 1) / share) - me + 1;
       }
     }
-    u += todo;
-    done += todo;
-    if (done == tiles) {
-      done = 0;
-      if (++ti == num_tiles) {
-        ti = 0;
-        ++hk;
-      }
+    }
+    if (start + cost + tiles >= end) break;
+    if (++ti == num_tiles) {
+      ti = 0;
+      ++hk;
     }
   }
   if (!left && tid == 0) tail[0] = -1;
+
+  // The share again, with care, where its references did not hold: scores that outgrew them by more
+  // than the weights can hold, or values that are not finite.  Here the reference follows the
+  // maximum, and a value that is not finite enters only the rows that see it, as itself: its places
+  // are taken out of the product with V and counted by products of zeros and ones.  Right for
+  // everything and two to three times slower.
+  if (!__syncthreads_or(off)) return;
+  char *sk = smem, *sv = smem + 32 * D * 2;
+  hk = uniform((int)(first / per_head));
+  ti = uniform(find_tile(p.before, num_tiles, cost, first - hk * per_head));
+#pragma unroll 1
+  for (;;) {
+    const TileRec rec = ((const TileRec*)p.tiles)[ti];
+    const int64_t start = hk * per_head + uniform64(p.before[ti]) + (int64_t)ti * cost;
+    const int tiles = uniform((int)(p.before[ti + 1] - p.before[ti]));
+    const int done = (int)max((int64_t)0, first - start - cost);
+    const int todo = (int)min((int64_t)tiles, end - start - cost) - done;
+    if (todo > 0) {
+    const int tok0 = p.cu[rec.b], n = p.cu[rec.b + 1] - tok0;
+    const int first_page = p.kv.ptr[rec.b], pages = p.kv.ptr[rec.b + 1] - first_page;
+    const int len = pages > 0 ? (pages - 1) * (int)p.kv.page.d + p.kv.lpl[rec.b] : 0, past = len - n;
+    const int key_a = rec.key_begin + done * C::kKeys;
+    const int key_b = min(rec.key_end, key_a + todo * C::kKeys);
+    const int64_t part = done == 0 && todo == tiles ? -1 : 2 * (int64_t)me + (done > 0 ? 0 : 1);
+#pragma unroll 1
+    for (int rows = 0; rows < C::kRows; rows += 32 * kWaves) {
+      const int row = rec.tile * C::kRows + rows + wave * 32 + col;
+      const int tok = (int)div_by(row, p.group), g = row - tok * G;
+      const bool real = tok < n;
+      const int lim = real ? (p.causal ? min(past + tok, len - 1) : len - 1) : -1;
+      const int low = real && p.window > 0 ? max(0, past + tok - p.window + 1) : 0;
+      const int64_t h = (int64_t)hk * G + (real ? g : 0);
+      u32x4 q[kSteps];
+#pragma unroll
+      for (int t = 0; t < kSteps; ++t)
+        q[t] = *(const u32x4*)((const u16*)p.q.p + (int64_t)(tok0 + (real ? tok : 0)) * p.q.ts + h * p.q.hs + 8 * half + 16 * t);
+      f32x16 o[kBlocks];
+#pragma unroll
+      for (int d = 0; d < kBlocks; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
+      float m = kNoScore, l = 0.f;
+#pragma unroll 1
+      for (int key0 = key_a; key0 < key_b; key0 += 32) {
+        __syncthreads();
+        for (int x = tid; x < 32 * D / 8; x += 64 * kWaves) {
+          const int r = x / (D / 8), c = x % (D / 8), key = key0 + r;
+          u32x4 wk{0u, 0u, 0u, 0u}, wv = wk;
+          if (key < key_b) {
+            const int pg = (int)div_by(key, p.kv.page);
+            const int64_t at = (int64_t)p.kv.idx[first_page + pg] * p.kv.ps + (int64_t)(key - pg * (int)p.kv.page.d) * p.kv.ts +
+                               hk * p.kv.hs + 8 * c;
+            wk = *(const u32x4*)((const u16*)p.kv.k + at);
+            wv = *(const u32x4*)((const u16*)p.kv.v + at);
+          }
+          *(u32x4*)(sk + k_at<D>(r, c)) = wk;
+          *(u32x4*)(sv + v_at<D>(r, c)) = wv;
+        }
+        __syncthreads();
+        f32x16 s;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] = 0.f;
+#pragma unroll
+        for (int t = 0; t < kSteps; ++t) s = E::mfma(*(const u32x4*)(sk + k_at<D>(col, 2 * t + half)), q[t], s);
+        // value e is of key 4 half + 8 (e / 4) + e % 4
+        auto seen = [&](int e) __attribute__((always_inline)) {
+          const int key = key0 + 4 * half + 8 * (e >> 2) + (e & 3);
+          return key <= min(lim, key_b - 1) && key >= low;
+        };
+        float top = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          s[e] = seen(e) ? score<CAP>(p, s[e]) : -INFINITY;
+          top = fmaxf(top, s[e]);
+        }
+        const float to = fmaxf(m, fmaxf(top, other_half(top))), f = __builtin_amdgcn_exp2f(m - to);
+        m = to;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < kBlocks; ++d)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[d][e] *= f;
+        u32x4 pt[2];
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          const float a = __builtin_amdgcn_exp2f(s[e] - m), b = __builtin_amdgcn_exp2f(s[e + 1] - m);
+          l += a + b;
+          pt[e >> 3][(e >> 1) & 3] = E::pack(a, b);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int d = 0; d < kBlocks; ++d) {
+            // keys 16 t + 4 half + 0..3, and 8 more
+            const int key = 16 * t + 4 * half + ((lane & 15) >> 2);
+            const int dim = 32 * d + 16 * ((lane >> 4) & 1) + 4 * (lane & 3), sub = (dim & 7) * 2;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(sv + v_at<D>(key, dim >> 3) + sub));
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(sv + v_at<D>(key + 8, dim >> 3) + sub));
+            const u32x2 wl = __builtin_bit_cast(u32x2, lo), wh = __builtin_bit_cast(u32x2, hi);
+            u32x4 vf{wl[0], wl[1], wh[0], wh[1]};
+            uint32_t odd = 0;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) odd |= (vf[x] & E::kExp) + E::kCarry;
+            if (__any((odd & 0x80008000u) != 0)) {
+              u32x4 ones, plus, minus;
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                ones[x] = (seen(8 * t + 2 * x) ? E::kOne : 0u) | (seen(8 * t + 2 * x + 1) ? E::kOne << 16 : 0u);
+                plus[x] = minus[x] = 0u;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  // an infinity, or a NaN (both signs: their sum is NaN)
+                  const uint32_t v = (vf[x] >> (16 * y)) & 0xffffu, big = E::kExp & 0x7fffu;
+                  if ((v & 0x7fffu) >= big) {
+                    if (v != (big | 0x8000u)) plus[x] |= E::kOne << (16 * y);
+                    if (v != big) minus[x] |= E::kOne << (16 * y);
+                    vf[x] &= y ? 0x0000ffffu : 0xffff0000u;
+                  }
+                }
+              }
+              f32x16 np, nm;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) np[e] = nm[e] = 0.f;
+              np = E::mfma(plus, ones, np);
+              nm = E::mfma(minus, ones, nm);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                o[d][e] += np[e] > 0.f ? INFINITY : 0.f;
+                o[d][e] += nm[e] > 0.f ? -INFINITY : 0.f;
+              }
+            }
+            o[d] = E::mfma(vf, pt[t], o[d]);
+          }
+      }
+      store_rows<E, D>(p, rec, hk, tok0, n, rows + wave * 32 + col, part, o, m, l + other_half(l), lim < low);
+    }
+    }
+    if (start + cost + tiles >= end) break;
+    if (++ti == num_tiles) {
+      ti = 0;
+      ++hk;
+    }
+  }
 }
 
 // Joins the parts of the tiles that cross shares: workgroup (w, y) takes kGroups
@@ -702,17 +868,23 @@ __global__ __launch_bounds__(256) void chunk_join_kernel(AttnParams p) {
   const int tok = (int)div_by(row, p.group), g = row - tok * (int)p.group.d;
   if (tok >= n) return;
   auto at = [&](int i) { return (int64_t)(i == 0 ? 2 * w + 1 : 2 * (w + i)) * p.part_rows + in_tile; };
+  // (a part without weights counts for nothing, whatever its reference)
   float top = kNoScore;
-  for (int i = 0; i < parts; ++i) top = fmaxf(top, p.part_ml[at(i) * 2]);
+#pragma unroll 8
+  for (int i = 0; i < parts; ++i) {
+    const float2 ml = *(const float2*)(p.part_ml + at(i) * 2);
+    top = ml.y != 0.f ? fmaxf(top, ml.x) : top;
+  }
   f32x4 acc{0.f, 0.f, 0.f, 0.f};
   float sum = 0.f;
+#pragma unroll 8
   for (int i = 0; i < parts; ++i) {
-    const float f = __builtin_amdgcn_exp2f(p.part_ml[at(i) * 2] - top);
-    sum += f * p.part_ml[at(i) * 2 + 1];
+    const float2 ml = *(const float2*)(p.part_ml + at(i) * 2);
+    const float f = ml.y != 0.f ? __builtin_amdgcn_exp2f(ml.x - top) : 0.f;
+    sum += f * ml.y;
     acc += f * *(const f32x4*)(p.part_o + at(i) * D + d);
   }
-  // a row that saw nothing in any part
-  const bool none = sum == 0.f;
+  const bool none = sum == 0.f;  // a row that saw nothing in any part
   acc *= none ? 0.f : 1.f / sum;
   const int64_t h = (int64_t)hk * p.group.d + g;
   *(u32x2*)((u16*)p.o.p + (int64_t)(tok0 + tok) * p.o.ts + h * p.o.hs + d) =
@@ -743,7 +915,7 @@ ChunkWs chunk_ws(int64_t T, int64_t B, int64_t G) {
   w.recs = take((w.tiles + 1) * sizeof(TileRec));
   w.before = take((w.tiles + 1) * sizeof(int64_t));
   w.seqs = take(B * sizeof(int));
-  w.count = take(sizeof(int));
+  w.count = take(2 * sizeof(int));
   w.parts = take(shares * 2 * sizeof(int));
   w.ml = take(2 * shares * w.part_rows * 2 * sizeof(float));
   w.o = take(2 * shares * w.part_rows * D * sizeof(float));
@@ -766,7 +938,7 @@ hipError_t launch_chunk_cap(const AttnParams& p, hipStream_t s) {
   hipError_t e = allow_lds(chunk_kernel<E, D, CAP>, Chunk<D>::kLds, raised);
   if (e != hipSuccess) return e;
   const int shares = device_cus();
-  plan_kernel<<<dim3(1), dim3(1024), 0, s>>>(p, Chunk<D>::kRows, Chunk<D>::kKeys);
+  plan_kernel<<<dim3(1), dim3(1024), 0, s>>>(p, Chunk<D>::kRows, Chunk<D>::kKeys, shares);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   chunk_kernel<E, D, CAP><<<dim3(shares), dim3(64 * kWaves), Chunk<D>::kLds, s>>>(p);
   if ((e = hipGetLastError()) != hipSuccess) return e;
