@@ -1025,13 +1025,17 @@ struct Span {
   int first_page, len, begin;
 };
 __device__ __forceinline__ Span dec_span(const AttnParams& p, int b) {
-  const int f = p.kv.ptr[b], pages = p.kv.ptr[b + 1] - f;
-  const int len = pages > 0 ? (pages - 1) * (int)p.kv.page.d + p.kv.lpl[b] : 0;
+  const int f = p.kv.ptr[b], e = p.kv.ptr[b + 1], last = p.kv.lpl[b];
+  const int len = e > f ? (e - f - 1) * (int)p.kv.page.d + last : 0;
   return Span{f, len, p.window > 0 ? max(0, len - p.window) : 0};
 }
 // its 128-key tiles, counted from the one that holds `begin`
 __device__ __forceinline__ int dec_tiles(const Span& s) {
   return s.len <= s.begin ? 0 : (s.len + kDecTile - 1) / kDecTile - s.begin / kDecTile;
+}
+// a / b of units: 32 bits, but for a batch of 2^31 units and more
+__device__ __forceinline__ int64_t div_units(int64_t a, int64_t b) {
+  return (a | b) >> 31 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
 template <class E, int D, bool CAP>
@@ -1043,29 +1047,31 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
   constexpr int kSteps = D / 32, kBlocks = D / 16;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   __shared__ int page_ids[kDecPages];
-  __shared__ int s_where[3];
+  __shared__ int s_where[6];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, grp = lane >> 4, col = lane & 15;
   const int G = (int)p.group.d, vh = (G + kDecRows - 1) / kDecRows;  // row blocks of a kv-head
   const int heads = p.Hkv * vh, B = p.kv.B;
 
-  // sequences without a token: zeros
-  for (int b = blockIdx.x; b < B; b += gridDim.x)
-    if (dec_span(p, b).len <= 0) {
-      for (int x = tid; x < p.Hq * (D / 8); x += 64 * kWaves)
+  // this workgroup's share: units first .. end of the runs laid end to end
+  const int per = (B + 64 * kWaves - 1) / (64 * kWaves);
+  const int b0 = tid * per, b1 = min(B, b0 + per);
+  int mine = 0;
+  Span sp{0, 0, 0};
+  for (int b = b0; b < b1; ++b) {
+    sp = dec_span(p, b);
+    mine += dec_tiles(sp);
+    if (sp.len <= 0 && b % gridDim.x == blockIdx.x) {  // a sequence without a token: zeros
+      for (int x = 0; x < p.Hq * (D / 8); ++x)
         *(u32x4*)((u16*)p.o.p + (int64_t)b * p.o.ts + (int64_t)(x / (D / 8)) * p.o.hs + 8 * (x % (D / 8))) =
             u32x4{0u, 0u, 0u, 0u};
       if (p.lse)
-        for (int h = tid; h < p.Hq; h += 64 * kWaves) p.lse[(int64_t)b * p.Hq + h] = -INFINITY;
+        for (int h = 0; h < p.Hq; ++h) p.lse[(int64_t)b * p.Hq + h] = -INFINITY;
     }
-
-  // this workgroup's share: units first .. end of the runs laid end to end
-  const int per = (B + 64 * kWaves - 1) / (64 * kWaves);
-  int mine = 0;
-  for (int b = tid * per; b < min(B, (tid + 1) * per); ++b) mine += dec_tiles(dec_span(p, b));
+  }
   int total;
   const int before = block_exclusive_scan(mine, &total);
   const int64_t units = (int64_t)total * heads;
-  const int64_t share = (units + gridDim.x - 1) / gridDim.x;
+  const int64_t share = div_units(units + gridDim.x - 1, gridDim.x);
   const int64_t first = (int64_t)blockIdx.x * share, end = min(units, first + share);
   int* tail = p.parts + 2 * blockIdx.x;  // {item, parts} of the run this share leaves unfinished
   if (first >= end) {
@@ -1074,23 +1080,30 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
   }
   if (first >= (int64_t)before * heads && first < (int64_t)(before + mine) * heads) {
     int64_t at = (int64_t)before * heads;
-    int b = tid * per;
-    for (;; ++b) {
-      const int64_t n = (int64_t)dec_tiles(dec_span(p, b)) * heads;
-      if (first < at + n) break;
-      at += n;
-    }
+    int b = b0, n = mine;
+    if (per > 1)
+      for (;; ++b) {
+        sp = dec_span(p, b);
+        n = dec_tiles(sp);
+        if (first < at + (int64_t)n * heads) break;
+        at += (int64_t)n * heads;
+      }
+    const int h = (int)div_units(first - at, n);
     s_where[0] = b;
-    s_where[1] = (int)((first - at) / dec_tiles(dec_span(p, b)));
-    s_where[2] = (int)((first - at) % dec_tiles(dec_span(p, b)));
+    s_where[1] = h;
+    s_where[2] = (int)(first - at - (int64_t)h * n);
+    s_where[3] = sp.first_page;
+    s_where[4] = sp.len;
+    s_where[5] = sp.begin;
   }
   __syncthreads();
-  int b = s_where[0], h = s_where[1], t = s_where[2];
+  int b = s_where[0], h = s_where[1], t = s_where[2], known = b;
+  sp = Span{s_where[3], s_where[4], s_where[5]};
   bool left = false;  // an unfinished run
 
   char* ring = smem + wave * (2 * NS * kSlot);
   for (int64_t u = first; u < end;) {
-    const Span sp = dec_span(p, b);
+    if (b != known) sp = dec_span(p, known = b);
     const int tiles = dec_tiles(sp);
     if (tiles == 0) {
       ++b;
@@ -1113,7 +1126,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
     const int key_a = (sp.begin / kDecTile + t) * kDecTile;           // keys of this part
     const int key_b = min(sp.len, key_a + todo * kDecTile);
     const char* kbase = p.kv.k + 2 * (int64_t)hk * p.kv.hs;
-    const int64_t vdiff = p.kv.v - p.kv.k;
+    const char* vbase = p.kv.v + 2 * (int64_t)hk * p.kv.hs;
 
     // as many tiles at a time as the staged page ids reach
     for (int a0 = max(key_a, sp.begin); a0 < key_b;) {
@@ -1130,8 +1143,26 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
       const int start = a0 / kDecTile * kDecTile + wave * kDecKeys;   // this wave's first tile
       const int n = (a1 - a0 / kDecTile * kDecTile + kDecTile - 1) / kDecTile;
 
-      // values (V) or keys of tile i into their slot
-      auto load = [&](int i, bool V) {
+      // Where the rows lie that this lane loads of a tile, in bytes from the start of the kv-head (-1:
+      // not a key of this part, zeros): each lane of a half finds one row's place, and the others take
+      // it from there.
+      int64_t at[kLoads];
+      auto place = [&](int i) __attribute__((always_inline)) {
+        const int key = start + i * kDecTile + (lane & 31);
+        int64_t mine = -1;
+        if (key >= a0 && key < a1) {
+          const int pg = (int)div_by(key, p.kv.page);
+          mine = 2 * ((int64_t)page_ids[pg - page0] * p.kv.ps + (int64_t)(key - pg * (int)p.kv.page.d) * p.kv.ts);
+        }
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x) {
+          const int r = x * kRowsPerLoad + lane / (D / 8);
+          const uint32_t lo = __shfl((int)(uint32_t)mine, r, 64), hi = __shfl((int)(mine >> 32), r, 64);
+          at[x] = (int64_t)(((uint64_t)hi << 32) | lo);
+        }
+      };
+      // values (V) or keys of the placed tile into the slot of tile i
+      auto load = [&](int i, bool V) __attribute__((always_inline)) {
         const uint32_t dst = lds_of(ring + (V ? NS * kSlot : 0) + (i % NS) * kSlot);
 #pragma unroll
         for (int x = 0; x < kLoads; ++x) {
@@ -1139,18 +1170,13 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
           // the piece that belongs at this lane's place: the turning is its own inverse
           const int c = V ? (slot ^ (D == 64 ? ((r >> 1) & 1) << 2 : (r & 3) << 2))
                           : (slot ^ (D == 64 ? (r >> 1) & 7 : r & 15));
-          const int key = start + i * kDecTile + r;
-          const char* src = (const char*)&g_zero;
-          if (key >= a0 && key < a1 && i < n) {
-            const int pg = (int)div_by(key, p.kv.page);
-            src = kbase + 2 * ((int64_t)page_ids[pg - page0] * p.kv.ps + (int64_t)(key - pg * (int)p.kv.page.d) * p.kv.ts +
-                               8 * c) + (V ? vdiff : 0);
-          }
-          dma16<true>(dst + x * 1024, src);
+          const char* src = (V ? vbase : kbase) + at[x] + 16 * c;
+          dma16<true>(dst + x * 1024, at[x] < 0 ? (const char*)&g_zero : src);
         }
       };
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
+        place(i);
         load(i, false);
         load(i, true);
       }
@@ -1168,6 +1194,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
             s[kb] = mfma16<E>(*(const u32x4*)(sk + k_at<D>(kb * 16 + col, 4 * x + grp)), q[x], s[kb]);
         }
         wait_lds();
+        place(i + NS);
         load(i + NS, false);
         float x[8], top = -INFINITY;
         const int key = start + i * kDecTile + 4 * grp;
@@ -1222,8 +1249,10 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
     float* mo = (float*)smem;
     __syncthreads();
     __shared__ float ml[kWaves][kDecRows][2];
+    if (col < rows) {
 #pragma unroll
-    for (int d = 0; d < kBlocks; ++d) *(f32x4*)(mo + (wave * kDecRows + col) * D + 16 * d + 4 * grp) = o[d];
+      for (int d = 0; d < kBlocks; ++d) *(f32x4*)(mo + (wave * kDecRows + col) * D + 16 * d + 4 * grp) = o[d];
+    }
     if (grp == 0) {
       ml[wave][col][0] = m;
       ml[wave][col][1] = l;
@@ -1263,7 +1292,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
       left = true;
       if (tid == 0) {
         tail[0] = b * heads + h;
-        tail[1] = (int)((u + (tiles - t) - 1) / share) - (int)blockIdx.x + 1;
+        tail[1] = (int)div_units(u + (tiles - t) - 1, share) - (int)blockIdx.x + 1;
       }
     }
     u += todo;
