@@ -7,16 +7,32 @@ the tensors' device, on torch's current stream, and there is no fallback.
 
 from __future__ import annotations
 
+from functools import lru_cache
 from typing import Optional, Tuple
 
 import torch
 
 from ._lib import (GDN_INDEX_INT32, GDN_INDEX_INT64, _AttentionC, _CacheC, _check, _need, _RopeC, _RowsC,
-                   _ScalingC, _stream, _workspace, load)
+                   _ScalingC, _workspace, load)
+from ._lib import _stream as _stream_of_device
 
 # element types (GDN_TYPE_*)
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3}
+
+
+def _stream(dev: torch.device):
+    """torch's current stream on ``dev``: its handle alone, since at small sizes a
+    ``torch.cuda.Stream`` object would cost as much as the kernel."""
+    if dev.type != "cuda" or dev.index is None:
+        return _stream_of_device(dev)
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _dense(shape, dtype, dev):
+    """A new dense [tokens, heads, dim] tensor and its gdn_rows_t."""
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    return t, _RowsC(t.data_ptr(), shape[1] * shape[2], shape[2])
 
 
 def _dtype(t, name: str) -> int:
@@ -125,16 +141,18 @@ def rope(q, k, table, positions, interleaved: bool = False, transposed: bool = F
     if tuple(positions.shape) != (T,):
         raise ValueError(f"positions must be [{T}], got {tuple(positions.shape)}")
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
-    qo = _rows(q_out, "q_out", q.dtype, dev, Hq, T, D)
+        q_out, qo = _dense((T, Hq, D), q.dtype, dev)
+    else:
+        qo = _rows(q_out, "q_out", q.dtype, dev, Hq, T, D)
     kr = ko = None
     Hk = 0
     if k is not None:
         kr = _rows(k, "k", q.dtype, dev, None, T, D)
         Hk = k.shape[1]
         if k_out is None:
-            k_out = torch.empty((T, Hk, D), dtype=q.dtype, device=dev)
-        ko = _rows(k_out, "k_out", q.dtype, dev, Hk, T, D)
+            k_out, ko = _dense((T, Hk, D), q.dtype, dev)
+        else:
+            ko = _rows(k_out, "k_out", q.dtype, dev, Hk, T, D)
     _check(lib.gdn_rope(rp, code, D, Hq, Hk, T, positions.data_ptr(),
                         GDN_INDEX_INT64 if positions.dtype == torch.int64 else GDN_INDEX_INT32,
                         qr, kr, qo, ko, stream))
@@ -175,10 +193,18 @@ def kv_append_paged(k, v, cu_seqlens, k_cache, v_cache, page_indices, page_indpt
         qr = _rows(q, "q", k.dtype, dev, None, T, D)
         Hq = q.shape[1]
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=k.dtype, device=dev)
-        qo = _rows(q_out, "q_out", k.dtype, dev, Hq, T, D)
+            q_out, qo = _dense((T, Hq, D), k.dtype, dev)
+        else:
+            qo = _rows(q_out, "q_out", k.dtype, dev, Hq, T, D)
     _check(lib.gdn_kv_append_paged(rp, code, D, Hq, Hk, cu, T, kr, vr, cache, qr, qo, stream))
     return q_out
+
+
+@lru_cache(maxsize=256)
+def _workspace_size(total_tokens: int, num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                    device: int) -> int:
+    d = _AttentionC(num_q_heads, num_kv_heads, head_dim, 0, 0.0, 0.0, 0, 1)
+    return int(load().gdn_attention_workspace_size(d, total_tokens, num_seqs))
 
 
 def attention_workspace_size(total_tokens: int, num_seqs: int, num_q_heads: int, num_kv_heads: int,
@@ -199,10 +225,11 @@ def _attention(fn, q, cu_seqlens, k_cache, v_cache, page_indices, page_indptr, p
     d = _AttentionC(Hq, k_cache.shape[2], D, code, float(scale) if scale else 0.0,
                     float(softcap) if softcap else 0.0, int(window), bool(causal))
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
-    o = _rows(out, "out", q.dtype, dev, Hq, T, D)
+        out, o = _dense((T, Hq, D), q.dtype, dev)
+    else:
+        o = _rows(out, "out", q.dtype, dev, Hq, T, D)
     lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if return_lse else None
-    ws = _workspace(workspace, lib.gdn_attention_workspace_size(d, T, cache.num_seqs), dev)
+    ws = _workspace(workspace, _workspace_size(T, cache.num_seqs, Hq, k_cache.shape[2], D, dev.index), dev)
     tail = (cache, o, lse.data_ptr() if return_lse else None, ws.data_ptr(), ws.numel() * ws.element_size(),
             stream)
     if fn == "prefill":

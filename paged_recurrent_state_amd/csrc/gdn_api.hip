@@ -823,7 +823,7 @@ int run_attention(const gdn_attention_dims_t* dims, const gdn_rows_t* q, const i
   const double scale = dims->scale > 0.f ? dims->scale : 1.0 / std::sqrt((double)dims->head_dim);
   const double log2e = 1.4426950408889634074;
   if (dims->softcap > 0.f) {
-    p.scale = (float)(scale / dims->softcap);
+    p.scale = (float)(2.0 * log2e * scale / dims->softcap);
     p.cap = (float)(dims->softcap * log2e);
   } else {
     p.scale = (float)(scale * log2e);

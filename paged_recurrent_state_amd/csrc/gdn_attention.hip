@@ -131,18 +131,16 @@ __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)"
 
 __device__ const u32x4 g_zero = {0u, 0u, 0u, 0u};  // read in place of keys outside a run
 
-// tanh by one exponential: 1 - 2 / (e^{2y} + 1), within 2^-22 of it.
-__device__ __forceinline__ float tanh_of(float y) {
-  const float e = __builtin_amdgcn_exp2f(y * (2.f * kLog2e));
-  return 1.f - 2.f * __builtin_amdgcn_rcpf(e + 1.f);
+// How far a capped score lies under the cap, over twice the cap: with
+// p.scale = 2 log2(e) scale / softcap, tanh(y) = 1 - 2 / (e^{2y} + 1).
+__device__ __forceinline__ float under_cap(const AttnParams& p, float x) {
+  return __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x * p.scale) + 1.f);
 }
 
 // Score in log2 units.
 template <bool CAP>
 __device__ __forceinline__ float score(const AttnParams& p, float x) {
-  x *= p.scale;
-  if constexpr (CAP) x = p.cap * tanh_of(x);
-  return x;
+  return CAP ? __builtin_fmaf(under_cap(p, x), -2.f * p.cap, p.cap) : x * p.scale;
 }
 
 // ------------------------------------------------------------------ chunks
@@ -193,19 +191,33 @@ struct Chunk {
   static constexpr int kLds = kSlotsK * kSlotK + kSlotsV * kSlotV + kPlaces * 8;
 };
 
-// A tile of query rows (plan_kernel): sequence, place in it, keys it sees.
+// A tile of query rows: its first row in its sequence, the keys it sees, and the
+// sequence's new tokens, tokens and first page.
 struct TileRec {
-  int b, tile, key_begin, key_end;
+  int row0, key_begin, key_end, tok0, n, len, first_page, unused;
+};
+// What plan_kernel says of the list: tiles, what each costs besides its key tiles,
+// and what one kv-head costs in all.
+struct PlanHead {
+  int tiles, cost;
+  int64_t per_head;
+};
+// A tile that a share leaves unfinished: how many parts it has (0: none), its
+// first row, its sequence's first new token and their number, and its kv-head.
+struct Unfinished {
+  int parts, row0, tok0, n, hk, unused[3];
 };
 
 constexpr int kTileCost = 512;  // what starting and ending a tile costs, in keys
-constexpr int kMinShare = 2;  // key tiles of a share at least: fewer parts to join
+constexpr int kMinShare = 2;    // key tiles of a share at least: fewer parts to join
 
 // One workgroup: lists every sequence's tiles, and the running total of their key
 // tiles (of one kv-head), [tiles + 1].
 __global__ __launch_bounds__(1024) void plan_kernel(AttnParams p, int rows, int keys, int shares) {
+  __shared__ int few[1024];
   const int B = p.kv.B, G = (int)p.group.d;
   // tiles before each sequence
+  int* seq_before = B <= 1024 ? few : p.seq_before;
   const int per = (B + 1023) / 1024;
   const int b0 = min(B, (int)threadIdx.x * per), b1 = min(B, b0 + per);
   auto count = [&](int b) { return (int)(((int64_t)max(0, p.cu[b + 1] - p.cu[b]) * G + rows - 1) / rows); };
@@ -214,10 +226,9 @@ __global__ __launch_bounds__(1024) void plan_kernel(AttnParams p, int rows, int 
   int total;
   int at = block_exclusive_scan(mine, &total);
   for (int b = b0; b < b1; ++b) {
-    p.seq_before[b] = at;
-    at += count(b);
+    seq_before[b] = at;
+    if (b + 1 < b1) at += count(b);
   }
-  if (threadIdx.x == 0) p.num_tiles[0] = total;
   __syncthreads();
   int64_t run = 0;
   for (int i0 = 0; i0 < total; i0 += 1024) {
@@ -227,20 +238,22 @@ __global__ __launch_bounds__(1024) void plan_kernel(AttnParams p, int rows, int 
       int lo = 0, hi = B - 1;  // the last sequence with seq_before <= i has tile i
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (p.seq_before[mid] <= i)
+        if (seq_before[mid] <= i)
           lo = mid;
         else
           hi = mid - 1;
       }
-      const int tokens = p.cu[lo + 1] - p.cu[lo], pages = p.kv.ptr[lo + 1] - p.kv.ptr[lo];
-      const int len = pages > 0 ? (pages - 1) * (int)p.kv.page.d + p.kv.lpl[lo] : 0;
-      const int past = len - tokens;
-      TileRec r;
-      r.b = lo;
-      r.tile = i - p.seq_before[lo];
-      const int first = (int)div_by((uint32_t)r.tile * rows, p.group);
-      const int last = min(tokens - 1, (int)div_by((uint32_t)r.tile * rows + rows - 1, p.group));
-      r.key_end = p.causal ? max(0, min(past + last + 1, len)) : len;
+      TileRec r{};
+      const int pages_end = p.kv.ptr[lo + 1], last_len = p.kv.lpl[lo], tok1 = p.cu[lo + 1];
+      r.first_page = p.kv.ptr[lo];
+      r.tok0 = p.cu[lo];
+      r.n = tok1 - r.tok0;
+      r.len = pages_end > r.first_page ? (pages_end - r.first_page - 1) * (int)p.kv.page.d + last_len : 0;
+      r.row0 = (i - seq_before[lo]) * rows;
+      const int past = r.len - r.n;
+      const int first = (int)div_by((uint32_t)r.row0, p.group);
+      const int last = min(r.n - 1, (int)div_by((uint32_t)r.row0 + rows - 1, p.group));
+      r.key_end = p.causal ? max(0, min(past + last + 1, r.len)) : r.len;
       r.key_begin = p.window > 0 ? min(r.key_end, max(0, past + first - p.window + 1) / keys * keys) : 0;
       ((TileRec*)p.tiles)[i] = r;
       x = max(1, (r.key_end - r.key_begin + keys - 1) / keys);  // a tile without keys still writes its rows
@@ -253,7 +266,8 @@ __global__ __launch_bounds__(1024) void plan_kernel(AttnParams p, int rows, int 
   if (threadIdx.x == 0) {
     p.before[total] = run;
     // a tile costs as many key tiles more than it has, or less where shares are small
-    p.num_tiles[1] = (int)min((int64_t)(kTileCost / keys), run * p.Hkv / (4 * (int64_t)shares));
+    const int cost = (int)min((int64_t)(kTileCost / keys), run * p.Hkv / (4 * (int64_t)shares));
+    *(PlanHead*)p.head = PlanHead{total, cost, run + (int64_t)total * cost};
   }
 }
 
@@ -275,11 +289,11 @@ __device__ __forceinline__ int find_tile(const int64_t* before, int tiles, int c
 // A lane's column of output (row in_tile of the tile, half of its values): the
 // finished row, or, into part `part` >= 0, what the join needs.
 template <class E, int D>
-__device__ __forceinline__ void store_rows(const AttnParams& p, const TileRec& rec, int hk, int tok0, int n, int in_tile,
+__device__ __forceinline__ void store_rows(const AttnParams& p, const TileRec& rec, int hk, int in_tile,
                                            int64_t part, const f32x16 (&o)[D / 32], float m, float sum, bool none) {
-  const int half = (threadIdx.x & 63) >> 5, row = rec.tile * Chunk<D>::kRows + in_tile;
-  const int tok = (int)div_by(row, p.group), g = row - tok * (int)p.group.d;
-  if (tok >= n) return;
+  const int half = (threadIdx.x & 63) >> 5, row = rec.row0 + in_tile;
+  const int tok0 = rec.tok0, tok = (int)div_by(row, p.group), g = row - tok * (int)p.group.d;
+  if (tok >= rec.n) return;
   if (part < 0) {
     const float inv = none ? 0.f : 1.f / sum;
     const int64_t h = (int64_t)hk * p.group.d + g;
@@ -322,16 +336,17 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int G = (int)p.group.d;
 
-  const int num_tiles = uniform(p.num_tiles[0]), cost = uniform(p.num_tiles[1]);
-  const int64_t per_head = uniform64(p.before[num_tiles]) + (int64_t)num_tiles * cost, units = per_head * p.Hkv;
+  const PlanHead plan = *(const PlanHead*)p.head;
+  const int num_tiles = uniform(plan.tiles), cost = uniform(plan.cost);
+  const int64_t per_head = uniform64(plan.per_head), units = per_head * p.Hkv;
   const int64_t share = max((int64_t)kMinShare, (units + gridDim.x - 1) / gridDim.x);
   // neighbouring shares on one XCD (workgroup x runs on XCD x % 8)
   const int shares8 = gridDim.x >> 3;
   const int me = (gridDim.x & 7) ? blockIdx.x : (blockIdx.x & 7) * shares8 + (blockIdx.x >> 3);
   const int64_t first = (int64_t)me * share, end = min(units, first + share);
-  int* tail = p.parts + 2 * me;
+  Unfinished* tail = (Unfinished*)p.parts + me;
   if (first >= end) {
-    if (tid == 0) tail[0] = -1;
+    if (tid == 0) tail->parts = 0;
     return;
   }
   bool off = false;
@@ -363,24 +378,22 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
 
   for (;;) {
     TileRec rec = ((const TileRec*)p.tiles)[ti];
-    rec = TileRec{uniform(rec.b), uniform(rec.tile), uniform(rec.key_begin), uniform(rec.key_end)};
+    rec = TileRec{uniform(rec.row0), uniform(rec.key_begin), uniform(rec.key_end), uniform(rec.tok0),
+                  uniform(rec.n), uniform(rec.len), uniform(rec.first_page), 0};
     // this share's part of the tile's key tiles: from `done` on (those before are the share before's)
     const int64_t start = hk * per_head + uniform64(p.before[ti]) + (int64_t)ti * cost;
     const int tiles = uniform((int)(p.before[ti + 1] - p.before[ti]));
     const int done = (int)max((int64_t)0, first - start - cost);
     const int todo = (int)min((int64_t)tiles, end - start - cost) - done;
     if (todo > 0) {
-    const int tok0 = uniform(p.cu[rec.b]), n = uniform(p.cu[rec.b + 1]) - tok0;
-    const int first_page = uniform(p.kv.ptr[rec.b]), pages = uniform(p.kv.ptr[rec.b + 1]) - first_page;
-    const int len = pages > 0 ? (pages - 1) * (int)p.kv.page.d + uniform(p.kv.lpl[rec.b]) : 0;
-    const int past = len - n;
+    const int tok0 = rec.tok0, n = rec.n, first_page = rec.first_page, len = rec.len, past = len - n;
 
     // this lane's rows
     int lim[NQ], low[NQ];  // keys low .. lim
     u32x4 q[NQ][kSteps];
 #pragma unroll
     for (int a = 0; a < NQ; ++a) {
-      const int row = rec.tile * C::kRows + wave * 32 * NQ + a * 32 + col;
+      const int row = rec.row0 + wave * 32 * NQ + a * 32 + col;
       const int tok = (int)div_by(row, p.group), g = row - tok * G;
       const bool real = tok < n;
       lim[a] = real ? (p.causal ? min(past + tok, len - 1) : len - 1) : -1;
@@ -394,7 +407,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
     int all_lim = 0x7fffffff, all_low = 0;
 #pragma unroll
     for (int a = 0; a < NQ; ++a) {
-      const int row = rec.tile * C::kRows + wave * 32 * NQ + a * 32 + col;
+      const int row = rec.row0 + wave * 32 * NQ + a * 32 + col;
       if ((int)div_by(row, p.group) < n) all_lim = min(all_lim, lim[a]);
       all_low = max(all_low, low[a]);
     }
@@ -413,7 +426,6 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
 
     f32x16 o[NQ][kBlocks];
     float m[NQ], l[NQ];
-    const float scale = CAP ? 1.f : p.scale;
     const int step = p.even_pages ? kRowsW : 1;
 
 #pragma unroll
@@ -532,14 +544,13 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
             for (int a = 0; a < NQ; ++a) s[a] = E::mfma(kf[t], q[a][t], s[a]);
           }
       };
-      // value e of row block a of the block of keys from key0: bounded, in units of 1 / scale, and
-      // (MASK) -inf where the row does not see the key; this lane's keys are 4 half + 8 (e / 4) + e % 4
+      // whether row block a sees the key of value e in the block of keys from key0 (this lane's keys are
+      // 4 half + 8 (e / 4) + e % 4): span[a] keys from first[a] on
+      uint32_t span[NQ];
+#pragma unroll
+      for (int a = 0; a < NQ; ++a) span[a] = (uint32_t)max(0, min(lim[a], a1 - 1) + 1 - low[a]);
       auto seen = [&](int a, int e, int key0) __attribute__((always_inline)) {
-        const int key = key0 + 4 * half + 8 * (e >> 2) + (e & 3);
-        return key <= min(lim[a], a1 - 1) && key >= low[a];
-      };
-      auto value = [&](const f32x16 (&x)[NQ], int a, int e) __attribute__((always_inline)) {
-        return CAP ? score<true>(p, x[a][e]) : x[a][e];
+        return (uint32_t)(8 * (e >> 2) + (e & 3) + (key0 + 4 * half - low[a])) < span[a];
       };
       u32x4 pt[NQ][2], pw[NQ][2];
       float sum[NQ];
@@ -550,12 +561,17 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
 #pragma unroll
           for (int e = 0; e < 16; e += 2)
             if (16 * a + e >= v0 && 16 * a + e < v1) {
-              float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(value(x, a, e), scale, -m[a]));
-              float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(value(x, a, e + 1), scale, -m[a]));
+              float w0, w1;
+              if constexpr (CAP) {
+                w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(under_cap(p, x[a][e]), -2.f * p.cap, p.cap - m[a]));
+                w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(under_cap(p, x[a][e + 1]), -2.f * p.cap, p.cap - m[a]));
+              } else {
+                w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[a][e], p.scale, -m[a]));
+                w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[a][e + 1], p.scale, -m[a]));
+              }
               if constexpr (decltype(mask)::value) {
                 w0 = seen(a, e, key0) ? w0 : 0.f;
                 w1 = seen(a, e + 1, key0) ? w1 : 0.f;
-                if (e % 4 == 2) __builtin_amdgcn_sched_barrier(0);  // (the comparisons' masks would fill the scalar registers)
               }
               sum[a] = e == 0 ? w0 + w1 : sum[a] + w0 + w1;
               pw[a][e >> 3][(e >> 1) & 3] = E::pack(w0, w1);
@@ -580,7 +596,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
           for (int a = 0; a < NQ; ++a) {
             float top = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) top = fmaxf(top, seen(a, e, key0) ? value(x, a, e) * scale : -INFINITY);
+            for (int e = 0; e < 16; ++e) top = fmaxf(top, seen(a, e, key0) ? score<CAP>(p, x[a][e]) : -INFINITY);
             top = fmaxf(top, other_half(top));
             if (m[a] == kNoScore && top > kNoScore) m[a] = top + E::kUp;
           }
@@ -692,12 +708,11 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
     }
 #pragma unroll
     for (int a = 0; a < NQ; ++a)
-      store_rows<E, D>(p, rec, hk, tok0, n, wave * 32 * NQ + a * 32 + col, part, o[a], m[a], l[a], lim[a] < low[a]);
+      store_rows<E, D>(p, rec, hk, wave * 32 * NQ + a * 32 + col, part, o[a], m[a], l[a], lim[a] < low[a]);
     if (!whole && !head) {
       left = true;
       if (tid == 0) {
-        tail[0] = hk * num_tiles + ti;
-        tail[1] = (int)((start + cost + tiles - 1) / share) - me + 1;
+        *tail = Unfinished{(int)((start + cost + tiles - 1) / share) - me + 1, rec.row0, rec.tok0, rec.n, hk, {}};
       }
     }
     }
@@ -707,7 +722,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
       ++hk;
     }
   }
-  if (!left && tid == 0) tail[0] = -1;
+  if (!left && tid == 0) tail->parts = 0;
 
   // The share again, with care, where its references did not hold: scores that outgrew them by more
   // than the weights can hold, or values that are not finite.  Here the reference follows the
@@ -726,15 +741,13 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
     const int done = (int)max((int64_t)0, first - start - cost);
     const int todo = (int)min((int64_t)tiles, end - start - cost) - done;
     if (todo > 0) {
-    const int tok0 = p.cu[rec.b], n = p.cu[rec.b + 1] - tok0;
-    const int first_page = p.kv.ptr[rec.b], pages = p.kv.ptr[rec.b + 1] - first_page;
-    const int len = pages > 0 ? (pages - 1) * (int)p.kv.page.d + p.kv.lpl[rec.b] : 0, past = len - n;
+    const int tok0 = rec.tok0, n = rec.n, first_page = rec.first_page, len = rec.len, past = len - n;
     const int key_a = rec.key_begin + done * C::kKeys;
     const int key_b = min(rec.key_end, key_a + todo * C::kKeys);
     const int64_t part = done == 0 && todo == tiles ? -1 : 2 * (int64_t)me + (done > 0 ? 0 : 1);
 #pragma unroll 1
     for (int rows = 0; rows < C::kRows; rows += 32 * kWaves) {
-      const int row = rec.tile * C::kRows + rows + wave * 32 + col;
+      const int row = rec.row0 + rows + wave * 32 + col;
       const int tok = (int)div_by(row, p.group), g = row - tok * G;
       const bool real = tok < n;
       const int lim = real ? (p.causal ? min(past + tok, len - 1) : len - 1) : -1;
@@ -842,7 +855,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
             o[d] = E::mfma(vf, pt[t], o[d]);
           }
       }
-      store_rows<E, D>(p, rec, hk, tok0, n, rows + wave * 32 + col, part, o, m, l + other_half(l), lim < low);
+      store_rows<E, D>(p, rec, hk, rows + wave * 32 + col, part, o, m, l + other_half(l), lim < low);
     }
     }
     if (start + cost + tiles >= end) break;
@@ -860,37 +873,39 @@ template <class E, int D>
 __global__ __launch_bounds__(256) void chunk_join_kernel(AttnParams p) {
   constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
   const int w = blockIdx.x, d = 4 * (threadIdx.x % kLanes), in_tile = blockIdx.y * kGroups + threadIdx.x / kLanes;
-  const int item = p.parts[2 * w], parts = p.parts[2 * w + 1];
-  if (item < 0) return;
-  const int num_tiles = p.num_tiles[0], hk = item / num_tiles;
-  const TileRec rec = ((const TileRec*)p.tiles)[item - hk * num_tiles];
-  const int tok0 = p.cu[rec.b], n = p.cu[rec.b + 1] - tok0, row = rec.tile * Chunk<D>::kRows + in_tile;
-  const int tok = (int)div_by(row, p.group), g = row - tok * (int)p.group.d;
-  if (tok >= n) return;
-  auto at = [&](int i) { return (int64_t)(i == 0 ? 2 * w + 1 : 2 * (w + i)) * p.part_rows + in_tile; };
-  // (a part without weights counts for nothing, whatever its reference)
-  float top = kNoScore;
-#pragma unroll 8
-  for (int i = 0; i < parts; ++i) {
-    const float2 ml = *(const float2*)(p.part_ml + at(i) * 2);
-    top = ml.y != 0.f ? fmaxf(top, ml.x) : top;
-  }
+  const Unfinished u = ((const Unfinished*)p.parts)[w];
+  const int row = u.row0 + in_tile, tok = (int)div_by(row, p.group), g = row - tok * (int)p.group.d;
+  if (u.parts == 0 || tok >= u.n) return;
+  float top = kNoScore, sum = 0.f;
   f32x4 acc{0.f, 0.f, 0.f, 0.f};
-  float sum = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < parts; ++i) {
-    const float2 ml = *(const float2*)(p.part_ml + at(i) * 2);
-    const float f = ml.y != 0.f ? __builtin_amdgcn_exp2f(ml.x - top) : 0.f;
-    sum += f * ml.y;
-    acc += f * *(const f32x4*)(p.part_o + at(i) * D + d);
+  // four parts at a time, on the way together
+  for (int i0 = 0; i0 < u.parts; i0 += 4) {
+    float2 ml[4];
+    f32x4 o[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int i = min(i0 + x, u.parts - 1);
+      const int64_t at = (int64_t)(i == 0 ? 2 * w + 1 : 2 * (w + i)) * p.part_rows + in_tile;
+      ml[x] = *(const float2*)(p.part_ml + at * 2);
+      o[x] = *(const f32x4*)(p.part_o + at * D + d);
+      if (i0 + x >= u.parts) ml[x].y = 0.f;
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (ml[x].y != 0.f) {  // (a part without weights counts for nothing, whatever its reference)
+        const float to = fmaxf(top, ml[x].x), f = __builtin_amdgcn_exp2f(top - to), h = __builtin_amdgcn_exp2f(ml[x].x - to);
+        top = to;
+        sum = sum * f + ml[x].y * h;
+        acc = acc * f + o[x] * h;
+      }
   }
   const bool none = sum == 0.f;  // a row that saw nothing in any part
   acc *= none ? 0.f : 1.f / sum;
-  const int64_t h = (int64_t)hk * p.group.d + g;
-  *(u32x2*)((u16*)p.o.p + (int64_t)(tok0 + tok) * p.o.ts + h * p.o.hs + d) =
+  const int64_t h = (int64_t)u.hk * p.group.d + g;
+  *(u32x2*)((u16*)p.o.p + (int64_t)(u.tok0 + tok) * p.o.ts + h * p.o.hs + d) =
       u32x2{E::pack(acc[0], acc[1]), E::pack(acc[2], acc[3])};
   if (p.lse && d == 0)
-    p.lse[(int64_t)(tok0 + tok) * p.Hq + h] = none ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+    p.lse[(int64_t)(u.tok0 + tok) * p.Hq + h] = none ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
 size_t align16(size_t x) { return (x + 15) & ~size_t(15); }
@@ -915,8 +930,8 @@ ChunkWs chunk_ws(int64_t T, int64_t B, int64_t G) {
   w.recs = take((w.tiles + 1) * sizeof(TileRec));
   w.before = take((w.tiles + 1) * sizeof(int64_t));
   w.seqs = take(B * sizeof(int));
-  w.count = take(2 * sizeof(int));
-  w.parts = take(shares * 2 * sizeof(int));
+  w.count = take(sizeof(PlanHead));
+  w.parts = take(shares * sizeof(Unfinished));
   w.ml = take(2 * shares * w.part_rows * 2 * sizeof(float));
   w.o = take(2 * shares * w.part_rows * D * sizeof(float));
   w.total = at;
@@ -954,7 +969,7 @@ hipError_t launch_chunk(AttnParams p, void* workspace, hipStream_t s) {
   p.tiles = base + w.recs;
   p.before = (int64_t*)(base + w.before);
   p.seq_before = (int*)(base + w.seqs);
-  p.num_tiles = (int*)(base + w.count);
+  p.head = base + w.count;
   p.parts = (int*)(base + w.parts);
   p.part_ml = (float*)(base + w.ml);
   p.part_o = (float*)(base + w.o);

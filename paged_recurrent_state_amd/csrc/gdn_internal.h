@@ -229,19 +229,19 @@ struct AttnParams {
   FastDiv group;  // q-heads per kv-head
   int window;     // 0: none
   int causal;
-  float scale;    // of the raw scores, in log2 units (softcap: scale / softcap)
+  float scale;    // of the raw scores, in log2 units (softcap: 2 log2(e) scale / softcap)
   float cap;      // softcap in log2 units, 0: none
   // workspace: parts of the runs that are cut between workgroups
   float* part_o;   // [2 * shares][rows][D]
   float* part_ml;  // [2 * shares][rows][2]: reference and sum
-  int* parts;      // [shares][2]: the run a share leaves unfinished (-1: none), and its parts
-  int part_rows;   // chunks: rows of a part
-  int even_pages;  // chunks: every 16 keys from a multiple of 16 lie in one page
-  // chunks: the list of query tiles (plan_kernel)
-  void* tiles;
+  int* parts;      // the run each share leaves unfinished
+  // chunks
+  int part_rows;    // rows of a part
+  int even_pages;   // every 16 keys from a multiple of 16 lie in one page
+  void* tiles;      // the list of query tiles (plan_kernel)
   int64_t* before;  // [tiles + 1]: key tiles of the tiles before
-  int* seq_before;  // [B]: tiles before each sequence's
-  int* num_tiles;
+  int* seq_before;  // [B]: tiles before each sequence's (more than 1024 sequences)
+  void* head;       // PlanHead
 };
 hipError_t launch_attention(const AttnParams& p, int D, int dtype, void* workspace, hipStream_t s);
 size_t attention_bytes(int D, int64_t T, int64_t B, int64_t group);  // workspace of launch_attention

@@ -229,6 +229,58 @@ def test_infinite_values_in_seen_slots_reach_the_rows_that_see_them():
     assert torch.isfinite(rest).all()
 
 
+@pytest.mark.parametrize("D,dtype,window,cap", [(64, HF, 0, 0.0), (128, BF, 0, 0.0), (128, HF, 70, 0.0), (256, BF, 0, 20.0)])
+@pytest.mark.parametrize("past", [0, 700])
+def test_values_that_are_not_finite_reach_only_the_rows_that_see_them(D, dtype, window, cap, past):
+    """NaN and infinities among the values of new tokens: earlier rows of the same chunk do not see them,
+    later ones get the formula's value in their column (inf, -inf, or NaN where both meet)."""
+    n, Hk, G = 150, 2, 2
+    q, cu, c = case([n], [past], 16, Hk, G, D, dtype, 90 + D)
+    ref = oracle_of(q, cu, c, window=window, softcap=cap)
+    where = oatt.slots(c["page_indices"].tolist(), c["page_indptr"].tolist(), c["last_page_len"].tolist(), 16, 0)
+    bad = [(40, 0, 3, float("nan")), (41, 0, 9, float("inf")), (77, 0, 9, float("-inf")), (100, 1, D - 1, float("-inf")),
+           (149, 1, 0, float("inf"))]
+    for tok, h, d, x in bad:
+        c["v_cache"][where[past + tok][0], where[past + tok][1], h, d] = x
+    o, lse = run_prefill(q, cu, c, window=window, softcap=cap)
+    x = au.f64(o)
+    clean = np.ones(x.shape, dtype=bool)
+    for tok, h, d, v in bad:
+        last = n if not window else min(n, tok + window)
+        rows = slice(tok, last)
+        heads = slice(h * G, (h + 1) * G)
+        clean[rows, heads, d] = False
+        both = d == 9 and v == float("-inf")
+        got = x[rows, heads, d]
+        if np.isnan(v):
+            assert np.isnan(got).all()
+        elif both:
+            # tokens 41 and 77 meet in column 9: NaN where a row sees the two, -inf where only the second
+            two = 41 + window - tok if window else n
+            assert np.isnan(got[:max(two, 0)]).all() and np.isneginf(got[max(two, 0):]).all()
+        elif d == 9:
+            assert np.isposinf(got[:77 - tok]).all()
+        else:
+            assert (got == v).all()
+    eo, el = au.attention_bounds(ref, D, dtype, cap)
+    assert (np.abs(x - ref[0])[clean] <= eo[clean]).all()
+    assert (np.abs(au.f64(lse) - ref[1]) <= el).all()
+
+
+@pytest.mark.parametrize("D,dtype", [(64, HF), (128, BF), (128, HF), (256, BF)])
+@pytest.mark.parametrize("window", [0, 300])
+def test_scores_that_outgrow_the_first_block(D, dtype, window):
+    """One late key whose score lies far above all before it, in a row's own share and in another's."""
+    q, cu, c = case([60], [2000], 64, 1, 2, D, dtype, 95)
+    where = oatt.slots(c["page_indices"].tolist(), c["page_indptr"].tolist(), c["last_page_len"].tolist(), 64, 0)
+    q[:] = q[0, 0]
+    p, i = where[1990]
+    # |q|^2 is about D: a score of 16 sqrt(D), 128 to 256, against about 1 for the others
+    c["k_cache"][p, i, 0] = (q[0, 0].float() * 16).to(dtype)
+    o, lse = run_prefill(q, cu, c, window=window)
+    au.check_attention(o, lse, oracle_of(q, cu, c, window=window), D, dtype)
+
+
 def rows_of(ref, keep):
     return tuple(x[keep] for x in ref)
 
