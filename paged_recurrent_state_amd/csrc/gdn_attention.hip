@@ -370,8 +370,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
   // points at 4 values of key i / 4 and receives value i of four keys)
   uint32_t frag_k[C::kTurnsK];
 #pragma unroll
-  for (int t = 0; t < C::kTurnsK; ++t) frag_k[t] = lds_of(smem) + C::k_at(col, 2 * t + half);
-  const uint32_t frag_v = lds_of(smem) + NSK * C::kSlotK + 8 * (lane & 1) +
+  for (int t = 0; t < C::kTurnsK; ++t) frag_k[t] = C::k_at(col, 2 * t + half);
+  const uint32_t frag_v = 8 * (lane & 1) +
                           C::v_at(4 * half + ((lane & 15) >> 2), 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1));
 
   const uint32_t token_bytes = (uint32_t)(2 * p.kv.ts);
@@ -473,22 +473,20 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
           }
         }
       };
-      // load x of the placed tile's keys (or V: values) into the slot of tile i, from one place
-      auto load_one = [&](int i, bool V, int x) __attribute__((always_inline)) {
-        const uint32_t dst = lds_of(smem) + (V ? NSK * C::kSlotK + i % NSV * C::kSlotV : i % NSK * C::kSlotK) +
-                             (wave * kLoads + x) * (V ? C::kBlockV : C::kBlockK);
+      // load x of the placed tile's keys (or V: values) into a slot, from one place
+      auto load_one = [&](uint32_t slot, bool V, int x) __attribute__((always_inline)) {
+        const uint32_t dst = slot + (wave * kLoads + x) * (V ? C::kBlockV : C::kBlockK);
         dma16_at(dst, (V ? vbase : kbase) + at, V ? off_v[x] : off_k[x]);
       };
-      auto load = [&](int i, bool V) __attribute__((always_inline)) {
+      auto load = [&](uint32_t slot, bool V) __attribute__((always_inline)) {
         if (one) {
 #pragma unroll
-          for (int x = 0; x < kLoads; ++x) load_one(i, V, x);
+          for (int x = 0; x < kLoads; ++x) load_one(slot, V, x);
         } else {
-          const uint32_t dst = lds_of(smem) + (V ? NSK * C::kSlotK + i % NSV * C::kSlotV : i % NSK * C::kSlotK);
 #pragma unroll
           for (int x = 0; x < kLoads; ++x) {
             const char* src = (V ? vbase : kbase) + lane_at[x][V] + (V ? piece_v : piece_k[x]);
-            dma16<false>(dst + (wave * kLoads + x) * (V ? C::kBlockV : C::kBlockK),
+            dma16<false>(slot + (wave * kLoads + x) * (V ? C::kBlockV : C::kBlockK),
                          lane_at[x][V] < 0 ? (const char*)&g_zero : src);
           }
         }
@@ -500,13 +498,28 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
       };
 
-      // K fragments t0 .. t1 of block kb (32 keys) of tile i
+      // The slots of tile i's keys and values, of tile i + 1's keys, and those that tile i - 1 leaves free,
+      // as addresses in LDS.
+      const uint32_t keys0 = lds_of(smem), values0 = keys0 + NSK * C::kSlotK;
+      uint32_t k_now = keys0, k_next = keys0 + C::kSlotK, k_free = keys0 + (NSK - 1) * C::kSlotK;
+      uint32_t v_now = values0, v_free = values0 + (NSV - 1) * C::kSlotV;
+      auto turn = [&]() __attribute__((always_inline)) {
+        k_free = k_now;
+        k_now = k_next;
+        k_next = k_next == keys0 + (NSK - 1) * C::kSlotK ? keys0 : k_next + C::kSlotK;
+        v_free = v_now;
+        v_now = v_now == values0 + (NSV - 1) * C::kSlotV ? values0 : v_now + C::kSlotV;
+      };
+      // (where the keys go that tile i asks for, three tiles ahead)
+      auto k_ahead = [&]() __attribute__((always_inline)) { return NSK == 4 ? k_free : k_now; };
+
+      // K fragments t0 .. t1 of block kb (32 keys) of the tile in a slot
       u32x4 kf[kSteps];
-      auto read_k = [&](int i, int kb, int t0, int t1) __attribute__((always_inline)) {
+      auto read_k = [&](uint32_t slot, int kb, int t0, int t1) __attribute__((always_inline)) {
         uint32_t from[C::kTurnsK];
 #pragma unroll
         for (int t = 0; t < C::kTurnsK; ++t) {
-          from[t] = frag_k[t] + i % NSK * C::kSlotK;
+          from[t] = frag_k[t] + slot;
           asm("" : "+v"(from[t]));  // (so that the rest goes into the reads' immediates)
         }
 #pragma unroll
@@ -517,8 +530,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
       };
       // V fragments of half t of block kb of tile i: keys 16 t + 4 half + 0..3, and 8 more
       u32x2 vf[2][kBlocks][2];
-      auto read_v = [&](int i, int kb, int t) __attribute__((always_inline)) {
-        uint32_t from = frag_v + i % NSV * C::kSlotV;
+      auto read_v = [&](int kb, int t) __attribute__((always_inline)) {
+        uint32_t from = frag_v + v_now;
         asm("" : "+v"(from));
 #pragma unroll
         for (int d = 0; d < kBlocks; ++d)
@@ -621,16 +634,16 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
           f32x16 x[NQ];
 #pragma unroll
           for (int a = 0; a < NQ; ++a) x[a] = s[a];
-          const int ni = kb + 1 < KB ? i : i + 1, nkb = kb + 1 < KB ? kb + 1 : 0;
+          const int nkb = kb + 1 < KB ? kb + 1 : 0;
           if constexpr (!kInner) refer(x, a0 + i * C::kKeys + kb * 32);
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             if (g < 2) {
               product(g);
-              read_k(ni, nkb, g * kSteps / 2, (g + 1) * kSteps / 2);
+              read_k(nkb ? k_now : k_next, nkb, g * kSteps / 2, (g + 1) * kSteps / 2);
             } else {
               scores((g - 2) * kSteps / 2, (g - 1) * kSteps / 2);
-              read_v(i, kb, g - 2);
+              read_v(kb, g - 2);
             }
             weights(std::bool_constant<!kInner>(), x, g * 4 * NQ, (g + 1) * 4 * NQ, a0 + i * C::kKeys + kb * 32);
             const int part = kb * 4 + g;
@@ -638,13 +651,19 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
               if (part == 2 * KB) advance(i + 3);
 #pragma unroll
               for (int y = part * 2 * kLoads / (4 * KB); y < (part + 1) * 2 * kLoads / (4 * KB); ++y)
-                y < kLoads ? load_one(i + 2, true, y) : load_one(i + 3, false, y - kLoads);
+                y < kLoads ? load_one(v_free, true, y) : load_one(k_ahead(), false, y - kLoads);
+              // one product, then up to four vector operations, in turn
+#pragma unroll
+              for (int y = 0; y < kSteps * NQ / 2; ++y) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+              }
               __builtin_amdgcn_sched_barrier(0);
             } else {
-              if (part == 0) load(i + 2, true);
+              if (part == 0) load(v_free, true);
               if (part == 2 * KB) {
                 place(i + 3);
-                load(i + 3, false);
+                load(k_ahead(), false);
               }
             }
           }
@@ -655,16 +674,17 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
             for (int t = 0; t < 2; ++t) pt[a][t] = pw[a][t];
           }
         }
+        turn();
       };
 #pragma unroll
       for (int x = 0; x < 3; ++x) {
         place(x);
-        load(x, false);
-        if (x < 2) load(x, true);
+        load(keys0 + x * C::kSlotK, false);
+        if (x < 2) load(values0 + x * C::kSlotV, true);
       }
       wait_vm<4 * kLoads>();
       asm volatile("s_barrier" ::: "memory");
-      read_k(0, 0, 0, kSteps);
+      read_k(keys0, 0, 0, kSteps);
       scores(0, kSteps);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
