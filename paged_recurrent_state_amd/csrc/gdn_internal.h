@@ -241,7 +241,7 @@ struct AttnParams {
   void* tiles;      // the list of query tiles (plan_kernel)
   int64_t* before;  // [tiles + 1]: key tiles of the tiles before
   int* seq_before;  // [B]: tiles before each sequence's (more than 1024 sequences)
-  void* head;       // PlanHead
+  void* head;       // PlanHead; null: few tiles, every workgroup plans for itself
 };
 hipError_t launch_attention(const AttnParams& p, int D, int dtype, void* workspace, hipStream_t s);
 size_t attention_bytes(int D, int64_t T, int64_t B, int64_t group);  // workspace of launch_attention
