@@ -711,15 +711,16 @@ RowsDev rows_dev(const gdn_rows_t* r) {
   return r ? RowsDev{(char*)r->data, r->token_stride, r->head_stride} : RowsDev{nullptr, 0, 0};
 }
 
-// whether every row starts at a multiple of 16 bytes (a stride that only one
+// whether every row starts at a multiple of `bytes` (a stride that only one
 // token or head steps over does not matter)
-bool aligned16(const gdn_rows_t* r, int64_t tokens, int32_t heads, int size) {
-  return !r || ((uintptr_t)r->data % 16 == 0 && (tokens < 2 || r->token_stride * size % 16 == 0) &&
-                (heads < 2 || r->head_stride * size % 16 == 0));
+bool aligned(const gdn_rows_t* r, int64_t tokens, int32_t heads, int size, int bytes) {
+  return !r || ((uintptr_t)r->data % bytes == 0 && (tokens < 2 || r->token_stride * size % bytes == 0) &&
+                (heads < 2 || r->head_stride * size % bytes == 0));
 }
-bool aligned16(const gdn_kv_cache_t* c, int32_t heads, int size) {
-  return (uintptr_t)c->k % 16 == 0 && (uintptr_t)c->v % 16 == 0 && c->page_stride * size % 16 == 0 &&
-         (c->page_size < 2 || c->token_stride * size % 16 == 0) && (heads < 2 || c->head_stride * size % 16 == 0);
+bool aligned(const gdn_kv_cache_t* c, int32_t heads, int size, int bytes) {
+  return (uintptr_t)c->k % bytes == 0 && (uintptr_t)c->v % bytes == 0 && c->page_stride * size % bytes == 0 &&
+         (c->page_size < 2 || c->token_stride * size % bytes == 0) &&
+         (heads < 2 || c->head_stride * size % bytes == 0);
 }
 
 int check_rows(const gdn_rows_t* r, const char* name, int64_t tokens) {
@@ -765,9 +766,11 @@ int check_heads(int32_t head_dim, int32_t q, int32_t k) {
 
 int type_size(int32_t dtype) { return dtype == GDN_TYPE_F32 ? 4 : 2; }
 
-// 16-byte accesses: whole 8-value pieces with their pairs in one thread
-bool rope_vec(const RopeParams& p, const gdn_rope_t* r, int size) {
-  return p.D % 16 == 0 && (!r || (r->rot_dim % 16 == 0 && (uintptr_t)r->table % 16 == 0));
+// Whether pieces of `width` values can be taken: whole pairs in a thread, and the
+// table's pieces aligned (to 16 bytes at most).
+bool rope_pieces(const RopeParams& p, const gdn_rope_t* r, int width) {
+  return p.D % (2 * width) == 0 &&
+         (!r || (r->rot_dim % (2 * width) == 0 && (uintptr_t)r->table % std::min(16, 4 * width) == 0));
 }
 
 void set_rope(RopeParams& p, const gdn_rope_t* r) {
@@ -801,9 +804,9 @@ int run_attention(const gdn_attention_dims_t* dims, const gdn_rows_t* q, const i
   const int32_t group = dims->num_q_heads / dims->num_kv_heads;
   if (T * group >= (int64_t(1) << 31) - 4096)  // (32-bit row numbers, to the end of the last tile)
     return fail(GDN_EINVAL, "query rows of a kv-head (%lld) must stay below 2^31 - 4096", (long long)(T * group));
-  if (!aligned16(q, T, dims->num_q_heads, 2)) return fail(GDN_EINVAL, "rows of q must be 16-byte aligned");
-  if (!aligned16(out, T, dims->num_q_heads, 2)) return fail(GDN_EINVAL, "rows of out must be 16-byte aligned");
-  if (!aligned16(cache, dims->num_kv_heads, 2))
+  if (!aligned(q, T, dims->num_q_heads, 2, 16)) return fail(GDN_EINVAL, "rows of q must be 16-byte aligned");
+  if (!aligned(out, T, dims->num_q_heads, 2, 16)) return fail(GDN_EINVAL, "rows of out must be 16-byte aligned");
+  if (!aligned(cache, dims->num_kv_heads, 2, 16))
     return fail(GDN_EINVAL, "rows of the cache must be 16-byte aligned");
   const size_t need = gdn_attention_workspace_size(dims, T, cache->num_seqs);
   if (need > 0 && (!workspace || workspace_bytes < need))
@@ -898,10 +901,14 @@ int gdn_rope(const gdn_rope_t* rope, int32_t dtype, int32_t head_dim, int32_t nu
   p.pos64 = index_dtype == GDN_INDEX_INT64;
   p.kv.page = fast_div(1);
   const int sz = type_size(dtype);
-  bool vec = rope_vec(p, rope, sz);
-  if (num_q_heads) vec = vec && aligned16(q, num_tokens, num_q_heads, sz) && aligned16(q_out, num_tokens, num_q_heads, sz);
-  if (num_k_heads) vec = vec && aligned16(k, num_tokens, num_k_heads, sz) && aligned16(k_out, num_tokens, num_k_heads, sz);
-  if (int rc = launched(launch_rope(p, dtype, rope->interleaved != 0, vec, stream), "rotary kernel")) return rc;
+  auto fits = [&](int width) {
+    const int bytes = width * sz;  // 16 at most
+    return rope_pieces(p, rope, width) &&
+           (!num_q_heads || (aligned(q, num_tokens, num_q_heads, sz, bytes) && aligned(q_out, num_tokens, num_q_heads, sz, bytes))) &&
+           (!num_k_heads || (aligned(k, num_tokens, num_k_heads, sz, bytes) && aligned(k_out, num_tokens, num_k_heads, sz, bytes)));
+  };
+  const int width = sz == 2 && fits(8) ? 8 : fits(4) ? 4 : fits(2) ? 2 : 1;
+  if (int rc = launched(launch_rope(p, dtype, rope->interleaved != 0, width, stream), "rotary kernel")) return rc;
   return ok();
 }
 
@@ -940,10 +947,14 @@ int gdn_kv_append_paged(const gdn_rope_t* rope, int32_t dtype, int32_t head_dim,
   p.cu = cu_seqlens;
   p.kv = kv_dev(cache);
   const int sz = type_size(dtype);
-  bool vec = rope_vec(p, rope, sz) && aligned16(k, total_tokens, num_kv_heads, sz) &&
-             aligned16(v, total_tokens, num_kv_heads, sz) && aligned16(cache, num_kv_heads, sz);
-  if (q) vec = vec && aligned16(q, total_tokens, Hq, sz) && aligned16(q_out, total_tokens, Hq, sz);
-  if (int rc = launched(launch_rope(p, dtype, rope && rope->interleaved != 0, vec, stream), "append kernel")) return rc;
+  auto fits = [&](int width) {
+    const int bytes = width * sz;  // 16 at most
+    return rope_pieces(p, rope, width) && aligned(k, total_tokens, num_kv_heads, sz, bytes) &&
+           aligned(v, total_tokens, num_kv_heads, sz, bytes) && aligned(cache, num_kv_heads, sz, bytes) &&
+           (!q || (aligned(q, total_tokens, Hq, sz, bytes) && aligned(q_out, total_tokens, Hq, sz, bytes)));
+  };
+  const int width = sz == 2 && fits(8) ? 8 : fits(4) ? 4 : fits(2) ? 2 : 1;
+  if (int rc = launched(launch_rope(p, dtype, rope && rope->interleaved != 0, width, stream), "append kernel")) return rc;
   return ok();
 }
 

@@ -214,7 +214,8 @@ struct RopeParams {
   FastDiv heads;       // Hq + Hk + Hv
   FastDiv row_units;   // threads a row takes
 };
-hipError_t launch_rope(RopeParams p, int dtype, bool interleaved, bool vec, hipStream_t s);
+// width: values of a piece (8, 4, 2, or 1: one pair a thread)
+hipError_t launch_rope(RopeParams p, int dtype, bool interleaved, int width, hipStream_t s);
 hipError_t launch_rope_table(float* table, int64_t rows, int rot, double base, double factor, int bands,
                              double original, double low, double high, double magnitude, hipStream_t s);
 

@@ -7,10 +7,12 @@
 // magnitude stays).  Every value is read once and written once, two products and
 // a sum each, so the kernel is bound by memory.
 //
-// A thread takes 16 values of a row, in two 16-byte (fp32: 32-byte) pieces that
-// hold eight whole pairs: values 8u .. and rot/2 + 8u .. of the half layout, 16
-// neighbours otherwise, so no value moves between lanes.  Rows whose sizes,
-// strides or addresses do not allow 16-byte accesses take one pair a thread.
+// A thread takes 2 W values of a row, in two pieces: values W u .. and rot/2 + W u
+// .., which hold W whole pairs in either layout (pairs across the two, or W / 2
+// within each), so no value moves between lanes and neighbouring threads take
+// neighbouring pieces.  A piece is 16 bytes, or less where the sizes, strides or
+// addresses allow no more (heads of 80 values of which 20 turn: W = 2), or one pair
+// a thread.
 // A workgroup takes as many tokens as keep its threads busy; their places in the
 // page table are looked up once per token, by one lane each.
 #include <algorithm>
@@ -20,8 +22,6 @@
 namespace gdn {
 
 namespace {
-
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 struct Bf16 {
   typedef u16 type;
@@ -40,27 +40,11 @@ __device__ __forceinline__ void from_f(float x, u16& y) { y = f2bf(x); }
 __device__ __forceinline__ void from_f(float x, _Float16& y) { y = (_Float16)x; }
 __device__ __forceinline__ void from_f(float x, float& y) { y = x; }
 
-__device__ __forceinline__ void load8(const u16* p, float (&x)[8]) {
-  const u32x4 w = *(const u32x4*)p;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ void load8(const _Float16* p, float (&x)[8]) {
-  const f16x8 w = *(const f16x8*)p;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = (float)w[i];
-}
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const f32x4 a = *(const f32x4*)p, b = *(const f32x4*)(p + 4);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[i] = a[i];
-    x[4 + i] = b[i];
-  }
-}
+// W values at once, 16 bytes at most.
+template <int W, typename E>
+struct Piece {
+  typedef E type __attribute__((ext_vector_type(W)));
+};
 template <bool NT, typename V>
 __device__ __forceinline__ void put(V* p, V w) {
   if constexpr (NT)
@@ -68,24 +52,22 @@ __device__ __forceinline__ void put(V* p, V w) {
   else
     *p = w;
 }
-template <bool NT>
-__device__ __forceinline__ void store8(u16* p, const float (&x)[8]) {
-  u32x4 w;
+template <int W, typename E>
+__device__ __forceinline__ void load(const E* p, float (&x)[W]) {
+  const typename Piece<W, E>::type w = *(const typename Piece<W, E>::type*)p;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = f2bf2(x[2 * i], x[2 * i + 1]);
-  put<NT>((u32x4*)p, w);
+  for (int i = 0; i < W; ++i) x[i] = to_f(w[i]);
 }
-template <bool NT>
-__device__ __forceinline__ void store8(_Float16* p, const float (&x)[8]) {
-  f16x8 w;
+template <bool NT, int W, typename E>
+__device__ __forceinline__ void store(E* p, const float (&x)[W]) {
+  typename Piece<W, E>::type w;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = (_Float16)x[i];
-  put<NT>((f16x8*)p, w);
-}
-template <bool NT>
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  put<NT>((f32x4*)p, f32x4{x[0], x[1], x[2], x[3]});
-  put<NT>((f32x4*)(p + 4), f32x4{x[4], x[5], x[6], x[7]});
+  for (int i = 0; i < W; ++i) {
+    E y;
+    from_f(x[i], y);
+    w[i] = y;
+  }
+  put<NT>((typename Piece<W, E>::type*)p, w);
 }
 
 // (a c - b s, b c + a s), one product of each rounded and the other fused, the
@@ -106,11 +88,12 @@ struct Place {
 };
 
 // Stores pass the caches (NT) when the call writes more than the L2s hold together:
-// 369 MB of prompts 74.4 -> 63.4 us, 688 MB of gradients 127.7 -> 123.8 us (5.6-5.8
-// TB/s, the rate of a copy); below that the next kernel may find them there.
+// 369 MB of prompts 74.4 -> 63.4 us, 688 MB of gradients 127.7 -> 123.8 us; below that
+// the next kernel may find them there.  With pieces that neighbouring threads take side
+// by side these are 56.2 and 114.3 us now (6.6 and 6.0 TB/s; a copy reaches 5.7-6.0).
 constexpr int64_t kCacheBytes = 32 << 20;
 
-template <class Tag, bool NEAR, bool VEC, bool NT>
+template <class Tag, bool NEAR, int W, bool NT>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeParams p) {
   typedef typename Tag::type E;
   __shared__ Place place[kRopeTokens];
@@ -183,37 +166,42 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeParams p) {
     }
     const bool known = pl.pos >= 0 && pl.pos < p.table_rows;
     const float* tab = p.table + (known ? pl.pos : 0) * rot;
-    if constexpr (VEC) {
-      int a = 16 * w, b = a + 8;
-      turn = turn && a < rot;
-      if (!NEAR && turn) {
-        a = 8 * w;
-        b = half + a;
-      }
-      float x[8], y[8];
-      load8(src + a, x);
-      load8(src + b, y);
+    if constexpr (W > 1) {
+      // the turned part, or what passes: two halves either way
+      const int turned = turn ? rot / (2 * W) : 0;
+      turn = w < turned;
+      const int a = W * (turn ? w : w + turned);
+      const int b = a + (turn ? half : (p.D >> 1) - W * turned);
+      float x[W], y[W];
+      load<W>(src + a, x);
+      load<W>(src + b, y);
       if (turn) {
-        float c[8], s[8];
-        load8(tab + 8 * w, c);
-        load8(tab + half + 8 * w, s);
+        // cosines and sines: of the pairs across the pieces, or of each one's own
+        constexpr int P = NEAR ? W / 2 : W;
+        float c[2][P], s[2][P];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (!known) c[i] = s[i] = __builtin_nanf("");
-          s[i] *= p.sign;
+        for (int k = 0; k < (NEAR ? 2 : 1); ++k) {
+          const float* t = tab + (NEAR ? (k ? b : a) / 2 : a);
+          load<P>(t, c[k]);
+          load<P>(t + half, s[k]);
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            if (!known) c[k][i] = s[k][i] = __builtin_nanf("");
+            s[k][i] *= p.sign;
+          }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (!NEAR)
-            turn_pair(x[i], y[i], c[i], s[i]);
-          else if (i < 4)
-            turn_pair(x[2 * i], x[2 * i + 1], c[i], s[i]);
-          else
-            turn_pair(y[2 * i - 8], y[2 * i - 7], c[i], s[i]);
+        for (int i = 0; i < P; ++i) {
+          if constexpr (NEAR) {
+            turn_pair(x[2 * i], x[2 * i + 1], c[0][i], s[0][i]);
+            turn_pair(y[2 * i], y[2 * i + 1], c[1][i], s[1][i]);
+          } else {
+            turn_pair(x[i], y[i], c[0][i], s[0][i]);
+          }
         }
       }
-      store8<NT>(dst + a, x);
-      store8<NT>(dst + b, y);
+      store<NT, W>(dst + a, x);
+      store<NT, W>(dst + b, y);
     } else if (turn && w < half) {
       const int a = NEAR ? 2 * w : w, b = NEAR ? a + 1 : a + half;
       const float c = known ? tab[w] : __builtin_nanf("");
@@ -261,30 +249,35 @@ __global__ __launch_bounds__(256) void rope_table_kernel(float* table, int64_t r
 }
 
 template <class Tag, bool NEAR>
-void launch_rope_type(const RopeParams& p, bool vec, bool nt, dim3 grid, hipStream_t s) {
+void launch_rope_type(const RopeParams& p, int width, bool nt, dim3 grid, hipStream_t s) {
   const dim3 blk(kRopeThreads);
-  if (!vec)
-    rope_kernel<Tag, NEAR, false, false><<<grid, blk, 0, s>>>(p);
-  else if (nt)
-    rope_kernel<Tag, NEAR, true, true><<<grid, blk, 0, s>>>(p);
+  constexpr int kMost = 16 / sizeof(typename Tag::type);  // 8, or 4 of fp32
+  if (width == kMost && nt)
+    rope_kernel<Tag, NEAR, kMost, true><<<grid, blk, 0, s>>>(p);
+  else if (width == kMost)
+    rope_kernel<Tag, NEAR, kMost, false><<<grid, blk, 0, s>>>(p);
+  else if (width == 4)
+    rope_kernel<Tag, NEAR, 4, false><<<grid, blk, 0, s>>>(p);
+  else if (width == 2)
+    rope_kernel<Tag, NEAR, 2, false><<<grid, blk, 0, s>>>(p);
   else
-    rope_kernel<Tag, NEAR, true, false><<<grid, blk, 0, s>>>(p);
+    rope_kernel<Tag, NEAR, 1, false><<<grid, blk, 0, s>>>(p);
 }
 template <class Tag>
-void launch_rope_type(const RopeParams& p, bool near_, bool vec, dim3 grid, hipStream_t s) {
+void launch_rope_type(const RopeParams& p, bool near_, int width, dim3 grid, hipStream_t s) {
   const bool nt = p.T * (p.Hq + p.Hk + p.Hv) * p.D * (int64_t)sizeof(typename Tag::type) > kCacheBytes;
   if (near_)
-    launch_rope_type<Tag, true>(p, vec, nt, grid, s);
+    launch_rope_type<Tag, true>(p, width, nt, grid, s);
   else
-    launch_rope_type<Tag, false>(p, vec, nt, grid, s);
+    launch_rope_type<Tag, false>(p, width, nt, grid, s);
 }
 
 }  // namespace
 
-hipError_t launch_rope(RopeParams p, int dtype, bool interleaved, bool vec, hipStream_t s) {
+hipError_t launch_rope(RopeParams p, int dtype, bool interleaved, int width, hipStream_t s) {
   const int H = p.Hq + p.Hk + p.Hv;
   if (p.T == 0 || H == 0) return hipSuccess;
-  const int units = vec ? p.D / 16 : p.D - p.rot / 2;
+  const int units = width > 1 ? p.D / (2 * width) : p.D - p.rot / 2;
   p.heads = fast_div(H);
   p.row_units = fast_div(units);
   // two rounds of the workgroup's threads
@@ -292,11 +285,11 @@ hipError_t launch_rope(RopeParams p, int dtype, bool interleaved, bool vec, hipS
   p.tokens_per_block = (int)std::max<int64_t>(1, std::min<int64_t>(kRopeTokens, 2 * kRopeThreads / per_token));
   const dim3 grid((uint32_t)((p.T + p.tokens_per_block - 1) / p.tokens_per_block));
   if (dtype == 0)
-    launch_rope_type<Bf16>(p, interleaved, vec, grid, s);
+    launch_rope_type<Bf16>(p, interleaved, width, grid, s);
   else if (dtype == 1)
-    launch_rope_type<Half>(p, interleaved, vec, grid, s);
+    launch_rope_type<Half>(p, interleaved, width, grid, s);
   else
-    launch_rope_type<Single>(p, interleaved, vec, grid, s);
+    launch_rope_type<Single>(p, interleaved, width, grid, s);
   return hipGetLastError();
 }
 

@@ -58,3 +58,41 @@ def test_large_append_equals_its_parts():
                                          lpl, table=tab, q=q[rows])
     torch.cuda.synchronize()
     assert torch.equal(one, two) and torch.equal(q1, q2)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,rot", [(80, 48), (48, 0), (64, 64)])
+@pytest.mark.parametrize("shift", [0, 1, 2, 4])
+def test_every_piece_width_gives_the_same_bits(dtype, interleaved, D, rot, shift):
+    """Rows that start 0, 1, 2 and 4 values after an aligned address take pieces of other widths
+    (rows of 81 values: one pair at a time); the values are those of aligned rows, bit by bit, and
+    nothing beside the rows is written."""
+    import paged_recurrent_state_amd as m
+    T, H, page = 21, 3, 8
+    cu, pages = au.i32([0, T], DEV), -(-T // page)
+    where = (torch.arange(pages, dtype=torch.int32, device=DEV), au.i32([0, pages], DEV), page,
+             au.i32([T - (pages - 1) * page], DEV))
+    tab = m.rope_table(T, rot) if rot else None
+    k, v = (au.queries(T, H, D, dtype, s, DEV) for s in (8, 9))
+    outs = []
+    for at, row in ((0, D), (shift, D + (shift == 1))):
+        def rows(n, x=None):
+            flat = torch.full((n * row + at + 5,), 7.0, dtype=dtype, device=DEV)
+            view = flat[at:at + n * row].view(-1, H, row)[..., :D]
+            if x is not None:
+                view.copy_(x)
+            return flat, view
+        slots = pages * page * H
+        (fk, ck), (fv, cv) = rows(slots), rows(slots)
+        (_, kk), (_, vv) = rows(T * H, k), rows(T * H, v)
+        m.kv_append_paged(kk, vv, cu, ck.unflatten(0, (pages, page)),
+                          cv.unflatten(0, (pages, page)), *where, table=tab, interleaved=interleaved)
+        torch.cuda.synchronize()
+        outs.append((ck[:T].clone(), cv[:T].clone()))
+        for flat, view in ((fk, ck), (fv, cv)):
+            assert (view[T:] == 7).all() and (flat[:at] == 7).all() and (flat[at + slots * row:] == 7).all()
+            if row > D:
+                assert (flat[at:at + slots * row].view(-1, row)[:, D:] == 7).all()
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    assert torch.equal(outs[0][1], v)
