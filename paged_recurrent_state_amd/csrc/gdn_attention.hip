@@ -191,7 +191,7 @@ struct Chunk {
   // A batch that may have more tiles than these is planned by a kernel of its own; otherwise every
   // workgroup lists them for itself, which saves the launch (17 tokens over 1,000: 26.3 -> 24.6 us).
   static constexpr int kFewTiles = 64 * kWaves;
-  static constexpr int kPlanLds = kFewTiles * (32 + 8 + 4) + 8;
+  static constexpr int kPlanLds = kFewTiles * (32 + 8 + 20) + 8;  // (TileRec, running totals, SeqRec)
   static constexpr int kLds = kPlanLds + kSlotsK * kSlotK + kSlotsV * kSlotV + kPlaces * 8;
 };
 
@@ -206,53 +206,60 @@ struct PlanHead {
   int tiles, cost;
   int64_t per_head;
 };
-// A tile that a share leaves unfinished: how many parts it has (0: none), its
-// first row, its sequence's first new token and their number, and its kv-head.
+// A sequence: tiles before its own, first new token and their number, first page,
+// and tokens.
+struct SeqRec {
+  int before, tok0, n, first_page, len;
+};
+// A tile that a share leaves unfinished: how many parts it has (0: none), the
+// share that starts it, its first row, its sequence's first new token and their
+// number, and its kv-head.
 struct Unfinished {
-  int parts, row0, tok0, n, hk, unused[3];
+  int parts, share, row0, tok0, n, hk, unused[2];
 };
 
 constexpr int kTileCost = 512;  // what starting and ending a tile costs, in keys
 constexpr int kMinShare = 2;    // key tiles of a share at least: fewer parts to join
 
+// a / b of units: 32 bits, but for a batch of 2^31 units and more
+__device__ __forceinline__ int64_t div_units(int64_t a, int64_t b) {
+  return (a | b) >> 31 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // One workgroup lists every sequence's tiles and the running total of their key
-// tiles (of one kv-head), [tiles + 1].  seq_before: room for B integers.
-__device__ __forceinline__ PlanHead make_plan(const AttnParams& p, int rows, int keys, int shares, int* seq_before,
+// tiles (of one kv-head), [tiles + 1].  seqs: room for B.
+__device__ __forceinline__ PlanHead make_plan(const AttnParams& p, int rows, int keys, int shares, SeqRec* seqs,
                                               TileRec* tiles, int64_t* before) {
   const int B = p.kv.B, G = (int)p.group.d, threads = blockDim.x;
   // tiles before each sequence
   const int per = (B + threads - 1) / threads;
   const int b0 = min(B, (int)threadIdx.x * per), b1 = min(B, b0 + per);
-  auto count = [&](int b) { return (int)(((int64_t)max(0, p.cu[b + 1] - p.cu[b]) * G + rows - 1) / rows); };
   int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += count(b);
-  int total;
-  int at = block_exclusive_scan(mine, &total);
   for (int b = b0; b < b1; ++b) {
-    seq_before[b] = at;
-    if (b + 1 < b1) at += count(b);
+    const int tok0 = p.cu[b], tok1 = p.cu[b + 1], f = p.kv.ptr[b], e = p.kv.ptr[b + 1], last = p.kv.lpl[b];
+    const int n = max(0, tok1 - tok0);
+    seqs[b] = SeqRec{mine, tok0, n, f, e > f ? (e - f - 1) * (int)p.kv.page.d + last : 0};
+    mine += (int)(((int64_t)n * G + rows - 1) / rows);
   }
+  int total;
+  const int at = block_exclusive_scan(mine, &total);
+  for (int b = b0; b < b1; ++b) seqs[b].before += at;
   __syncthreads();
   int64_t run = 0;
   for (int i0 = 0; i0 < total; i0 += threads) {
     const int i = i0 + (int)threadIdx.x;
     int x = 0;
     if (i < total) {
-      int lo = 0, hi = B - 1;  // the last sequence with seq_before <= i has tile i
+      int lo = 0, hi = B - 1;  // the last sequence that starts at tile i or before has it
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (seq_before[mid] <= i)
+        if (seqs[mid].before <= i)
           lo = mid;
         else
           hi = mid - 1;
       }
-      TileRec r{};
-      const int pages_end = p.kv.ptr[lo + 1], last_len = p.kv.lpl[lo], tok1 = p.cu[lo + 1];
-      r.first_page = p.kv.ptr[lo];
-      r.tok0 = p.cu[lo];
-      r.n = tok1 - r.tok0;
-      r.len = pages_end > r.first_page ? (pages_end - r.first_page - 1) * (int)p.kv.page.d + last_len : 0;
-      r.row0 = (i - seq_before[lo]) * rows;
+      const SeqRec q = seqs[lo];
+      TileRec r{(i - q.before) * rows, 0, 0, q.tok0, q.n, q.len, q.first_page, 0};
       const int past = r.len - r.n;
       const int first = (int)div_by((uint32_t)r.row0, p.group);
       const int last = min(r.n - 1, (int)div_by((uint32_t)r.row0 + rows - 1, p.group));
@@ -268,14 +275,14 @@ __device__ __forceinline__ PlanHead make_plan(const AttnParams& p, int rows, int
   }
   if (threadIdx.x == 0) before[total] = run;
   // a tile costs as many key tiles more than it has, or less where shares are small
-  const int cost = (int)min((int64_t)(kTileCost / keys), run * p.Hkv / (4 * (int64_t)shares));
+  const int cost = (int)min((int64_t)(kTileCost / keys), div_units(run * p.Hkv, 4 * (int64_t)shares));
   return PlanHead{total, cost, run + (int64_t)total * cost};
 }
 
 // The plan of a batch with more tiles than a workgroup lists by itself.
 __global__ __launch_bounds__(1024) void plan_kernel(AttnParams p, int rows, int keys, int shares) {
-  __shared__ int few[1024];
-  const PlanHead h = make_plan(p, rows, keys, shares, p.kv.B <= 1024 ? few : p.seq_before, (TileRec*)p.tiles, p.before);
+  __shared__ SeqRec few[1024];
+  const PlanHead h = make_plan(p, rows, keys, shares, p.kv.B <= 1024 ? few : (SeqRec*)p.seqs, (TileRec*)p.tiles, p.before);
   if (threadIdx.x == 0) *(PlanHead*)p.head = h;
 }
 
@@ -353,25 +360,29 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
   } else {
     TileRec* recs = (TileRec*)own_plan;
     int64_t* before = (int64_t*)(own_plan + C::kFewTiles * sizeof(TileRec));
-    plan = make_plan(p, C::kRows, C::kKeys, gridDim.x, (int*)(before + C::kFewTiles + 1), recs, before);
+    plan = make_plan(p, C::kRows, C::kKeys, gridDim.x, (SeqRec*)(before + C::kFewTiles + 1), recs, before);
     tile_recs = recs;
     tile_before = before;
     __syncthreads();
   }
   const int num_tiles = uniform(plan.tiles), cost = uniform(plan.cost);
   const int64_t per_head = uniform64(plan.per_head), units = per_head * p.Hkv;
-  const int64_t share = max((int64_t)kMinShare, (units + gridDim.x - 1) / gridDim.x);
+  const int64_t share = max((int64_t)kMinShare, div_units(units + gridDim.x - 1, gridDim.x));
   // neighbouring shares on one XCD (workgroup x runs on XCD x % 8)
   const int shares8 = gridDim.x >> 3;
   const int me = (gridDim.x & 7) ? blockIdx.x : (blockIdx.x & 7) * shares8 + (blockIdx.x >> 3);
   const int64_t first = (int64_t)me * share, end = min(units, first + share);
-  Unfinished* tail = (Unfinished*)p.parts + me;
-  if (first >= end) {
-    if (tid == 0) tail->parts = 0;
-    return;
+  // records of unfinished tiles: one a tile where the batch has few (p.records of them at most; those
+  // past the last tile say that there is none), one a share otherwise
+  Unfinished* records = (Unfinished*)p.parts;
+  if (p.records) {
+    if (tid == 0 && me < p.records && me >= num_tiles * p.Hkv) records[me].parts = 0;
+  } else if (first >= end && tid == 0) {
+    records[me].parts = 0;
   }
+  if (first >= end) return;
   bool off = false;
-  int hk = uniform((int)(first / per_head));
+  int hk = uniform((int)div_units(first, per_head));
   int ti = uniform(find_tile(tile_before, num_tiles, cost, first - hk * per_head));
   bool left = false;
 
@@ -750,11 +761,11 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
 #pragma unroll
     for (int a = 0; a < NQ; ++a)
       store_rows<E, D>(p, rec, hk, wave * 32 * NQ + a * 32 + col, part, o[a], m[a], l[a], lim[a] < low[a]);
-    if (!whole && !head) {
+    if (!head && (!whole || p.records)) {
       left = true;
-      if (tid == 0) {
-        *tail = Unfinished{(int)((start + cost + tiles - 1) / share) - me + 1, rec.row0, rec.tok0, rec.n, hk, {}};
-      }
+      const int parts = whole ? 0 : (int)div_units(start + cost + tiles - 1, share) - me + 1;
+      if (tid == 0)
+        records[p.records ? hk * num_tiles + ti : me] = Unfinished{parts, me, rec.row0, rec.tok0, rec.n, hk, {}};
     }
     }
     if (start + cost + tiles >= end) break;
@@ -763,7 +774,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
       ++hk;
     }
   }
-  if (!left && tid == 0) tail->parts = 0;
+  if (!left && !p.records && tid == 0) records[me].parts = 0;
 
   // The share again, with care, where its references did not hold: scores that outgrew them by more
   // than the weights can hold, or values that are not finite.  Here the reference follows the
@@ -772,7 +783,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
   // everything and two to three times slower.
   if (!__syncthreads_or(off)) return;
   char *sk = smem, *sv = smem + 32 * D * 2;
-  hk = uniform((int)(first / per_head));
+  hk = uniform((int)div_units(first, per_head));
   ti = uniform(find_tile(tile_before, num_tiles, cost, first - hk * per_head));
 #pragma unroll 1
   for (;;) {
@@ -907,15 +918,15 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
   }
 }
 
-// Joins the parts of the tiles that cross shares: workgroup (w, y) takes kGroups
-// rows of the tile that share w leaves unfinished; its parts are slot 1 of w and
-// slot 0 of the shares after it.
+// Joins the parts of the tiles that cross shares: workgroup (r, y) takes kGroups
+// rows of the tile of record r; its parts are slot 1 of the share that starts it
+// and slot 0 of the shares after that.
 template <class E, int D>
 __global__ __launch_bounds__(256) void chunk_join_kernel(AttnParams p) {
   constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
-  const int w = blockIdx.x, d = 4 * (threadIdx.x % kLanes), in_tile = blockIdx.y * kGroups + threadIdx.x / kLanes;
-  const Unfinished u = ((const Unfinished*)p.parts)[w];
-  const int row = u.row0 + in_tile, tok = (int)div_by(row, p.group), g = row - tok * (int)p.group.d;
+  const int d = 4 * (threadIdx.x % kLanes), in_tile = blockIdx.y * kGroups + threadIdx.x / kLanes;
+  const Unfinished u = ((const Unfinished*)p.parts)[blockIdx.x];
+  const int w = u.share, row = u.row0 + in_tile, tok = (int)div_by(row, p.group), g = row - tok * (int)p.group.d;
   if (u.parts == 0 || tok >= u.n) return;
   float top = kNoScore, sum = 0.f;
   f32x4 acc{0.f, 0.f, 0.f, 0.f};
@@ -970,7 +981,7 @@ ChunkWs chunk_ws(int64_t T, int64_t B, int64_t G) {
   };
   w.recs = take((w.tiles + 1) * sizeof(TileRec));
   w.before = take((w.tiles + 1) * sizeof(int64_t));
-  w.seqs = take(B * sizeof(int));
+  w.seqs = take(B * sizeof(SeqRec));
   w.count = take(sizeof(PlanHead));
   w.parts = take(shares * sizeof(Unfinished));
   w.ml = take(2 * shares * w.part_rows * 2 * sizeof(float));
@@ -1001,7 +1012,8 @@ hipError_t launch_chunk_cap(const AttnParams& p, hipStream_t s) {
   chunk_kernel<E, D, CAP><<<dim3(shares), dim3(64 * kWaves), Chunk<D>::kLds, s>>>(p);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int groups = 256 / (D / 4);
-  chunk_join_kernel<E, D><<<dim3(shares, (p.part_rows + groups - 1) / groups), dim3(256), 0, s>>>(p);
+  chunk_join_kernel<E, D><<<dim3(p.records ? p.records : shares, (p.part_rows + groups - 1) / groups), dim3(256), 0,
+                            s>>>(p);
   return hipGetLastError();
 }
 
@@ -1011,12 +1023,13 @@ hipError_t launch_chunk(AttnParams p, void* workspace, hipStream_t s) {
   char* base = (char*)workspace;
   p.tiles = base + w.recs;
   p.before = (int64_t*)(base + w.before);
-  p.seq_before = (int*)(base + w.seqs);
+  p.seqs = base + w.seqs;
   p.head = w.tiles > Chunk<D>::kFewTiles ? base + w.count : nullptr;
   p.parts = (int*)(base + w.parts);
   p.part_ml = (float*)(base + w.ml);
   p.part_o = (float*)(base + w.o);
   p.part_rows = (int)w.part_rows;
+  p.records = w.tiles * p.Hkv <= device_cus() ? (int)w.tiles * p.Hkv : 0;
   // a wave's rows of a tile start at a multiple of 16 (or 8) keys; their offsets in a page must fit
   // 32 bits
   p.even_pages = p.kv.page.d % 16 == 0 && p.kv.ts >= 0 && p.kv.ts * p.kv.page.d < (int64_t(1) << 30);
@@ -1091,11 +1104,6 @@ __device__ __forceinline__ Span dec_span(const AttnParams& p, int b) {
 __device__ __forceinline__ int dec_tiles(const Span& s) {
   return s.len <= s.begin ? 0 : (s.len + kDecTile - 1) / kDecTile - s.begin / kDecTile;
 }
-// a / b of units: 32 bits, but for a batch of 2^31 units and more
-__device__ __forceinline__ int64_t div_units(int64_t a, int64_t b) {
-  return (a | b) >> 31 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
-
 template <class E, int D, bool CAP>
 __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(AttnParams p) {
   constexpr int NS = kDecStages<D>;
@@ -1119,6 +1127,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
     sp = dec_span(p, b);
     mine += dec_tiles(sp);
     if (sp.len <= 0 && b % gridDim.x == blockIdx.x) {  // a sequence without a token: zeros
+      for (int h = 0; p.records && h < heads; ++h) p.parts[4 * (b * heads + h) + 2] = 0;
       for (int x = 0; x < p.Hq * (D / 8); ++x)
         *(u32x4*)((u16*)p.o.p + (int64_t)b * p.o.ts + (int64_t)(x / (D / 8)) * p.o.hs + 8 * (x % (D / 8))) =
             u32x4{0u, 0u, 0u, 0u};
@@ -1131,9 +1140,10 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
   const int64_t units = (int64_t)total * heads;
   const int64_t share = div_units(units + gridDim.x - 1, gridDim.x);
   const int64_t first = (int64_t)blockIdx.x * share, end = min(units, first + share);
-  int* tail = p.parts + 2 * blockIdx.x;  // {item, parts} of the run this share leaves unfinished
+  // records {item, its first share, parts} of unfinished runs (parts 0: none): one an item, a sequence's
+  // row block, where the batch has few, one a share otherwise
   if (first >= end) {
-    if (tid == 0) tail[0] = -1;
+    if (!p.records && tid == 0) p.parts[4 * blockIdx.x + 2] = 0;
     return;
   }
   if (first >= (int64_t)before * heads && first < (int64_t)(before + mine) * heads) {
@@ -1346,11 +1356,13 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
         }
       }
     }
-    if (!whole && !head) {
+    if (!head && (!whole || p.records)) {
       left = true;
       if (tid == 0) {
-        tail[0] = b * heads + h;
-        tail[1] = (int)div_units(u + (tiles - t) - 1, share) - (int)blockIdx.x + 1;
+        int* rec = p.parts + 4 * (p.records ? b * heads + h : blockIdx.x);
+        rec[0] = b * heads + h;
+        rec[1] = blockIdx.x;
+        rec[2] = whole ? 0 : (int)div_units(u + (tiles - t) - 1, share) - (int)blockIdx.x + 1;
       }
     }
     u += todo;
@@ -1364,18 +1376,19 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
     }
     __syncthreads();
   }
-  if (!left && tid == 0) tail[0] = -1;
+  if (!left && !p.records && tid == 0) p.parts[4 * blockIdx.x + 2] = 0;
 }
 
-// Joins the parts of the runs that cross shares: workgroup (w, r) takes row r of
-// the run that share w leaves unfinished; its parts are slot 1 of w and slot 0 of
-// the shares after it.
+// Joins the parts of the runs that cross shares: workgroup (x, r) takes row r of
+// the run of record x; its parts are slot 1 of the share that starts it and slot 0
+// of the shares after that.
 template <class E, int D>
 __global__ __launch_bounds__(256) void decode_join_kernel(AttnParams p) {
   constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
-  const int w = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, d = 4 * (tid % kLanes), g = tid / kLanes;
-  const int item = p.parts[2 * w], parts = p.parts[2 * w + 1];
-  if (item < 0) return;
+  const int r = blockIdx.y, tid = threadIdx.x, d = 4 * (tid % kLanes), g = tid / kLanes;
+  const int4 rec = ((const int4*)p.parts)[blockIdx.x];
+  const int item = rec.x, w = rec.y, parts = rec.z;
+  if (parts == 0) return;
   const int G = (int)p.group.d, vh = (G + kDecRows - 1) / kDecRows, heads = p.Hkv * vh;
   const int b = item / heads, h = item - b * heads, hk = h / vh, row0 = (h - hk * vh) * kDecRows;
   if (row0 + r >= G) return;
@@ -1426,7 +1439,7 @@ hipError_t launch_decode_cap(const AttnParams& p, hipStream_t s) {
   const int shares = decode_shares<D>();
   decode_kernel<E, D, CAP><<<dim3(shares), dim3(64 * kWaves), kDecLds<D>, s>>>(p);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  decode_join_kernel<E, D><<<dim3(shares, std::min<int>(kDecRows, (int)p.group.d)), dim3(256), 0, s>>>(p);
+  decode_join_kernel<E, D><<<dim3(p.records ? p.records : shares, std::min<int>(kDecRows, (int)p.group.d)), dim3(256), 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -1436,12 +1449,14 @@ hipError_t launch_dec(AttnParams p, void* workspace, hipStream_t s) {
   p.part_o = (float*)workspace;
   p.part_ml = p.part_o + (int64_t)2 * shares * kDecRows * D;
   p.parts = (int*)(p.part_ml + (int64_t)2 * shares * kDecRows * 2);
+  const int64_t items = (int64_t)p.kv.B * p.Hkv * ((p.group.d + kDecRows - 1) / kDecRows);
+  p.records = items <= shares ? (int)items : 0;
   return p.cap > 0.f ? launch_decode_cap<E, D, true>(p, s) : launch_decode_cap<E, D, false>(p, s);
 }
 
 template <int D>
 size_t decode_bytes() {
-  return (size_t)decode_shares<D>() * (2 * kDecRows * (D + 2) * sizeof(float) + 2 * sizeof(int));
+  return (size_t)decode_shares<D>() * (2 * kDecRows * (D + 2) * sizeof(float) + 4 * sizeof(int));
 }
 
 template <class E>

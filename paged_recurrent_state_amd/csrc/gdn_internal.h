@@ -235,13 +235,14 @@ struct AttnParams {
   // workspace: parts of the runs that are cut between workgroups
   float* part_o;   // [2 * shares][rows][D]
   float* part_ml;  // [2 * shares][rows][2]: reference and sum
-  int* parts;      // the run each share leaves unfinished
+  int* parts;      // records of runs that more than one share works on
+  int records;     // how many: one a run, in batches of few; 0: one a share
   // chunks
   int part_rows;    // rows of a part
   int even_pages;   // every 16 keys from a multiple of 16 lie in one page
   void* tiles;      // the list of query tiles (plan_kernel)
   int64_t* before;  // [tiles + 1]: key tiles of the tiles before
-  int* seq_before;  // [B]: tiles before each sequence's (more than 1024 sequences)
+  void* seqs;      // [B]: the sequences, when they are more than 1024
   void* head;       // PlanHead; null: few tiles, every workgroup plans for itself
 };
 hipError_t launch_attention(const AttnParams& p, int D, int dtype, void* workspace, hipStream_t s);
