@@ -1040,25 +1040,23 @@ hipError_t launch_chunk(AttnParams p, void* workspace, hipStream_t s) {
 //
 // One token per sequence: the G query rows of a kv-head against every key the
 // sequence holds.  Bound by reading the cache once, so the work is cut by bytes:
-// every (sequence, kv-head) is a run of 128-key tiles, the runs of the batch laid
-// end to end are cut into equal shares, one a workgroup, and a run that crosses
-// shares is joined afterwards from its parts' (m, l, o).
+// every (sequence, kv-head) is a run of 32-key tiles, the runs of the batch laid
+// end to end are cut into equal shares, one a wave, and a run that crosses shares
+// is joined afterwards from its parts' (m, l, o).
 //
-// The four waves of a workgroup take 32 of a tile's 128 keys each and never wait
-// for each other within a run: a wave loads its keys and values straight into
-// its own ring in LDS, and reads them once they have landed while the next are
-// on the way.  Products on 16x16x32 MFMAs in the same transposed form as above;
-// P enters as the sum of two 16-bit parts (the matrix units idle anyway), so
-// what it adds to the output's own rounding is invisible.
+// No wave waits for another: it loads its keys and values straight into its own
+// ring in LDS, and reads them once they have landed while the next are on the way.
+// Products on 16x16x32 MFMAs in the same transposed form as above; P enters as the
+// sum of two 16-bit parts (the matrix units idle anyway), so what it adds to the
+// output's own rounding is invisible.
 
-constexpr int kDecKeys = 32;                     // keys of a wave's tile
-constexpr int kDecTile = kDecKeys * kWaves;      // keys of a workgroup's tile
-constexpr int kDecRows = 16;                     // query rows of a workgroup
-constexpr int kDecPages = 1024;                  // page ids staged at a time
+constexpr int kDecTile = 32;   // keys of a tile
+constexpr int kDecRows = 16;   // query rows of a run
+constexpr int kDecPages = 512; // page ids a wave stages at a time
 template <int D>
 constexpr int kDecStages = D == 64 ? 2 : 1;      // tiles of keys (and of values) in a wave's ring
 template <int D>
-constexpr int kDecLds = kWaves * kDecStages<D> * 2 * kDecKeys * D * 2;
+constexpr int kDecLds = kWaves * kDecStages<D> * 2 * kDecTile * D * 2;
 
 template <class E>
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c);
@@ -1100,31 +1098,32 @@ __device__ __forceinline__ Span dec_span(const AttnParams& p, int b) {
   const int len = e > f ? (e - f - 1) * (int)p.kv.page.d + last : 0;
   return Span{f, len, p.window > 0 ? max(0, len - p.window) : 0};
 }
-// its 128-key tiles, counted from the one that holds `begin`
+// its tiles, counted from the one that holds `begin`
 __device__ __forceinline__ int dec_tiles(const Span& s) {
   return s.len <= s.begin ? 0 : (s.len + kDecTile - 1) / kDecTile - s.begin / kDecTile;
 }
 template <class E, int D, bool CAP>
 __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(AttnParams p) {
   constexpr int NS = kDecStages<D>;
-  constexpr int kSlot = kDecKeys * D * 2;     // bytes of 32 keys
-  constexpr int kLoads = kSlot / 1024;        // load instructions of 32 keys
+  constexpr int kSlot = kDecTile * D * 2;     // bytes of a tile's keys
+  constexpr int kLoads = kSlot / 1024;        // load instructions for them
   constexpr int kRowsPerLoad = 512 / D;
   constexpr int kSteps = D / 32, kBlocks = D / 16;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
-  __shared__ int page_ids[kDecPages];
-  __shared__ int s_where[6];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, grp = lane >> 4, col = lane & 15;
+  __shared__ int staged_ids[kWaves][kDecPages];
+  __shared__ int s_where[kWaves][3];
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), grp = lane >> 4, col = lane & 15;
   const int G = (int)p.group.d, vh = (G + kDecRows - 1) / kDecRows;  // row blocks of a kv-head
   const int heads = p.Hkv * vh, B = p.kv.B;
 
-  // this workgroup's share: units first .. end of the runs laid end to end
+  // this wave's share: units first .. end of the runs laid end to end
+  int* page_ids = staged_ids[wave];
+  const int me = blockIdx.x * kWaves + wave, shares = gridDim.x * kWaves;
   const int per = (B + 64 * kWaves - 1) / (64 * kWaves);
   const int b0 = tid * per, b1 = min(B, b0 + per);
   int mine = 0;
-  Span sp{0, 0, 0};
   for (int b = b0; b < b1; ++b) {
-    sp = dec_span(p, b);
+    const Span sp = dec_span(p, b);
     mine += dec_tiles(sp);
     if (sp.len <= 0 && b % gridDim.x == blockIdx.x) {  // a sequence without a token: zeros
       for (int h = 0; p.records && h < heads; ++h) p.parts[4 * (b * heads + h) + 2] = 0;
@@ -1138,40 +1137,47 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
   int total;
   const int before = block_exclusive_scan(mine, &total);
   const int64_t units = (int64_t)total * heads;
-  const int64_t share = div_units(units + gridDim.x - 1, gridDim.x);
-  const int64_t first = (int64_t)blockIdx.x * share, end = min(units, first + share);
+  const int64_t share = div_units(units + shares - 1, shares);
   // records {item, its first share, parts} of unfinished runs (parts 0: none): one an item, a sequence's
   // row block, where the batch has few, one a share otherwise
+  if (blockIdx.x * kWaves * share < units)
+    for (int w = 0; w < kWaves; ++w) {
+      const int64_t first = (blockIdx.x * kWaves + w) * share;
+      if (first >= (int64_t)before * heads && first < (int64_t)(before + mine) * heads) {
+        int64_t at = (int64_t)before * heads;
+        int b = b0, n = mine;
+        if (per > 1)
+          for (;; ++b) {
+            n = dec_tiles(dec_span(p, b));
+            if (first < at + (int64_t)n * heads) break;
+            at += (int64_t)n * heads;
+          }
+        const int h = (int)div_units(first - at, n);
+        s_where[w][0] = b;
+        s_where[w][1] = h;
+        s_where[w][2] = (int)(first - at - (int64_t)h * n);
+      }
+    }
+  __syncthreads();
+  const int64_t first = me * share, end = min(units, first + share);
   if (first >= end) {
-    if (!p.records && tid == 0) p.parts[4 * blockIdx.x + 2] = 0;
+    if (!p.records && lane == 0) p.parts[4 * me + 2] = 0;
     return;
   }
-  if (first >= (int64_t)before * heads && first < (int64_t)(before + mine) * heads) {
-    int64_t at = (int64_t)before * heads;
-    int b = b0, n = mine;
-    if (per > 1)
-      for (;; ++b) {
-        sp = dec_span(p, b);
-        n = dec_tiles(sp);
-        if (first < at + (int64_t)n * heads) break;
-        at += (int64_t)n * heads;
-      }
-    const int h = (int)div_units(first - at, n);
-    s_where[0] = b;
-    s_where[1] = h;
-    s_where[2] = (int)(first - at - (int64_t)h * n);
-    s_where[3] = sp.first_page;
-    s_where[4] = sp.len;
-    s_where[5] = sp.begin;
-  }
-  __syncthreads();
-  int b = s_where[0], h = s_where[1], t = s_where[2], known = b;
-  sp = Span{s_where[3], s_where[4], s_where[5]};
+  int b = uniform(s_where[wave][0]), h = uniform(s_where[wave][1]), t = uniform(s_where[wave][2]);
   bool left = false;  // an unfinished run
+  // the spans of 64 sequences from `base` on, one a lane
+  int base = b;
+  Span spans = dec_span(p, min(b + lane, B - 1));
 
   char* ring = smem + wave * (2 * NS * kSlot);
   for (int64_t u = first; u < end;) {
-    if (b != known) sp = dec_span(p, known = b);
+    if (b - base >= 64) {
+      base = b;
+      spans = dec_span(p, min(b + lane, B - 1));
+    }
+    const Span sp{uniform(__shfl(spans.first_page, b - base, 64)), uniform(__shfl(spans.len, b - base, 64)),
+                  uniform(__shfl(spans.begin, b - base, 64))};
     const int tiles = dec_tiles(sp);
     if (tiles == 0) {
       ++b;
@@ -1202,14 +1208,11 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
       const int64_t reach = (int64_t)(page0 + kDecPages) * p.kv.page.d;  // first key past the staged pages
       // (whole tiles; kDecPages pages are more than a tile's keys)
       const int a1 = reach >= key_b ? key_b : (int)reach / kDecTile * kDecTile;
-      __syncthreads();
-      {
-        const int last = (int)div_by(a1 - 1, p.kv.page);
-        for (int i = tid; i <= last - page0; i += 64 * kWaves) page_ids[i] = p.kv.idx[sp.first_page + page0 + i];
-      }
-      __syncthreads();
-      const int start = a0 / kDecTile * kDecTile + wave * kDecKeys;   // this wave's first tile
-      const int n = (a1 - a0 / kDecTile * kDecTile + kDecTile - 1) / kDecTile;
+      const int last = (int)div_by(a1 - 1, p.kv.page);
+      for (int i = lane; i <= last - page0; i += 64) page_ids[i] = p.kv.idx[sp.first_page + page0 + i];
+      wait_lds();
+      const int start = a0 / kDecTile * kDecTile;
+      const int n = (a1 - start + kDecTile - 1) / kDecTile;
 
       // Where the rows lie that this lane loads of a tile, in bytes from the start of the kv-head (-1:
       // not a key of this part, zeros): each lane of a half finds one row's place, and the others take
@@ -1311,58 +1314,33 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
       a0 = a1;
     }
 
-    // join the four waves
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
-    float* mo = (float*)smem;
-    __syncthreads();
-    __shared__ float ml[kWaves][kDecRows][2];
-    if (col < rows) {
-#pragma unroll
-      for (int d = 0; d < kBlocks; ++d) *(f32x4*)(mo + (wave * kDecRows + col) * D + 16 * d + 4 * grp) = o[d];
-    }
-    if (grp == 0) {
-      ml[wave][col][0] = m;
-      ml[wave][col][1] = l;
-    }
-    __syncthreads();
     const bool whole = t == 0 && todo == tiles;
     const bool head = t > 0;  // a part that continues a run: slot 0, one that starts it: slot 1
-    const int64_t slot = 2 * (int64_t)blockIdx.x + (head ? 0 : 1);
-    for (int x = tid; x < rows * (D / 4); x += 64 * kWaves) {
-      const int r = x / (D / 4), d = 4 * (x % (D / 4));
-      float top = ml[0][r][0];
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, ml[w][r][0]);
-      float sum = 0.f;
-      f32x4 acc{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const float f = __builtin_amdgcn_exp2f(ml[w][r][0] - top);
-        sum += f * ml[w][r][1];
-        acc += f * *(const f32x4*)(mo + (w * kDecRows + r) * D + d);
-      }
+    if (col < rows) {
       if (whole) {
-        const int64_t hq = (int64_t)hk * G + row0 + r;
-        acc *= 1.f / sum;
-        *(u32x2*)((u16*)p.o.p + (int64_t)b * p.o.ts + hq * p.o.hs + d) =
-            u32x2{E::pack(acc[0], acc[1]), E::pack(acc[2], acc[3])};
-        if (p.lse && d == 0) p.lse[(int64_t)b * p.Hq + hq] = (top + __builtin_amdgcn_logf(sum)) * kLn2;
+        const int64_t hq = (int64_t)hk * G + row0 + col;
+        const float inv = 1.f / l;
+        u16* dst = (u16*)p.o.p + (int64_t)b * p.o.ts + hq * p.o.hs + 4 * grp;
+#pragma unroll
+        for (int d = 0; d < kBlocks; ++d)
+          *(u32x2*)(dst + 16 * d) = u32x2{E::pack(o[d][0] * inv, o[d][1] * inv), E::pack(o[d][2] * inv, o[d][3] * inv)};
+        if (p.lse && grp == 0) p.lse[(int64_t)b * p.Hq + hq] = (m + __builtin_amdgcn_logf(l)) * kLn2;
       } else {
-        *(f32x4*)(p.part_o + (slot * kDecRows + r) * D + d) = acc;
-        if (d == 0) {
-          p.part_ml[(slot * kDecRows + r) * 2] = top;
-          p.part_ml[(slot * kDecRows + r) * 2 + 1] = sum;
-        }
+        const int64_t row = (2 * (int64_t)me + (head ? 0 : 1)) * kDecRows + col;
+#pragma unroll
+        for (int d = 0; d < kBlocks; ++d) *(f32x4*)(p.part_o + row * D + 16 * d + 4 * grp) = o[d];
+        if (grp == 0) *(float2*)(p.part_ml + row * 2) = float2{m, l};
       }
     }
     if (!head && (!whole || p.records)) {
       left = true;
-      if (tid == 0) {
-        int* rec = p.parts + 4 * (p.records ? b * heads + h : blockIdx.x);
+      if (lane == 0) {
+        int* rec = p.parts + 4 * (p.records ? b * heads + h : me);
         rec[0] = b * heads + h;
-        rec[1] = blockIdx.x;
-        rec[2] = whole ? 0 : (int)div_units(u + (tiles - t) - 1, share) - (int)blockIdx.x + 1;
+        rec[1] = me;
+        rec[2] = whole ? 0 : (int)div_units(u + (tiles - t) - 1, share) - me + 1;
       }
     }
     u += todo;
@@ -1374,61 +1352,85 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
         ++b;
       }
     }
-    __syncthreads();
   }
-  if (!left && !p.records && tid == 0) p.parts[4 * blockIdx.x + 2] = 0;
+  if (!left && !p.records && lane == 0) p.parts[4 * me + 2] = 0;
 }
 
-// Joins the parts of the runs that cross shares: workgroup (x, r) takes row r of
-// the run of record x; its parts are slot 1 of the share that starts it and slot 0
-// of the shares after that.
-template <class E, int D>
+// The join of some parts of a row: their reference, sum and output.
+struct Joined {
+  float top = kNoScore, sum = 0.f;
+  f32x4 acc{0.f, 0.f, 0.f, 0.f};
+  __device__ __forceinline__ void add(float m, float l, f32x4 o) {
+    if (l != 0.f) {  // (a part without weights counts for nothing, whatever its reference)
+      const float to = fmaxf(top, m), f = __builtin_amdgcn_exp2f(top - to), h = __builtin_amdgcn_exp2f(m - to);
+      top = to;
+      sum = sum * f + l * h;
+      acc = acc * f + o * h;
+    }
+  }
+};
+
+// Joins the parts of the runs that cross shares, of the run of record x; they are
+// slot 1 of the share that starts it and slot 0 of the shares after that.  Many
+// runs have few parts each: a group of D / 4 threads takes a row, a part after the
+// other.  FEW runs have up to hundreds: a workgroup takes 32 values of one row and
+// reads 128 parts at once (16 runs of about 100: 6.2 us, 15.6 with 32 at once).
+// Either way four parts of a thread are on the way together.
+template <class E, int D, bool FEW>
 __global__ __launch_bounds__(256) void decode_join_kernel(AttnParams p) {
-  constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
-  const int r = blockIdx.y, tid = threadIdx.x, d = 4 * (tid % kLanes), g = tid / kLanes;
+  constexpr int kLanes = FEW ? 8 : D / 4, kGroups = 256 / kLanes, kStep = FEW ? kGroups : 1;
+  const int tid = threadIdx.x, g = tid / kLanes, d = 4 * (blockIdx.z * kLanes + tid % kLanes);
+  const int r = FEW ? blockIdx.y : blockIdx.y * kGroups + g;
   const int4 rec = ((const int4*)p.parts)[blockIdx.x];
   const int item = rec.x, w = rec.y, parts = rec.z;
   if (parts == 0) return;
   const int G = (int)p.group.d, vh = (G + kDecRows - 1) / kDecRows, heads = p.Hkv * vh;
   const int b = item / heads, h = item - b * heads, hk = h / vh, row0 = (h - hk * vh) * kDecRows;
-  if (row0 + r >= G) return;
-  auto row = [&](int i) { return (int64_t)(i == 0 ? 2 * w + 1 : 2 * (w + i)) * kDecRows + r; };
-  __shared__ float red[256 / 64];
-  __shared__ f32x4 acc_s[256];
-  __shared__ float sum_s[256];
-  float top = kNoScore;
-  for (int i = tid; i < parts; i += 256) top = fmaxf(top, p.part_ml[row(i) * 2]);
+  if (row0 + r >= G || r >= kDecRows) return;
+  Joined a;
+  for (int i0 = FEW ? g : 0; i0 < parts; i0 += 4 * kStep) {
+    float2 ml[4];
+    f32x4 o[4];
 #pragma unroll
-  for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x, 64));
-  if ((tid & 63) == 0) red[tid >> 6] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  f32x4 acc{0.f, 0.f, 0.f, 0.f};
-  float sum = 0.f;
-  for (int i = g; i < parts; i += kGroups) {
-    const float f = __builtin_amdgcn_exp2f(p.part_ml[row(i) * 2] - top);
-    sum += f * p.part_ml[row(i) * 2 + 1];
-    acc += f * *(const f32x4*)(p.part_o + row(i) * D + d);
+    for (int x = 0; x < 4; ++x) {
+      const int i = min(i0 + x * kStep, parts - 1);
+      const int64_t row = (int64_t)(i == 0 ? 2 * w + 1 : 2 * (w + i)) * kDecRows + r;
+      ml[x] = *(const float2*)(p.part_ml + row * 2);
+      o[x] = *(const f32x4*)(p.part_o + row * D + d);
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (i0 + x * kStep < parts) a.add(ml[x].x, ml[x].y, o[x]);
   }
-  acc_s[tid] = acc;
-  sum_s[tid] = sum;
-  __syncthreads();
-  if (g) return;
-  for (int i = 1; i < kGroups; ++i) {
-    acc += acc_s[tid + i * kLanes];
-    sum += sum_s[tid + i * kLanes];
+  if constexpr (FEW) {
+    __shared__ f32x4 acc_s[kWaves][kLanes];
+    __shared__ float2 ml_s[kWaves][kLanes];
+#pragma unroll
+    for (int x = kLanes; x < 64; x <<= 1) {
+      f32x4 o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = __shfl_xor(a.acc[e], x, 64);
+      a.add(__shfl_xor(a.top, x, 64), __shfl_xor(a.sum, x, 64), o);
+    }
+    if ((tid & 63) < kLanes) {
+      acc_s[tid >> 6][tid & 63] = a.acc;
+      ml_s[tid >> 6][tid & 63] = float2{a.top, a.sum};
+    }
+    __syncthreads();
+    if (g) return;
+    for (int i = 1; i < kWaves; ++i) a.add(ml_s[i][tid].x, ml_s[i][tid].y, acc_s[i][tid]);
   }
-  acc *= 1.f / sum;
+  const f32x4 acc = a.acc * (1.f / a.sum);
   const int64_t hq = (int64_t)hk * G + row0 + r;
   *(u32x2*)((u16*)p.o.p + (int64_t)b * p.o.ts + hq * p.o.hs + d) =
       u32x2{E::pack(acc[0], acc[1]), E::pack(acc[2], acc[3])};
-  if (p.lse && d == 0) p.lse[(int64_t)b * p.Hq + hq] = (top + __builtin_amdgcn_logf(sum)) * kLn2;
+  if (p.lse && d == 0) p.lse[(int64_t)b * p.Hq + hq] = (a.top + __builtin_amdgcn_logf(a.sum)) * kLn2;
 }
 
-// Workgroups of a decode: as many as the compute units hold at once.
+// Waves of a decode: as many as the compute units hold at once.
 template <int D>
 int decode_shares() {
-  return device_cus() * (D == 256 ? 1 : 2);
+  return kWaves * device_cus() * (D == 256 ? 1 : 2);
 }
 
 template <class E, int D, bool CAP>
@@ -1437,9 +1439,14 @@ hipError_t launch_decode_cap(const AttnParams& p, hipStream_t s) {
   hipError_t e = allow_lds(decode_kernel<E, D, CAP>, kDecLds<D>, raised);
   if (e != hipSuccess) return e;
   const int shares = decode_shares<D>();
-  decode_kernel<E, D, CAP><<<dim3(shares), dim3(64 * kWaves), kDecLds<D>, s>>>(p);
+  decode_kernel<E, D, CAP><<<dim3(shares / kWaves), dim3(64 * kWaves), kDecLds<D>, s>>>(p);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  decode_join_kernel<E, D><<<dim3(p.records ? p.records : shares, std::min<int>(kDecRows, (int)p.group.d)), dim3(256), 0, s>>>(p);
+  const int rows = std::min<int>(kDecRows, (int)p.group.d), groups = 1024 / D;
+  if (p.records && 4 * p.records <= shares)
+    decode_join_kernel<E, D, true><<<dim3(p.records, rows, D / 32), dim3(256), 0, s>>>(p);
+  else
+    decode_join_kernel<E, D, false>
+        <<<dim3(p.records ? p.records : shares, (rows + groups - 1) / groups), dim3(256), 0, s>>>(p);
   return hipGetLastError();
 }
 
