@@ -335,7 +335,8 @@ __device__ __forceinline__ void store_rows(const AttnParams& p, const TileRec& r
   }
 }
 
-template <class E, int D, bool CAP>
+// EVEN: a wave's rows of a tile lie in one page (see launch_chunk).
+template <class E, int D, bool CAP, bool EVEN>
 __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
   typedef Chunk<D> C;
   constexpr int NQ = C::kNQ, NSK = C::kSlotsK, NSV = C::kSlotsV, KB = C::kKeys / 32;
@@ -458,7 +459,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
 
     f32x16 o[NQ][kBlocks];
     float m[NQ], l[NQ];
-    const int step = p.even_pages ? kRowsW : 1;
+    constexpr int step = EVEN ? kRowsW : 1;
 
 #pragma unroll
     for (int a = 0; a < NQ; ++a) {
@@ -484,7 +485,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
       // This wave's rows of a tile: one place when they lie in one page and are all there, otherwise
       // each lane's own (-1: past the end, zeros).  A tile's keys and, an iteration later, its values
       // go by the same places; `next` is read from LDS a tile ahead.
-      const int last_place = p.even_pages ? (a1 - a0 - 1) / C::kKeys : 0;
+      const int last_place = EVEN ? (a1 - a0 - 1) / C::kKeys : 0;
       bool one;
       int64_t at, next = places[wave];
       int64_t lane_at[kLoads][2];
@@ -494,13 +495,13 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
       };
       auto place = [&](int i) __attribute__((always_inline)) {
         const int key0 = a0 + i * C::kKeys + wave * kRowsW;
-        one = p.even_pages && key0 + kRowsW <= a1;
+        one = EVEN && key0 + kRowsW <= a1;
         advance(i);
         if (!one) {
 #pragma unroll
           for (int x = 0; x < 2 * kLoads; ++x) {
             const int r = x / 2 * C::kLoadRows + (x & 1 ? vr : kr);
-            const int64_t to = p.even_pages ? at + r * (int64_t)token_bytes : places[min(key0 + r, a1 - 1) - a0];
+            const int64_t to = EVEN ? at + r * (int64_t)token_bytes : places[min(key0 + r, a1 - 1) - a0];
             lane_at[x / 2][x & 1] = key0 + r < a1 ? to : -1;
           }
         }
@@ -521,6 +522,20 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
             dma16<false>(slot + (wave * kLoads + x) * (V ? C::kBlockV : C::kBlockK),
                          lane_at[x][V] < 0 ? (const char*)&g_zero : src);
           }
+        }
+      };
+      // The same inside the run, where pages end anywhere: every lane takes its row's place from LDS, a
+      // part before its load.
+      const int full = (a1 - a0) / C::kKeys;
+      constexpr int kAhead = (2 * kLoads + 4 * KB - 1) / (4 * KB);
+      int64_t ahead[kAhead];
+      auto look = [&](int i, int part) __attribute__((always_inline)) {
+#pragma unroll
+        for (int y = part * 2 * kLoads / (4 * KB); y < (part + 1) * 2 * kLoads / (4 * KB); ++y) {
+          const bool V = y < kLoads;
+          const int x = V ? y : y - kLoads;
+          ahead[y - part * 2 * kLoads / (4 * KB)] =
+              places[min(i + (V ? 2 : 3), full - 1) * C::kKeys + wave * kRowsW + x * C::kLoadRows + (V ? vr : kr)];
         }
       };
       // tile i's values and tile i + 1's keys are in LDS, and every wave is done with tile i - 1's values
@@ -680,14 +695,26 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
             weights(std::bool_constant<!kInner>(), x, g * 4 * NQ, (g + 1) * 4 * NQ, a0 + i * C::kKeys + kb * 32);
             const int part = kb * 4 + g;
             if constexpr (kInner) {
-              if (part == 2 * KB) advance(i + 3);
+              if (EVEN && part == 2 * KB) advance(i + 3);
 #pragma unroll
-              for (int y = part * 2 * kLoads / (4 * KB); y < (part + 1) * 2 * kLoads / (4 * KB); ++y)
-                y < kLoads ? load_one(v_free, true, y) : load_one(k_ahead(), false, y - kLoads);
-              // one product, then up to four vector operations, in turn
+              for (int y = part * 2 * kLoads / (4 * KB); y < (part + 1) * 2 * kLoads / (4 * KB); ++y) {
+                const bool V = y < kLoads;
+                const int x = V ? y : y - kLoads;
+                if constexpr (EVEN) {
+                  load_one(V ? v_free : k_ahead(), V, x);
+                } else {
+                  dma16<false>((V ? v_free : k_ahead()) + (wave * kLoads + x) * (V ? C::kBlockV : C::kBlockK),
+                               (V ? vbase : kbase) + ahead[y - part * 2 * kLoads / (4 * KB)] + (V ? piece_v : piece_k[x]));
+                }
+              }
+              if constexpr (!EVEN) look(part + 1 < 4 * KB ? i : i + 1, (part + 1) % (4 * KB));
+              // one product, from the fifth on a fragment read, then up to four vector operations, in turn
+              // (2,048 tokens over 32,768: 928 us; reads where the compiler puts them 950 to 975, with
+              // every product 969, from the third on 972)
 #pragma unroll
               for (int y = 0; y < kSteps * NQ / 2; ++y) {
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                if (y > 3) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
                 __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
               }
               __builtin_amdgcn_sched_barrier(0);
@@ -729,12 +756,13 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
       // Tiles inner0 .. inner1 are seen whole by every row of the wave, and every row has its reference
       // (those that see the first block have it now, the others from the tile that `all_low` lies in);
       // the loads they ask for are of whole tiles or of none.
-      const int full = (a1 - a0) / C::kKeys;
       const int inner0 = all_low <= a0 ? 0 : min(count, (all_low - a0) / C::kKeys + 1);
-      const int inner1 = p.even_pages ? min(full < count ? full - 3 : full, (min(all_lim, a1 - 1) - a0 + 1) / C::kKeys) : 0;
+      const int inner1 = min(full < count ? full - 3 : full, (min(all_lim, a1 - 1) - a0 + 1) / C::kKeys);
       int i = 0;
       for (; i < inner0; ++i) tile(std::false_type(), i);
+      if (!EVEN && i < inner1) look(i, 0);
       for (; i < inner1; ++i) tile(std::true_type(), i);
+      if (!EVEN && inner0 < inner1) place(i + 2);  // (what the next tile's values go by)
       // (the scores after the last block are of zeros, and nobody's)
       for (; i < count; ++i) tile(std::false_type(), i);
       product(0);
@@ -999,17 +1027,17 @@ hipError_t allow_lds(Kernel* k, int bytes, std::atomic<bool> (&raised)[kMaxDevic
   return e;
 }
 
-template <class E, int D, bool CAP>
-hipError_t launch_chunk_cap(const AttnParams& p, hipStream_t s) {
+template <class E, int D, bool CAP, bool EVEN>
+hipError_t launch_chunk_kernel(const AttnParams& p, hipStream_t s) {
   static std::atomic<bool> raised[kMaxDevices];
-  hipError_t e = allow_lds(chunk_kernel<E, D, CAP>, Chunk<D>::kLds, raised);
+  hipError_t e = allow_lds(chunk_kernel<E, D, CAP, EVEN>, Chunk<D>::kLds, raised);
   if (e != hipSuccess) return e;
   const int shares = device_cus();
   if (p.head) {
     plan_kernel<<<dim3(1), dim3(1024), 0, s>>>(p, Chunk<D>::kRows, Chunk<D>::kKeys, shares);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  chunk_kernel<E, D, CAP><<<dim3(shares), dim3(64 * kWaves), Chunk<D>::kLds, s>>>(p);
+  chunk_kernel<E, D, CAP, EVEN><<<dim3(shares), dim3(64 * kWaves), Chunk<D>::kLds, s>>>(p);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int groups = 256 / (D / 4);
   chunk_join_kernel<E, D><<<dim3(p.records ? p.records : shares, (p.part_rows + groups - 1) / groups), dim3(256), 0,
@@ -1030,10 +1058,14 @@ hipError_t launch_chunk(AttnParams p, void* workspace, hipStream_t s) {
   p.part_o = (float*)(base + w.o);
   p.part_rows = (int)w.part_rows;
   p.records = w.tiles * p.Hkv <= device_cus() ? (int)w.tiles * p.Hkv : 0;
-  // a wave's rows of a tile start at a multiple of 16 (or 8) keys; their offsets in a page must fit
-  // 32 bits
-  p.even_pages = p.kv.page.d % 16 == 0 && p.kv.ts >= 0 && p.kv.ts * p.kv.page.d < (int64_t(1) << 30);
-  return p.cap > 0.f ? launch_chunk_cap<E, D, true>(p, s) : launch_chunk_cap<E, D, false>(p, s);
+  // A wave's rows of a tile start at a multiple of 16 (or 8) keys: pages of a multiple of 16 tokens hold
+  // them whole, and a load goes by one place and 32-bit offsets; otherwise every row's place is staged
+  // (1,024 tokens over 8,192, pages of 64 and of 100: 152 and 156 us at D 128; with its
+  // tiles checked like the last ones, 232).
+  const bool even = p.kv.page.d % 16 == 0 && p.kv.ts >= 0 && p.kv.ts * p.kv.page.d < (int64_t(1) << 30);
+  if (p.cap > 0.f)
+    return even ? launch_chunk_kernel<E, D, true, true>(p, s) : launch_chunk_kernel<E, D, true, false>(p, s);
+  return even ? launch_chunk_kernel<E, D, false, true>(p, s) : launch_chunk_kernel<E, D, false, false>(p, s);
 }
 
 // ------------------------------------------------------------------ decode

@@ -239,7 +239,6 @@ struct AttnParams {
   int records;     // how many: one a run, in batches of few; 0: one a share
   // chunks
   int part_rows;    // rows of a part
-  int even_pages;   // every 16 keys from a multiple of 16 lie in one page
   void* tiles;      // the list of query tiles (plan_kernel)
   int64_t* before;  // [tiles + 1]: key tiles of the tiles before
   void* seqs;      // [B]: the sequences, when they are more than 1024
