@@ -52,9 +52,16 @@ __device__ __forceinline__ void put(V* p, V w) {
   else
     *p = w;
 }
-template <int W, typename E>
+template <bool NT, typename V>
+__device__ __forceinline__ V get(const V* p) {
+  if constexpr (NT)
+    return __builtin_nontemporal_load(p);
+  else
+    return *p;
+}
+template <int W, bool NT = false, typename E>
 __device__ __forceinline__ void load(const E* p, float (&x)[W]) {
-  const typename Piece<W, E>::type w = *(const typename Piece<W, E>::type*)p;
+  const typename Piece<W, E>::type w = get<NT>((const typename Piece<W, E>::type*)p);
 #pragma unroll
   for (int i = 0; i < W; ++i) x[i] = to_f(w[i]);
 }
@@ -87,10 +94,12 @@ struct Place {
   int64_t pos, dst;
 };
 
-// Stores pass the caches (NT) when the call writes more than the L2s hold together:
-// 369 MB of prompts 74.4 -> 63.4 us, 688 MB of gradients 127.7 -> 123.8 us; below that
-// the next kernel may find them there.  With pieces that neighbouring threads take side
-// by side these are 56.2 and 114.3 us now (6.6 and 6.0 TB/s; a copy reaches 5.7-6.0).
+// Loads and stores pass the caches (NT) when the call writes more than the L2s hold
+// together; below that the next kernel may find the rows there.  Other rows in every
+// call: 368 MB of prompts 69 us (5.3 TB/s; 72 when the loads stay), 688 MB of
+// gradients 115 us (6.0 TB/s; 117 when the loads stay, 128 when the stores do too; a
+// copy reaches 5.7-6.0); the same prompts again and again, part of which the
+// memory-side cache then holds, 56 us, 74 when the stores stay.
 constexpr int64_t kCacheBytes = 32 << 20;
 
 template <class Tag, bool NEAR, int W, bool NT>
@@ -173,8 +182,8 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeParams p) {
       const int a = W * (turn ? w : w + turned);
       const int b = a + (turn ? half : (p.D >> 1) - W * turned);
       float x[W], y[W];
-      load<W>(src + a, x);
-      load<W>(src + b, y);
+      load<W, NT>(src + a, x);
+      load<W, NT>(src + b, y);
       if (turn) {
         // cosines and sines: of the pairs across the pieces, or of each one's own
         constexpr int P = NEAR ? W / 2 : W;
@@ -280,7 +289,7 @@ hipError_t launch_rope(RopeParams p, int dtype, bool interleaved, int width, hip
   const int units = width > 1 ? p.D / (2 * width) : p.D - p.rot / 2;
   p.heads = fast_div(H);
   p.row_units = fast_div(units);
-  // two rounds of the workgroup's threads
+  // two rounds of the workgroup's threads (one 72, two 72, four 74, eight 82 us for the prompts)
   const int64_t per_token = (int64_t)H * units;
   p.tokens_per_block = (int)std::max<int64_t>(1, std::min<int64_t>(kRopeTokens, 2 * kRopeThreads / per_token));
   const dim3 grid((uint32_t)((p.T + p.tokens_per_block - 1) / p.tokens_per_block));
