@@ -1070,6 +1070,8 @@ hipError_t launch_chunk(AttnParams p, void* workspace, hipStream_t s) {
   p.part_ml = (float*)(base + w.ml);
   p.part_o = (float*)(base + w.o);
   p.part_rows = (int)w.part_rows;
+  // Few tiles: a record each, and joins launched for those alone (17 tokens over 1,000: 8 of them instead
+  // of 256 shares' take the join from 6.4 to 4.0 us).
   p.records = w.tiles * p.Hkv <= device_cus() ? (int)w.tiles * p.Hkv : 0;
   // A wave's rows of a tile start at a multiple of 16 (or 8) keys: pages of a multiple of 16 tokens hold
   // them whole, and a load goes by one place and 32-bit offsets; otherwise every row's place is staged
@@ -1493,6 +1495,8 @@ hipError_t launch_decode_cap(const AttnParams& p, hipStream_t s) {
   decode_kernel<E, D, CAP><<<dim3(shares / kWaves), dim3(64 * kWaves), kDecLds<D>, s>>>(p);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int rows = std::min<int>(kDecRows, (int)p.group.d), groups = 1024 / D;
+  // (512 sequences on 8 heads have 2 parts a run: 5.0 us by rows; 16 runs of about 100 parts: 15.6 us by
+  // rows, 6.2 by values)
   if (p.records && 4 * p.records <= shares)
     decode_join_kernel<E, D, true><<<dim3(p.records, rows, D / 32), dim3(256), 0, s>>>(p);
   else
