@@ -1097,10 +1097,10 @@ hipError_t launch_chunk(AttnParams p, void* workspace, hipStream_t s) {
 // sum of two 16-bit parts (the matrix units idle anyway), so what it adds to the
 // output's own rounding is invisible.
 //
-// Bound by memory: 512 sequences of up to 4,096 tokens (3.09 GB) 514 us, 6.0 TB/s;
-// 4 of 131,072 tokens 351 us, 6.1 TB/s (a copy reaches 5.7 to 6.0).  Where runs are
+// Bound by memory: 512 sequences of up to 4,096 tokens (3.09 GB) 512 us, 6.0 TB/s;
+// 4 of 131,072 tokens 353 us, 6.1 TB/s (a copy reaches 5.7 to 6.0).  Where runs are
 // short their start (page table, page ids, first keys) shows: 512 sequences of up to
-// 150 tokens on 8 heads 39 us, against 62 when four waves shared each run and
+// 150 tokens on 8 heads 38 us, against 62 when four waves shared each run and
 // waited for each other; long runs lose 1% to the parts they write.
 
 constexpr int kDecTile = 32;   // keys of a tile
@@ -1223,6 +1223,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
   int base = b;
   Span spans = dec_span(p, min(b + lane, B - 1));
 
+  int staged_b = -1, staged_page = 0, staged_last = 0;  // the page ids at hand
   char* ring = smem + wave * (2 * NS * kSlot);
   for (int64_t u = first; u < end;) {
     if (b - base >= 64) {
@@ -1262,8 +1263,14 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
       // (whole tiles; kDecPages pages are more than a tile's keys)
       const int a1 = reach >= key_b ? key_b : (int)reach / kDecTile * kDecTile;
       const int last = (int)div_by(a1 - 1, p.kv.page);
-      for (int i = lane; i <= last - page0; i += 64) page_ids[i] = p.kv.idx[sp.first_page + page0 + i];
-      wait_lds();
+      // (the heads of a sequence go by the same pages: 512 mixed sequences 517 -> 512 us)
+      if (b != staged_b || page0 != staged_page || last > staged_last) {
+        for (int i = lane; i <= last - page0; i += 64) page_ids[i] = p.kv.idx[sp.first_page + page0 + i];
+        wait_lds();
+        staged_b = b;
+        staged_page = page0;
+        staged_last = last;
+      }
       const int start = a0 / kDecTile * kDecTile;
       const int n = (a1 - start + kDecTile - 1) / kDecTile;
 
@@ -1495,9 +1502,9 @@ hipError_t launch_decode_cap(const AttnParams& p, hipStream_t s) {
   decode_kernel<E, D, CAP><<<dim3(shares / kWaves), dim3(64 * kWaves), kDecLds<D>, s>>>(p);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int rows = std::min<int>(kDecRows, (int)p.group.d), groups = 1024 / D;
-  // (512 sequences on 8 heads have 2 parts a run: 5.0 us by rows; 16 runs of about 100 parts: 15.6 us by
-  // rows, 6.2 by values)
-  if (p.records && 4 * p.records <= shares)
+  // (runs of 4 parts and fewer by rows: 64 sequences of 2,000 tokens on 8 heads 40 us in all, 44 by values;
+  // runs of 8 parts and more by values: 32 of 8,000 on 8 heads 48 us, 52 by rows)
+  if (p.records && 8 * p.records <= shares)
     decode_join_kernel<E, D, true><<<dim3(p.records, rows, D / 32), dim3(256), 0, s>>>(p);
   else
     decode_join_kernel<E, D, false>
