@@ -148,8 +148,9 @@ int gdn_kv_append_paged(const gdn_rope_t* rope, int32_t dtype, int32_t head_dim,
  * lse = -inf.  Scores, references, sums and the output accumulate in fp32.  In
  * the chunk call e^{x} enters the product with v rounded to the element type, as
  * the scores' matrix product takes q and k in theirs (bf16: 2.2e-3 of the output
- * in the mean, where the output's own rounding is 1.6e-3); the decode call passes
- * it as the sum of two such values and adds nothing visible.  Cache slots that no
+ * in the mean, where the output's own rounding is 1.6e-3; in fp16, whose least step
+ * is 2^-24, each weight is off by up to 2^-32 of the row's sum besides); the decode
+ * call passes it as the sum of two such values and adds nothing visible.  Cache slots that no
  * sequence holds are never read, whatever they contain; keys and values a row does
  * not see do not reach it, and infinities and NaN it sees enter it as themselves.
  */

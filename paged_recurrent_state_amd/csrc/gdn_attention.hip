@@ -6,10 +6,10 @@
 // in one pass over the keys: a reference m, the sum l of 2^{x - m} and the
 // unnormalised output, all in fp32 and in log2 units.  Any reference gives the same
 // quotient as long as nothing overflows or vanishes, so it need not be the maximum:
-// chunks take it from the first keys a row sees, and compute a share again, with a
+// chunks take it from the first keys a row sees (in fp16 they move it when a weight
+// grows large, l and o multiplied by 2^{m - m'}), and compute a share again, with a
 // reference that follows the maximum, in the rare case that this did not hold;
-// decode multiplies l and o by 2^{m - m'} when a score exceeds m by more than
-// kSlack.
+// decode moves it when a score exceeds m by more than kSlack.
 //
 // Products on 32x32x16 MFMAs, transposed so that a query row is a lane's column:
 //   S^T [keys x rows] = K Q^T     A = K rows from LDS, B = Q rows from registers
@@ -40,14 +40,19 @@ constexpr int kWaves = 4;
 constexpr float kNoScore = -3.0e38f;  // reference before the first score
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Element types.  Decode takes references kBias below a row's maximum, and new
-// ones when a score exceeds them by kSlack more (2^(kBias + kSlack) stays in
-// fp16's range).  Chunks take them kUp above the maximum of the first block a row
-// sees, and keep them while the row's weights sum to at most kHigh and nothing
-// overflows (fp16: later scores up to 20 above that maximum).  kOne is 1 in the
+// Element types.  References lie kBias below the highest score at hand, so that
+// scores far below it keep a weight: fp16 has none under 2^-25, and 2^17 keys at
+// that weight may hold all the values beside one heavy key that holds none.
+// 2^(kBias + kSlack) stays in the type's range.  Decode takes a new reference when a
+// score exceeds its own by kBias + kSlack.  Chunks take theirs from the first block a
+// row sees and keep it in bf16 (whose weights have fp32's range) while the row's
+// weights sum to at most kHigh and nothing overflows; in fp16 (kMoves) they take a
+// new one when 16 weights sum to more than 2^(kBias + kSlack).  Over 32,768 scores
+// spread by 2 (by 4) that is so in 2 (22) of a wave's 1,024 blocks.  kOne is 1 in the
 // type, kExp and kCarry find values that are not finite in a packed pair.
 struct Bf {
-  static constexpr float kBias = 0.f, kSlack = 8.f, kUp = 0.f, kHigh = 0x1p100f;
+  static constexpr float kBias = 0.f, kSlack = 8.f, kHigh = 0x1p100f;
+  static constexpr bool kMoves = false;
   static constexpr uint32_t kOne = 0x3f80u, kExp = 0x7f807f80u, kCarry = 0x00800080u;
   static __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
@@ -56,7 +61,8 @@ struct Bf {
   static __device__ __forceinline__ uint32_t pack(float a, float b) { return f2bf2(a, b); }
 };
 struct Hf {
-  static constexpr float kBias = 7.f, kSlack = 8.f, kUp = 4.f, kHigh = 0x1p100f;
+  static constexpr float kBias = 7.f, kSlack = 8.f, kHigh = 0x1p100f, kMost = 0x1p15f;
+  static constexpr bool kMoves = true;
   static constexpr uint32_t kOne = 0x3c00u, kExp = 0x7c007c00u, kCarry = 0x04000400u;
   static __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
@@ -659,8 +665,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
             for (int a = 0; a < NQ; ++a) o[a][d] = E::mfma(f, pt[a][t], o[a][d]);
           }
         };
-        // References for the rows that have none yet: the highest score that the row sees in the block of
-        // scores at hand, lowered weights kUp below 1 leaving room above.
+        // References for the rows that have none yet: kBias below the highest score that the row sees in the
+        // block of scores at hand.
         auto refer = [&](const f32x16 (&x)[NQ], int key0) __attribute__((always_inline)) {
           bool none = false;
 #pragma unroll
@@ -672,9 +678,30 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
 #pragma unroll
               for (int e = 0; e < 16; ++e) top = fmaxf(top, seen(a, e, key0) ? score<CAP>(p, x[a][e]) : -INFINITY);
               top = fmaxf(top, other_half(top));
-              if (m[a] == kNoScore && top > kNoScore) m[a] = top + E::kUp;
+              if (m[a] == kNoScore && top > kNoScore) m[a] = top - E::kBias;
             }
           }
+        };
+
+        // Weights that outgrew the element type's range: their rows' references move to kBias below the highest
+        // score of the block at hand, whose weights are taken again.
+        auto move = [&](auto mask, const f32x16 (&x)[NQ], int key0) __attribute__((always_inline)) {
+#pragma unroll
+          for (int a = 0; a < NQ; ++a) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (!decltype(mask)::value || seen(a, e, key0)) top = fmaxf(top, score<CAP>(p, x[a][e]));
+            top = fmaxf(top, other_half(top));
+            const float to = fmaxf(m[a], top - E::kBias), f = __builtin_amdgcn_exp2f(m[a] - to);
+            m[a] = to;
+            l[a] *= f;
+#pragma unroll
+            for (int d = 0; d < kBlocks; ++d)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[a][d][e] *= f;
+          }
+          weights(mask, x, 0, 16 * NQ, key0);
         };
 
         // One tile, block by block: the weights of a block, and beside them the product of the block
@@ -739,6 +766,18 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
                   load(k_ahead(), false);
                 }
               }
+            }
+            if constexpr (E::kMoves) {
+              float most = sum[0];
+#pragma unroll
+              for (int a = 1; a < NQ; ++a) most = fmaxf(most, sum[a]);
+              // (D 64 and 128: the weights are packed beside the products, not behind the branch: 2,048 tokens
+              // over 32,768 1,082 -> 1,062 us; at D 256 the compiler does better by itself, 254 against 260)
+              if constexpr (NQ == 2) {
+#pragma unroll
+                for (int e = 0; e < 8 * NQ; ++e) asm volatile("" ::"v"(pw[e >> 3][(e >> 2) & 1][e & 3]));
+              }
+              if (__any(most > E::kMost)) move(std::bool_constant<!kInner>(), x, a0 + i * C::kKeys + kb * 32);
             }
 #pragma unroll
             for (int a = 0; a < NQ; ++a) {
@@ -820,8 +859,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
   // The share again, with care, where its references did not hold: scores that outgrew them by more
   // than the weights can hold, or values that are not finite.  Here the reference follows the
   // maximum, and a value that is not finite enters only the rows that see it, as itself: its places
-  // are taken out of the product with V and counted by products of zeros and ones.  Right for
-  // everything and two to three times slower.
+  // are taken out of the product with V and counted by products of zeros and ones.  Five times slower.
   if (!__syncthreads_or(off)) return;
   char *sk = smem, *sv = smem + 32 * D * 2;
   hk = uniform((int)div_units(first, per_head));
@@ -889,7 +927,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
             s[e] = seen(e) ? score<CAP>(p, s[e]) : -INFINITY;
             top = fmaxf(top, s[e]);
           }
-          const float to = fmaxf(m, fmaxf(top, other_half(top))), f = __builtin_amdgcn_exp2f(m - to);
+          const float to = fmaxf(m, fmaxf(top, other_half(top)) - E::kBias), f = __builtin_amdgcn_exp2f(m - to);
           m = to;
           l *= f;
 #pragma unroll
