@@ -78,6 +78,40 @@ __device__ __forceinline__ float other_half(float x) {
   return __shfl_xor(x, 32, 64);
 }
 
+// An output taken to another reference: an infinity stays one, however far the
+// references lie apart (0 * inf would make it NaN).
+__device__ __forceinline__ float rescaled(float x, float f) { return __builtin_isinf(x) ? x : x * f; }
+__device__ __forceinline__ f32x4 rescaled(f32x4 x, float f) {
+  return f32x4{rescaled(x[0], f), rescaled(x[1], f), rescaled(x[2], f), rescaled(x[3], f)};
+}
+
+// Whether any of 8 values is an infinity or a NaN.
+template <class E>
+__device__ __forceinline__ bool has_odd(u32x4 v) {
+  uint32_t odd = 0;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) odd |= (v[x] & E::kExp) + E::kCarry;
+  return (odd & 0x80008000u) != 0;
+}
+// Takes the infinities and NaN out of 8 values and leaves ones in their places: in
+// `plus`, in `minus`, or for a NaN in both.
+template <class E>
+__device__ __forceinline__ void take_odd(u32x4& v, u32x4& plus, u32x4& minus) {
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    plus[x] = minus[x] = 0u;
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const uint32_t w = (v[x] >> (16 * y)) & 0xffffu, big = E::kExp & 0x7fffu;
+      if ((w & 0x7fffu) >= big) {
+        if (w != (big | 0x8000u)) plus[x] |= E::kOne << (16 * y);
+        if (w != big) minus[x] |= E::kOne << (16 * y);
+        v[x] &= y ? 0x0000ffffu : 0xffff0000u;
+      }
+    }
+  }
+}
+
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 typedef __attribute__((address_space(3))) const u32x4* lds_u32x4;
 
@@ -933,7 +967,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
 #pragma unroll
           for (int d = 0; d < kBlocks; ++d)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[d][e] *= f;
+            for (int e = 0; e < 16; ++e) o[d][e] = rescaled(o[d][e], f);
           u32x4 pt[2];
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
@@ -952,26 +986,12 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
               const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(sv + v_at<D>(key + 8, dim >> 3) + sub));
               const u32x2 wl = __builtin_bit_cast(u32x2, lo), wh = __builtin_bit_cast(u32x2, hi);
               u32x4 vf{wl[0], wl[1], wh[0], wh[1]};
-              uint32_t odd = 0;
-#pragma unroll
-              for (int x = 0; x < 4; ++x) odd |= (vf[x] & E::kExp) + E::kCarry;
-              if (__any((odd & 0x80008000u) != 0)) {
+              if (__any(has_odd<E>(vf))) {
                 u32x4 ones, plus, minus;
+                take_odd<E>(vf, plus, minus);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
+                for (int x = 0; x < 4; ++x)
                   ones[x] = (seen(8 * t + 2 * x) ? E::kOne : 0u) | (seen(8 * t + 2 * x + 1) ? E::kOne << 16 : 0u);
-                  plus[x] = minus[x] = 0u;
-#pragma unroll
-                  for (int y = 0; y < 2; ++y) {
-                    // an infinity, or a NaN (both signs: their sum is NaN)
-                    const uint32_t v = (vf[x] >> (16 * y)) & 0xffffu, big = E::kExp & 0x7fffu;
-                    if ((v & 0x7fffu) >= big) {
-                      if (v != (big | 0x8000u)) plus[x] |= E::kOne << (16 * y);
-                      if (v != big) minus[x] |= E::kOne << (16 * y);
-                      vf[x] &= y ? 0x0000ffffu : 0xffff0000u;
-                    }
-                  }
-                }
                 f32x16 np, nm;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) np[e] = nm[e] = 0.f;
@@ -1027,7 +1047,7 @@ __global__ __launch_bounds__(256) void chunk_join_kernel(AttnParams p) {
         const float to = fmaxf(top, ml[x].x), f = __builtin_amdgcn_exp2f(top - to), h = __builtin_amdgcn_exp2f(ml[x].x - to);
         top = to;
         sum = sum * f + ml[x].y * h;
-        acc = acc * f + o[x] * h;
+        acc = rescaled(acc, f) + rescaled(o[x], h);
       }
   }
   const bool none = sum == 0.f;  // a row that saw nothing in any part
@@ -1129,6 +1149,10 @@ hipError_t launch_chunk(AttnParams p, void* workspace, hipStream_t s) {
 // end to end are cut into equal shares, one a wave, and a run that crosses shares
 // is joined afterwards from its parts' (m, l, o).
 //
+// A run whose outputs are not finite is computed again with care: a value that is
+// not finite then enters as itself, however small its weight (its place is taken out
+// of the product with V and counted by products of ones).
+//
 // No wave waits for another: it loads its keys and values straight into its own
 // ring in LDS, and reads them once they have landed while the next are on the way.
 // Products on 16x16x32 MFMAs in the same transposed form as above; P enters as the
@@ -1162,22 +1186,20 @@ __device__ __forceinline__ f32x4 mfma16<Hf>(u32x4 a, u32x4 b, f32x4 c) {
                                                 0);
 }
 
-// Two weights as hi + lo in the element type: hi cut off, not rounded, so that lo
-// is not negative, and lo at least a trace of the weight: an infinite value that a
-// row sees then reaches its output as that infinity, never as 0 * inf.
+// Two weights as hi + lo in the element type, hi cut off, not rounded.
 template <class E>
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo);
 template <>
 __device__ __forceinline__ void split2<Bf>(float a, float b, uint32_t& hi, uint32_t& lo) {
   const uint32_t x = __float_as_uint(a) & 0xffff0000u, y = __float_as_uint(b) & 0xffff0000u;
   hi = (x >> 16) | y;
-  lo = f2bf2(fmaxf(a - __uint_as_float(x), a * 0x1p-20f), fmaxf(b - __uint_as_float(y), b * 0x1p-20f));
+  lo = f2bf2(a - __uint_as_float(x), b - __uint_as_float(y));
 }
 template <>
 __device__ __forceinline__ void split2<Hf>(float a, float b, uint32_t& hi, uint32_t& lo) {
   const f16x2 h = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_pkrtz(a, b));
   hi = __builtin_bit_cast(uint32_t, h);
-  lo = Hf::pack(fmaxf(a - (float)h[0], fminf(a, 0x1p-24f)), fmaxf(b - (float)h[1], fminf(b, 0x1p-24f)));
+  lo = Hf::pack(a - (float)h[0], b - (float)h[1]);
 }
 
 // Tokens sequence b holds, and the first its (only) query sees.
@@ -1263,6 +1285,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
 
   int staged_b = -1, staged_page = 0, staged_last = 0;  // the page ids at hand
   char* ring = smem + wave * (2 * NS * kSlot);
+  bool care = false;  // this run is computed again
   for (int64_t u = first; u < end;) {
     if (b - base >= 64) {
       base = b;
@@ -1284,7 +1307,9 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) q[s] = *(const u32x4*)(src + 32 * s + 8 * grp);
     }
+    static_assert(4 * kBlocks <= 64);
     f32x4 o[kBlocks];
+    uint64_t above = 0, below = 0;  // with care: outputs 4 d + e that an infinity, or a NaN (both), belongs to
     float m = kNoScore, l = 0.f;
 #pragma unroll
     for (int d = 0; d < kBlocks; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -1343,6 +1368,39 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
           dma16<true>(dst + x * 1024, at[x] < 0 ? (const char*)&g_zero : src);
         }
       };
+      // V^T of 16 values: keys 4 grp + 0..3 and 16 more, in the order S leaves them
+      auto read_v = [&](const char* sv, int d) __attribute__((always_inline)) {
+        const int kr = 4 * grp + (col >> 2), dim = 16 * d + 4 * (lane & 3), sub = (dim & 7) * 2;
+        const s16x4 wl = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(sv + v_at<D>(kr, dim >> 3) + sub));
+        const s16x4 wh = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(sv + v_at<D>(kr + 16, dim >> 3) + sub));
+        const u32x2 a = __builtin_bit_cast(u32x2, wl), c = __builtin_bit_cast(u32x2, wh);
+        return u32x4{a[0], a[1], c[0], c[1]};
+      };
+      // Takes what is not finite out of a tile of V, and notes the outputs it belongs to (keys outside the
+      // part are zeros here).
+      auto take_out = [&](char* sv) __attribute__((always_inline)) {
+        constexpr uint32_t kOnes = E::kOne | E::kOne << 16;
+        const u32x4 ones{kOnes, kOnes, kOnes, kOnes};
+        const f32x4 none{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int d = 0; d < kBlocks; ++d) {
+          u32x4 vf = read_v(sv, d), plus, minus;
+          take_odd<E>(vf, plus, minus);
+          const f32x4 np = mfma16<E>(plus, ones, none), nm = mfma16<E>(minus, ones, none);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            above |= (uint64_t)(np[e] > 0.f) << (4 * d + e);
+            below |= (uint64_t)(nm[e] > 0.f) << (4 * d + e);
+          }
+        }
+        wait_lds();
+        for (int x = lane; x < kSlot / 16; x += 64) {
+          u32x4 w = *(const u32x4*)(sv + 16 * x), plus, minus;
+          take_odd<E>(w, plus, minus);
+          *(u32x4*)(sv + 16 * x) = w;
+        }
+        wait_lds();
+      };
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         place(i);
@@ -1351,7 +1409,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
       }
       for (int i = 0; i < n; ++i) {
         const char* sk = ring + (i % NS) * kSlot;
-        const char* sv = ring + NS * kSlot + (i % NS) * kSlot;
+        char* sv = ring + NS * kSlot + (i % NS) * kSlot;
         // outstanding after the keys of tile i: its values and NS - 1 whole tiles
         wait_vm<(2 * NS - 1) * kLoads>();
         f32x4 s[2];
@@ -1394,14 +1452,10 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
         }
         // outstanding after the values of tile i: NS - 1 tiles and the keys just asked for
         wait_vm<(2 * NS - 1) * kLoads>();
+        if (care) take_out(sv);
 #pragma unroll
         for (int d = 0; d < kBlocks; ++d) {
-          // keys 4 grp + 0..3 and 16 more, in the order S left them
-          const int kr = 4 * grp + (col >> 2), dim = 16 * d + 4 * (lane & 3), sub = (dim & 7) * 2;
-          const s16x4 wl = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(sv + v_at<D>(kr, dim >> 3) + sub));
-          const s16x4 wh = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(sv + v_at<D>(kr + 16, dim >> 3) + sub));
-          const u32x2 a = __builtin_bit_cast(u32x2, wl), c = __builtin_bit_cast(u32x2, wh);
-          const u32x4 vf{a[0], a[1], c[0], c[1]};
+          const u32x4 vf = read_v(sv, d);
           o[d] = mfma16<E>(vf, lo, o[d]);
           o[d] = mfma16<E>(vf, hi, o[d]);
         }
@@ -1412,6 +1466,24 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
       a0 = a1;
     }
 
+    if (care) {
+#pragma unroll
+      for (int d = 0; d < kBlocks; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o[d][e] += above >> (4 * d + e) & 1 ? INFINITY : 0.f;
+          o[d][e] += below >> (4 * d + e) & 1 ? -INFINITY : 0.f;
+        }
+    } else {
+      float z = 0.f;
+#pragma unroll
+      for (int d = 0; d < kBlocks; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z = __builtin_fmaf(o[d][e], 0.f, z);
+      care = __any(z != 0.f);
+      if (care) continue;
+    }
+    care = false;
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
     const bool whole = t == 0 && todo == tiles;
@@ -1463,7 +1535,7 @@ struct Joined {
       const float to = fmaxf(top, m), f = __builtin_amdgcn_exp2f(top - to), h = __builtin_amdgcn_exp2f(m - to);
       top = to;
       sum = sum * f + l * h;
-      acc = acc * f + o * h;
+      acc = rescaled(acc, f) + rescaled(o, h);
     }
   }
 };
