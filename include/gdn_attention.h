@@ -145,14 +145,16 @@ int gdn_kv_append_paged(const gdn_rope_t* rope, int32_t dtype, int32_t head_dim,
  *     o   = sum_j e^{x_j} v_j / sum_j e^{x_j},   lse = log sum_j e^{x_j}
  * over the tokens j of the sequence with j <= t (causal; otherwise all of them)
  * and, for window > 0, j > t - window.  A row that sees no token gives o = 0 and
- * lse = -inf.  Scores, references, sums and the output accumulate in fp32.  In
- * the chunk call e^{x} enters the product with v rounded to the element type, as
- * the scores' matrix product takes q and k in theirs (bf16: 2.2e-3 of the output
- * in the mean, where the output's own rounding is 1.6e-3; in fp16, whose least step
- * is 2^-24, each weight is off by up to 2^-32 of the row's sum besides); the decode
- * call passes it as the sum of two such values and adds nothing visible.  Cache slots that no
- * sequence holds are never read, whatever they contain; keys and values a row does
- * not see do not reach it, and infinities and NaN it sees enter it as themselves.
+ * lse = -inf; one whose scores are all -inf gives o = NaN (0 / 0) and lse = -inf.
+ * Scores, references, sums and the output accumulate in fp32.  In the chunk call
+ * e^{x} enters the product with v rounded to the element type, as the scores'
+ * matrix product takes q and k in theirs (bf16: 2.2e-3 of the output in the mean,
+ * where the output's own rounding is 1.6e-3; in fp16, whose least step is 2^-24,
+ * each weight is off by up to 2^-32 of the row's sum besides); the decode call
+ * passes it as the sum of two such values and adds nothing visible.  Cache slots
+ * that no sequence holds are never read, whatever they contain; keys and values a
+ * row does not see do not reach it, and infinities and NaN it sees enter it as
+ * themselves.
  */
 typedef struct {
   int32_t num_q_heads;

@@ -37,7 +37,7 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 4;
-constexpr float kNoScore = -3.0e38f;  // reference before the first score
+constexpr float kNoScore = -__FLT_MAX__;  // reference before the first score
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Element types.  References lie kBias below the highest score at hand, so that
@@ -356,7 +356,9 @@ __device__ __forceinline__ int find_tile(const int64_t* before, int tiles, int c
 }
 
 // A lane's column of output (row in_tile of the tile, half of its values): the
-// finished row, or, into part `part` >= 0, what the join needs.
+// finished row, or, into part `part` >= 0, what the join needs.  A row that sees no
+// token (none) says so by a sum of -1 in its parts; one whose scores are all -inf has
+// a sum of 0, and by the formula 0 / 0 for its output.
 template <class E, int D>
 __device__ __forceinline__ void store_rows(const AttnParams& p, const TileRec& rec, int hk, int in_tile,
                                            int64_t part, const f32x16 (&o)[D / 32], float m, float sum, bool none) {
@@ -384,7 +386,7 @@ __device__ __forceinline__ void store_rows(const AttnParams& p, const TileRec& r
         *(f32x4*)(dst + 32 * d + 8 * i + 4 * half) = f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
     if (half == 0) {
       p.part_ml[(part * p.part_rows + in_tile) * 2] = m;
-      p.part_ml[(part * p.part_rows + in_tile) * 2 + 1] = sum;
+      p.part_ml[(part * p.part_rows + in_tile) * 2 + 1] = none ? -1.f : sum;
     }
   }
 }
@@ -1029,6 +1031,7 @@ __global__ __launch_bounds__(256) void chunk_join_kernel(AttnParams p) {
   if (u.parts == 0 || tok >= u.n) return;
   float top = kNoScore, sum = 0.f;
   f32x4 acc{0.f, 0.f, 0.f, 0.f};
+  bool none = false;
   // four parts at a time, on the way together
   for (int i0 = 0; i0 < u.parts; i0 += 4) {
     float2 ml[4];
@@ -1041,16 +1044,16 @@ __global__ __launch_bounds__(256) void chunk_join_kernel(AttnParams p) {
       o[x] = *(const f32x4*)(p.part_o + at * D + d);
       if (i0 + x >= u.parts) ml[x].y = 0.f;
     }
+    none = ml[0].y < 0.f;  // (so in every part)
 #pragma unroll
     for (int x = 0; x < 4; ++x)
-      if (ml[x].y != 0.f) {  // (a part without weights counts for nothing, whatever its reference)
+      if (!(ml[x].y <= 0.f)) {  // (a part without weights counts for nothing, whatever its reference)
         const float to = fmaxf(top, ml[x].x), f = __builtin_amdgcn_exp2f(top - to), h = __builtin_amdgcn_exp2f(ml[x].x - to);
         top = to;
         sum = sum * f + ml[x].y * h;
         acc = rescaled(acc, f) + rescaled(o[x], h);
       }
   }
-  const bool none = sum == 0.f;  // a row that saw nothing in any part
   acc *= none ? 0.f : 1.f / sum;
   const int64_t h = (int64_t)u.hk * p.group.d + g;
   *(u32x2*)((u16*)p.o.p + (int64_t)(u.tok0 + tok) * p.o.ts + h * p.o.hs + d) =
