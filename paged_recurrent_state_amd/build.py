@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -44,12 +45,34 @@ def hipcc() -> str:
     return cand
 
 
-def _compile(src: str) -> str:
-    obj = os.path.join(OBJDIR, os.path.splitext(src)[0] + ".o")
-    cmd = [hipcc(), *FLAGS, *SOURCE_FLAGS.get(src, []), "-I", INCLUDE, "-I", CSRC, "-c", os.path.join(CSRC, src), "-o", obj]
+def spills(remarks: str) -> dict:
+    """Kernels that keep vector registers in memory, from the compiler's resource remarks:
+    {name: (registers spilled, bytes of scratch a lane)}."""
+    found, name = {}, None
+    for line in remarks.splitlines():
+        m = re.search(r"remark:\s+(Function Name|VGPRs Spill|ScratchSize \[bytes/lane\]): (\S+)", line)
+        if not m:
+            continue
+        if m[1] == "Function Name":
+            name = m[2]
+        elif int(m[2]):
+            regs, scratch = found.get(name, (0, 0))
+            found[name] = (int(m[2]), scratch) if m[1] == "VGPRs Spill" else (regs, int(m[2]))
+    return found
+
+
+def _compile(src: str, csrc: str = CSRC, objdir: str = OBJDIR) -> str:
+    obj = os.path.join(objdir, os.path.splitext(src)[0] + ".o")
+    cmd = [hipcc(), *FLAGS, *SOURCE_FLAGS.get(src, []), "-Rpass-analysis=kernel-resource-usage", "-I", INCLUDE,
+           "-I", CSRC, "-c", os.path.join(csrc, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed on {src}:\n{r.stderr}")
+    # the kernels are laid out to fit the registers (the chunk attention's instances take up to 477 of 512):
+    # one that no longer does is an error of its source, not only slower
+    if bad := spills(r.stderr):
+        os.remove(obj)
+        raise RuntimeError(f"kernels of {src} spill (vector registers, bytes of scratch a lane): {bad}")
     return obj
 
 

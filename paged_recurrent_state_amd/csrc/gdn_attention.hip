@@ -357,15 +357,16 @@ __device__ __forceinline__ int find_tile(const int64_t* before, int tiles, int c
 
 // A lane's column of output (row in_tile of the tile, half of its values): the
 // finished row, or, into part `part` >= 0, what the join needs.  A row that sees no
-// token (none) says so by a sum of -1 in its parts; one whose scores are all -inf has
-// a sum of 0, and by the formula 0 / 0 for its output.
+// token has a sum of -1, in its parts too; one whose scores are all -inf a sum of 0,
+// and by the formula 0 / 0 for its output.
 template <class E, int D>
 __device__ __forceinline__ void store_rows(const AttnParams& p, const TileRec& rec, int hk, int in_tile,
-                                           int64_t part, const f32x16 (&o)[D / 32], float m, float sum, bool none) {
+                                           int64_t part, const f32x16 (&o)[D / 32], float m, float sum) {
   const int half = (threadIdx.x & 63) >> 5, row = rec.row0 + in_tile;
   const int tok0 = rec.tok0, tok = (int)div_by(row, p.group), g = row - tok * (int)p.group.d;
   if (tok >= rec.n) return;
   if (part < 0) {
+    const bool none = sum < 0.f;
     const float inv = none ? 0.f : 1.f / sum;
     const int64_t h = (int64_t)hk * p.group.d + g;
     u16* dst = (u16*)p.o.p + (int64_t)(tok0 + tok) * p.o.ts + h * p.o.hs;
@@ -386,7 +387,7 @@ __device__ __forceinline__ void store_rows(const AttnParams& p, const TileRec& r
         *(f32x4*)(dst + 32 * d + 8 * i + 4 * half) = f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
     if (half == 0) {
       p.part_ml[(part * p.part_rows + in_tile) * 2] = m;
-      p.part_ml[(part * p.part_rows + in_tile) * 2 + 1] = none ? -1.f : sum;
+      p.part_ml[(part * p.part_rows + in_tile) * 2 + 1] = sum;
     }
   }
 }
@@ -808,8 +809,9 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
 #pragma unroll
               for (int a = 1; a < NQ; ++a) most = fmaxf(most, sum[a]);
               // (D 64 and 128: the weights are packed beside the products, not behind the branch: 2,048 tokens
-              // over 32,768 1,082 -> 1,062 us; at D 256 the compiler does better by itself, 254 against 260)
-              if constexpr (NQ == 2) {
+              // over 32,768 1,082 -> 1,062 us; at D 256 the compiler does better by itself, 254 against 260, and
+              // with a cap it would spill)
+              if constexpr (NQ == 2 && !CAP) {
 #pragma unroll
                 for (int e = 0; e < 8 * NQ; ++e) asm volatile("" ::"v"(pw[e >> 3][(e >> 2) & 1][e & 3]));
               }
@@ -872,11 +874,14 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
         for (int d = 0; d < kBlocks; ++d)
 #pragma unroll
           for (int e = 0; e < 16; ++e) z = __builtin_fmaf(o[a][d][e], 0.f, z);
-        if (lim[a] >= 0) off = off || !(l[a] <= E::kHigh) || z != 0.f;
+        if (lim[a] < 0)
+          l[a] = -1.f;
+        else
+          off = off || !(l[a] <= E::kHigh) || z != 0.f;
       }
 #pragma unroll
       for (int a = 0; a < NQ; ++a)
-        store_rows<E, D>(p, rec, hk, wave * 32 * NQ + a * 32 + col, part, o[a], m[a], l[a], lim[a] < low[a]);
+        store_rows<E, D>(p, rec, hk, wave * 32 * NQ + a * 32 + col, part, o[a], m[a], l[a]);
       if (!head && (!whole || p.records)) {
         left = true;
         const int parts = whole ? 0 : (int)div_units(start + cost + tiles - 1, share) - me + 1;
@@ -1008,7 +1013,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
               o[d] = E::mfma(vf, pt[t], o[d]);
             }
         }
-        store_rows<E, D>(p, rec, hk, rows + wave * 32 + col, part, o, m, l + other_half(l), lim < low);
+        store_rows<E, D>(p, rec, hk, rows + wave * 32 + col, part, o, m, lim < 0 ? -1.f : l + other_half(l));
       }
     }
     if (start + cost + tiles >= end) break;
