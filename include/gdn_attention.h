@@ -151,10 +151,11 @@ int gdn_kv_append_paged(const gdn_rope_t* rope, int32_t dtype, int32_t head_dim,
  * matrix product takes q and k in theirs (bf16: 2.2e-3 of the output in the mean,
  * where the output's own rounding is 1.6e-3; in fp16, whose least step is 2^-24,
  * each weight is off by up to 2^-32 of the row's sum besides); the decode call
- * passes it as the sum of two such values and adds nothing visible.  Cache slots
- * that no sequence holds are never read, whatever they contain; keys and values a
- * row does not see do not reach it, and infinities and NaN it sees enter it as
- * themselves.
+ * passes it as the sum of two such values and adds nothing visible.  A capped score
+ * is off by up to 2^-19 of itself, or, in the chunk call and for caps of up to 64, by
+ * up to 2^-21 of the cap; caps over 1e30 count as none.  Cache slots that no sequence
+ * holds are never read, whatever they contain; keys and values a row does not see do
+ * not reach it, and infinities and NaN it sees enter it as themselves.
  */
 typedef struct {
   int32_t num_q_heads;

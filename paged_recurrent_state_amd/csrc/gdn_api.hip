@@ -825,7 +825,8 @@ int run_attention(const gdn_attention_dims_t* dims, const gdn_rows_t* q, const i
   p.causal = dims->causal != 0;
   const double scale = dims->scale > 0.f ? dims->scale : 1.0 / std::sqrt((double)dims->head_dim);
   const double log2e = 1.4426950408889634074;
-  if (dims->softcap > 0.f) {
+  // (a cap over 1e30 is none: it leaves scores below 1e26 as they are in fp32)
+  if (dims->softcap > 0.f && dims->softcap <= 1e30f) {
     p.scale = (float)(2.0 * log2e * scale / dims->softcap);
     p.cap = (float)(dims->softcap * log2e);
   } else {

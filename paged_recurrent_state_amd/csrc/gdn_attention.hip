@@ -171,6 +171,15 @@ __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)"
 
 __device__ const u32x4 g_zero = {0u, 0u, 0u, 0u};  // read in place of keys outside a run
 
+// Caps of scores: none; kCapShort, by 1 - 2 / (e^{2y} + 1) for tanh(y), which is off
+// by up to 2^-21 of the cap, near zero too; kCap, where scores under a quarter of the
+// cap go by the series of tanh, off by 2^-19 of the score at most.  Chunks take the
+// short form for caps up to kMostShort, where it is off by 3e-5 at most, a tenth of
+// what rounding the weights to fp16 is (2,048 tokens over 32,768: 1,154 us, 1,758 in
+// the long form, 912 without a cap); decode, bound by memory, always the long one.
+enum Cap { kNoCap, kCapShort, kCap };
+constexpr float kMostShort = 64.f;
+
 // How far a capped score lies under the cap, over twice the cap: with
 // p.scale = 2 log2(e) scale / softcap, tanh(y) = 1 - 2 / (e^{2y} + 1).
 __device__ __forceinline__ float under_cap(const AttnParams& p, float x) {
@@ -178,9 +187,15 @@ __device__ __forceinline__ float under_cap(const AttnParams& p, float x) {
 }
 
 // Score in log2 units.
-template <bool CAP>
+template <Cap CAP>
 __device__ __forceinline__ float score(const AttnParams& p, float x) {
-  return CAP ? __builtin_fmaf(under_cap(p, x), -2.f * p.cap, p.cap) : x * p.scale;
+  if constexpr (CAP == kNoCap) return x * p.scale;
+  const float far = __builtin_fmaf(under_cap(p, x), -2.f * p.cap, p.cap);
+  if constexpr (CAP == kCapShort) return far;
+  const float y = x * p.scale * (0.5f * kLn2), t = y * y;
+  const float r = __builtin_fmaf(__builtin_fmaf(t, -17.f / 315.f, 2.f / 15.f), t, -1.f / 3.f);
+  const float near_ = p.cap * __builtin_fmaf(r * t, y, y);  // (what is left out: 62/2835 y^9)
+  return fabsf(y) < 0.25f ? near_ : far;
 }
 
 // ------------------------------------------------------------------ chunks
@@ -393,7 +408,7 @@ __device__ __forceinline__ void store_rows(const AttnParams& p, const TileRec& r
 }
 
 // EVEN: a wave's rows of a tile lie in one page (see launch_chunk).
-template <class E, int D, bool CAP, bool EVEN>
+template <class E, int D, Cap CAP, bool EVEN>
 __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
   typedef Chunk<D> C;
   constexpr int NQ = C::kNQ, NSK = C::kSlotsK, NSV = C::kSlotsV, KB = C::kKeys / 32;
@@ -679,9 +694,12 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
             for (int e = 0; e < 16; e += 2)
               if (16 * a + e >= v0 && 16 * a + e < v1) {
                 float w0, w1;
-                if constexpr (CAP) {
+                if constexpr (CAP == kCapShort) {
                   w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(under_cap(p, x[a][e]), -2.f * p.cap, p.cap - m[a]));
                   w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(under_cap(p, x[a][e + 1]), -2.f * p.cap, p.cap - m[a]));
+                } else if constexpr (CAP == kCap) {
+                  w0 = __builtin_amdgcn_exp2f(score<CAP>(p, x[a][e]) - m[a]);
+                  w1 = __builtin_amdgcn_exp2f(score<CAP>(p, x[a][e + 1]) - m[a]);
                 } else {
                   w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[a][e], p.scale, -m[a]));
                   w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[a][e + 1], p.scale, -m[a]));
@@ -811,7 +829,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
               // (D 64 and 128: the weights are packed beside the products, not behind the branch: 2,048 tokens
               // over 32,768 1,082 -> 1,062 us; at D 256 the compiler does better by itself, 254 against 260, and
               // with a cap it would spill)
-              if constexpr (NQ == 2 && !CAP) {
+              if constexpr (NQ == 2 && CAP == kNoCap) {
 #pragma unroll
                 for (int e = 0; e < 8 * NQ; ++e) asm volatile("" ::"v"(pw[e >> 3][(e >> 2) & 1][e & 3]));
               }
@@ -1106,7 +1124,7 @@ hipError_t allow_lds(Kernel* k, int bytes, std::atomic<bool> (&raised)[kMaxDevic
   return e;
 }
 
-template <class E, int D, bool CAP, bool EVEN>
+template <class E, int D, Cap CAP, bool EVEN>
 hipError_t launch_chunk_kernel(const AttnParams& p, hipStream_t s) {
   static std::atomic<bool> raised[kMaxDevices];
   hipError_t e = allow_lds(chunk_kernel<E, D, CAP, EVEN>, Chunk<D>::kLds, raised);
@@ -1144,9 +1162,11 @@ hipError_t launch_chunk(AttnParams p, void* workspace, hipStream_t s) {
   // (1,024 tokens over 8,192, pages of 64 and of 100: 152 and 156 us at D 128; with its
   // tiles checked like the last ones, 232).
   const bool even = p.kv.page.d % 16 == 0 && p.kv.ts >= 0 && p.kv.ts * p.kv.page.d < (int64_t(1) << 30);
+  if (p.cap > kMostShort / kLn2)
+    return even ? launch_chunk_kernel<E, D, kCap, true>(p, s) : launch_chunk_kernel<E, D, kCap, false>(p, s);
   if (p.cap > 0.f)
-    return even ? launch_chunk_kernel<E, D, true, true>(p, s) : launch_chunk_kernel<E, D, true, false>(p, s);
-  return even ? launch_chunk_kernel<E, D, false, true>(p, s) : launch_chunk_kernel<E, D, false, false>(p, s);
+    return even ? launch_chunk_kernel<E, D, kCapShort, true>(p, s) : launch_chunk_kernel<E, D, kCapShort, false>(p, s);
+  return even ? launch_chunk_kernel<E, D, kNoCap, true>(p, s) : launch_chunk_kernel<E, D, kNoCap, false>(p, s);
 }
 
 // ------------------------------------------------------------------ decode
@@ -1223,7 +1243,7 @@ __device__ __forceinline__ Span dec_span(const AttnParams& p, int b) {
 __device__ __forceinline__ int dec_tiles(const Span& s) {
   return s.len <= s.begin ? 0 : (s.len + kDecTile - 1) / kDecTile - s.begin / kDecTile;
 }
-template <class E, int D, bool CAP>
+template <class E, int D, Cap CAP>
 __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(AttnParams p) {
   constexpr int NS = kDecStages<D>;
   constexpr int kSlot = kDecTile * D * 2;     // bytes of a tile's keys
@@ -1611,7 +1631,7 @@ int decode_shares() {
   return kWaves * device_cus() * (D == 256 ? 1 : 2);
 }
 
-template <class E, int D, bool CAP>
+template <class E, int D, Cap CAP>
 hipError_t launch_decode_cap(const AttnParams& p, hipStream_t s) {
   static std::atomic<bool> raised[kMaxDevices];
   hipError_t e = allow_lds(decode_kernel<E, D, CAP>, kDecLds<D>, raised);
@@ -1638,7 +1658,7 @@ hipError_t launch_dec(AttnParams p, void* workspace, hipStream_t s) {
   p.parts = (int*)(p.part_ml + (int64_t)2 * shares * kDecRows * 2);
   const int64_t items = (int64_t)p.kv.B * p.Hkv * ((p.group.d + kDecRows - 1) / kDecRows);
   p.records = items <= shares ? (int)items : 0;
-  return p.cap > 0.f ? launch_decode_cap<E, D, true>(p, s) : launch_decode_cap<E, D, false>(p, s);
+  return p.cap > 0.f ? launch_decode_cap<E, D, kCap>(p, s) : launch_decode_cap<E, D, kNoCap>(p, s);
 }
 
 template <int D>
