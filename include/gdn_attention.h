@@ -181,9 +181,11 @@ size_t gdn_attention_workspace_size(const gdn_attention_dims_t* dims, int64_t to
  * cu_seqlens[b] .. cu_seqlens[b+1], any count per sequence, none included) over
  * everything their sequences hold in the cache, the new tokens themselves
  * among it: append first, then attend.
- *   out: rows of total_tokens tokens; lse [total_tokens, num_q_heads] or NULL.
+ *   out: rows of total_tokens tokens that share no memory with q;
+ *   lse [total_tokens, num_q_heads] or NULL.
  * Errors: GDN_EINVAL (null pointers, negative sizes or window, page_size < 1,
- * rows or a cache that are not 16-byte aligned in every stride and address),
+ * rows or a cache that are not 16-byte aligned in every stride and address, out
+ * over q),
  * GDN_EUNSUPPORTED (head_dim, dtype, num_q_heads not a multiple of
  * num_kv_heads), GDN_EWORKSPACE, GDN_ELAUNCH.
  */
@@ -195,7 +197,8 @@ int gdn_attention_prefill_paged(const gdn_attention_dims_t* dims, const gdn_rows
 /*
  * gdn_attention_decode_paged -- one token per sequence: q and out hold num_seqs
  * rows, the query of sequence b sits at its last position.  A sequence without a
- * page gives o = 0 and lse = -inf.  Errors as gdn_attention_prefill_paged.
+ * page gives o = 0 and lse = -inf.  out may be q itself (the same address and
+ * strides).  Errors as gdn_attention_prefill_paged.
  */
 int gdn_attention_decode_paged(const gdn_attention_dims_t* dims, const gdn_rows_t* q,
                                const gdn_kv_cache_t* cache, const gdn_rows_t* out, float* lse,

@@ -254,7 +254,7 @@ def attention_prefill_paged(q, cu_seqlens, k_cache, v_cache, page_indices, page_
     Sequence b's new tokens (rows ``cu_seqlens[b] ..``) are the last of those it holds, already
     appended.  A row sees the tokens up to its own (``causal``) and, with ``window``, only the
     last ``window`` of them; ``softcap`` bounds the scores by ``softcap * tanh(x / softcap)``;
-    ``scale`` defaults to 1/sqrt(D)."""
+    ``scale`` defaults to 1/sqrt(D).  ``out`` must not share memory with q."""
     return _attention("prefill", q, cu_seqlens, k_cache, v_cache, page_indices, page_indptr, page_size,
                       last_page_len, scale, softcap, window, causal, return_lse, out, workspace)
 
@@ -264,6 +264,7 @@ def attention_decode_paged(q, k_cache, v_cache, page_indices, page_indptr, page_
                            return_lse: bool = False, out: Optional[torch.Tensor] = None,
                            workspace: Optional[torch.Tensor] = None):
     """``attention_prefill_paged`` for one token per sequence: q [B, Hq, D], row b at the last
-    position of sequence b (a sequence without a page gives zeros and an lse of -inf)."""
+    position of sequence b (a sequence without a page gives zeros and an lse of -inf).  ``out`` may
+    be q."""
     return _attention("decode", q, None, k_cache, v_cache, page_indices, page_indptr, page_size,
                       last_page_len, scale, softcap, window, True, return_lse, out, workspace)

@@ -723,6 +723,38 @@ bool aligned(const gdn_kv_cache_t* c, int32_t heads, int size, int bytes) {
          (heads < 2 || c->head_stride * size % bytes == 0);
 }
 
+// Whether rows of a and of b, each [tokens, heads, dim] of `size` bytes a value,
+// share memory.  Exact where the strides agree (one buffer's interleaved parts do not
+// share any), otherwise whether their spans do.
+bool share_memory(const gdn_rows_t* a, const gdn_rows_t* b, int64_t tokens, int32_t heads, int32_t dim, int size) {
+  typedef __int128 Wide;
+  struct Span {
+    Wide lo, hi;
+  };
+  auto stride = [&](int64_t s, int64_t n) { return n > 1 ? (Wide)s * size : (Wide)0; };  // (one row: any stride)
+  auto span = [&](const gdn_rows_t* r) {
+    const Wide t = (tokens - 1) * stride(r->token_stride, tokens), h = (heads - 1) * stride(r->head_stride, heads);
+    const Wide at = (Wide)(uintptr_t)r->data;
+    return Span{at + std::min<Wide>(t, 0) + std::min<Wide>(h, 0),
+                at + std::max<Wide>(t, 0) + std::max<Wide>(h, 0) + (Wide)dim * size};
+  };
+  const Span x = span(a), y = span(b);
+  if (x.hi <= y.lo || y.hi <= x.lo) return false;
+  const Wide ts = stride(a->token_stride, tokens), hs = stride(a->head_stride, heads);
+  if (ts != stride(b->token_stride, tokens) || hs != stride(b->head_stride, heads)) return true;
+  // rows i tokens and j heads apart: do they lie less than a row from each other for any i, j
+  const Wide apart = (Wide)(uintptr_t)b->data - (Wide)(uintptr_t)a->data, row = (Wide)dim * size;
+  for (int64_t j = 1 - heads; j < heads; ++j) {
+    const Wide r = apart + j * hs;
+    const Wide near_ = ts ? -r / ts : 0;  // (the i that brings them closest is this one or beside it)
+    for (Wide i = near_ - 1; i <= near_ + 1; ++i) {
+      const Wide gap = r + i * ts;
+      if (i > -tokens && i < tokens && gap < row && -gap < row) return true;
+    }
+  }
+  return false;
+}
+
 int check_rows(const gdn_rows_t* r, const char* name, int64_t tokens) {
   if (!r) return fail(GDN_EINVAL, "%s must not be NULL", name);
   if (tokens > 0 && !r->data) return fail(GDN_EINVAL, "%s has no data", name);
@@ -811,6 +843,13 @@ int run_attention(const gdn_attention_dims_t* dims, const gdn_rows_t* q, const i
   const size_t need = gdn_attention_workspace_size(dims, T, cache->num_seqs);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(GDN_EWORKSPACE, "workspace needs %zu bytes, got %zu", need, workspace ? workspace_bytes : 0);
+  // Workgroups read rows of q until the last ones have written theirs; in decode one wave reads a row, and
+  // writes it last.
+  const bool same = q->data == out->data && (T < 2 || q->token_stride == out->token_stride) &&
+                    (dims->num_q_heads < 2 || q->head_stride == out->head_stride);
+  if (!(same && !cu) && share_memory(q, out, T, dims->num_q_heads, dims->head_dim, 2))
+    return fail(GDN_EINVAL, cu ? "out must not share memory with q"
+                               : "out must be q itself or not share memory with it");
   AttnParams p{};
   p.q = rows_dev(q);
   p.o = rows_dev(out);
