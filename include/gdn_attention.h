@@ -171,7 +171,7 @@ typedef struct {
 /*
  * Workspace bytes of either attention call for at most total_tokens query rows
  * in at most num_seqs sequences (an upper bound that never decreases as either
- * grows).  0 on bad dims.
+ * grows), 256-byte aligned.  0 on bad dims.
  */
 size_t gdn_attention_workspace_size(const gdn_attention_dims_t* dims, int64_t total_tokens,
                                     int32_t num_seqs);

@@ -841,8 +841,9 @@ int run_attention(const gdn_attention_dims_t* dims, const gdn_rows_t* q, const i
   if (!aligned(cache, dims->num_kv_heads, 2, 16))
     return fail(GDN_EINVAL, "rows of the cache must be 16-byte aligned");
   const size_t need = gdn_attention_workspace_size(dims, T, cache->num_seqs);
-  if (need > 0 && (!workspace || workspace_bytes < need))
-    return fail(GDN_EWORKSPACE, "workspace needs %zu bytes, got %zu", need, workspace ? workspace_bytes : 0);
+  if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255))
+    return fail(GDN_EWORKSPACE, "workspace needs %zu bytes, 256-byte aligned (got %zu)", need,
+                workspace ? workspace_bytes : 0);
   // Workgroups read rows of q until the last ones have written theirs; in decode one wave reads a row, and
   // writes it last.
   const bool same = q->data == out->data && (T < 2 || q->token_stride == out->token_stride) &&
