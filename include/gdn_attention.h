@@ -111,7 +111,8 @@ int gdn_rope_table(const gdn_rope_scaling_t* scaling, float* table, int64_t rows
  * none) at the given positions into q_out and k_out, which may be the inputs.
  *   positions [num_tokens], int32, or int64 when index_dtype is GDN_INDEX_INT64.
  * Errors: GDN_EINVAL (null pointers, negative sizes, head_dim < 1, rot_dim odd
- * or outside 2 .. head_dim, unknown types), GDN_ELAUNCH.
+ * or outside 2 .. head_dim, unknown types; more than 65536 heads, a head_dim over
+ * 65536, or so many values a token that its threads pass 2^31), GDN_ELAUNCH.
  */
 int gdn_rope(const gdn_rope_t* rope, int32_t dtype, int32_t head_dim, int32_t num_q_heads,
              int32_t num_k_heads, int64_t num_tokens, const void* positions, int32_t index_dtype,

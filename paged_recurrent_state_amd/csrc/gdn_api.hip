@@ -805,6 +805,15 @@ bool rope_pieces(const RopeParams& p, const gdn_rope_t* r, int width) {
          (!r || (r->rot_dim % (2 * width) == 0 && (uintptr_t)r->table % std::min(16, 4 * width) == 0));
 }
 
+// (the kernel numbers a token's threads in 31 bits)
+int check_token_threads(const RopeParams& p, int width) {
+  const int64_t threads = (int64_t)(p.Hq + p.Hk + p.Hv) * rope_units(p, width);
+  if (threads >= (int64_t(1) << 31))
+    return fail(GDN_EINVAL, "heads times head_dim are too many: a token takes %lld threads, 2^31 - 1 at most",
+                (long long)threads);
+  return GDN_OK;
+}
+
 void set_rope(RopeParams& p, const gdn_rope_t* r) {
   if (!r) return;
   p.table = r->table;
@@ -949,6 +958,7 @@ int gdn_rope(const gdn_rope_t* rope, int32_t dtype, int32_t head_dim, int32_t nu
            (!num_k_heads || (aligned(k, num_tokens, num_k_heads, sz, bytes) && aligned(k_out, num_tokens, num_k_heads, sz, bytes)));
   };
   const int width = sz == 2 && fits(8) ? 8 : fits(4) ? 4 : fits(2) ? 2 : 1;
+  if (int rc = check_token_threads(p, width)) return rc;
   if (int rc = launched(launch_rope(p, dtype, rope->interleaved != 0, width, stream), "rotary kernel")) return rc;
   return ok();
 }
@@ -995,6 +1005,7 @@ int gdn_kv_append_paged(const gdn_rope_t* rope, int32_t dtype, int32_t head_dim,
            (!q || (aligned(q, total_tokens, Hq, sz, bytes) && aligned(q_out, total_tokens, Hq, sz, bytes)));
   };
   const int width = sz == 2 && fits(8) ? 8 : fits(4) ? 4 : fits(2) ? 2 : 1;
+  if (int rc = check_token_threads(p, width)) return rc;
   if (int rc = launched(launch_rope(p, dtype, rope && rope->interleaved != 0, width, stream), "append kernel")) return rc;
   return ok();
 }

@@ -215,6 +215,8 @@ struct RopeParams {
   FastDiv row_units;   // threads a row takes
 };
 // width: values of a piece (8, 4, 2, or 1: one pair a thread)
+// Threads a row takes; a token's are fewer than 2^31.
+inline int rope_units(const RopeParams& p, int width) { return width > 1 ? p.D / (2 * width) : p.D - p.rot / 2; }
 hipError_t launch_rope(RopeParams p, int dtype, bool interleaved, int width, hipStream_t s);
 hipError_t launch_rope_table(float* table, int64_t rows, int rot, double base, double factor, int bands,
                              double original, double low, double high, double magnitude, hipStream_t s);

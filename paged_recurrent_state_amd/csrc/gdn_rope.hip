@@ -286,7 +286,7 @@ void launch_rope_type(const RopeParams& p, bool near_, int width, dim3 grid, hip
 hipError_t launch_rope(RopeParams p, int dtype, bool interleaved, int width, hipStream_t s) {
   const int H = p.Hq + p.Hk + p.Hv;
   if (p.T == 0 || H == 0) return hipSuccess;
-  const int units = width > 1 ? p.D / (2 * width) : p.D - p.rot / 2;
+  const int units = rope_units(p, width);
   p.heads = fast_div(H);
   p.row_units = fast_div(units);
   // two rounds of the workgroup's threads (one 72, two 72, four 74, eight 82 us for the prompts)
