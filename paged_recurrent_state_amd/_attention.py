@@ -128,7 +128,49 @@ def rope(q, k, table, positions, interleaved: bool = False, transposed: bool = F
 
     ``table`` [positions, rot_dim] from ``rope_table``: the first ``rot_dim`` values of a head turn
     in pairs (i, i + rot_dim/2), or (2i, 2i + 1) with ``interleaved``.  ``transposed`` applies the
-    transposed map.  A position outside the table gives NaN."""
+    transposed map.  A position outside the table gives NaN.
+
+    q and k that require a gradient get it (the opposite map of the outputs' gradients); they and
+    ``q_out`` or ``k_out`` exclude each other, and the table has no gradient."""
+    # (asked first and without a call: at one token the host's time is all there is)
+    if torch.is_grad_enabled() and (
+            getattr(q, "requires_grad", False) or getattr(k, "requires_grad", False)
+            or getattr(table, "requires_grad", False) or getattr(q_out, "requires_grad", False)
+            or getattr(k_out, "requires_grad", False)):
+        if table.requires_grad:
+            raise RuntimeError("rope: the table has no gradient")
+        if q_out is not None or k_out is not None:
+            raise RuntimeError("rope: q_out and k_out take no part in automatic differentiation")
+        return _Rope.apply(q, k, table, positions, interleaved, transposed)
+    return _rope_rows(q, k, table, positions, interleaved, transposed, q_out, k_out)
+
+
+class _Rope(torch.autograd.Function):
+    """``rope`` and its gradient, which is linear: the opposite map of the outputs' gradients."""
+
+    @staticmethod
+    def forward(ctx, q, k, table, positions, interleaved, transposed):
+        ctx.save_for_backward(table, positions)
+        ctx.map = interleaved, transposed
+        ctx.set_materialize_grads(False)
+        return _rope_rows(q, k, table, positions, interleaved, transposed, None, None)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        table, positions = ctx.saved_tensors
+        interleaved, transposed = ctx.map
+        # (a gradient that was broadcast, as a sum's, is laid out first)
+        rows = [g if g is None or g.stride(-1) == 1 or g.shape[-1] == 1 else g.contiguous() for g in (dq, dk)]
+        given = [g for g in rows if g is not None]
+        turned = iter(())
+        if given:
+            turned = iter(rope(given[0], given[1] if len(given) > 1 else None, table, positions, interleaved,
+                               not transposed))
+        dq, dk = (None if g is None else next(turned) for g in rows)
+        return dq, dk, None, None, None, None
+
+
+def _rope_rows(q, k, table, positions, interleaved, transposed, q_out, k_out):
     lib = load()
     code, dev = _dtype(q, "q"), q.device
     stream = _stream(dev)
@@ -171,7 +213,8 @@ def kv_append_paged(k, v, cu_seqlens, k_cache, v_cache, page_indices, page_indpt
                     q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
                     ) -> Optional[torch.Tensor]:
     """Write the new tokens' k and v [T, Hkv, D] to the paged caches [pages, page_size, Hkv, D]
-    (any strides, the last dimension dense), in one launch.
+    (any strides, the last dimension dense), in one launch (no gradient: a serving call, as the
+    attention calls on these caches).
 
     ``table`` (``rope_table``) rotates the keys on the way, and ``q`` [T, Hq, D], when given, into
     ``q_out`` (returned; a new tensor unless given).  The page table is the one after the
