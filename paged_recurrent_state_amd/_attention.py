@@ -265,8 +265,11 @@ def _attention(fn, q, cu_seqlens, k_cache, v_cache, page_indices, page_indptr, p
     qr = _rows(q, "q", q.dtype, dev)
     T, Hq, D = q.shape
     cache = _cache(k_cache, v_cache, page_indices, page_indptr, int(page_size), last_page_len, q.dtype, dev, D)
-    d = _AttentionC(Hq, k_cache.shape[2], D, code, float(scale) if scale else 0.0,
-                    float(softcap) if softcap else 0.0, int(window), bool(causal))
+    # (the library takes what is not positive for its defaults)
+    scale, softcap = 0.0 if scale is None else float(scale), 0.0 if softcap is None else float(softcap)
+    if scale < 0.0 or softcap < 0.0:
+        raise ValueError(f"scale and softcap must not be negative, got {scale} and {softcap}")
+    d = _AttentionC(Hq, k_cache.shape[2], D, code, scale, softcap, int(window), bool(causal))
     if out is None:
         out, o = _dense((T, Hq, D), q.dtype, dev)
     else:
@@ -296,8 +299,8 @@ def attention_prefill_paged(q, cu_seqlens, k_cache, v_cache, page_indices, page_
 
     Sequence b's new tokens (rows ``cu_seqlens[b] ..``) are the last of those it holds, already
     appended.  A row sees the tokens up to its own (``causal``) and, with ``window``, only the
-    last ``window`` of them; ``softcap`` bounds the scores by ``softcap * tanh(x / softcap)``;
-    ``scale`` defaults to 1/sqrt(D).  ``out`` must not share memory with q."""
+    last ``window`` of them; ``softcap`` bounds the scores by ``softcap * tanh(x / softcap)`` (0: no
+    bound); ``scale`` defaults to 1/sqrt(D) (None or 0).  Neither may be negative.  ``out`` must not share memory with q."""
     return _attention("prefill", q, cu_seqlens, k_cache, v_cache, page_indices, page_indptr, page_size,
                       last_page_len, scale, softcap, window, causal, return_lse, out, workspace)
 
