@@ -119,7 +119,10 @@ class Model:
 
 
 def generate(prompts, chunk, tokens, seed=0, device="cuda", **kw):
-    """(logits after the prompts, decoded tokens [B, tokens], logits after the last, the time of a decoded token)"""
+    """(logits after the prompts, decoded tokens [B, tokens] (None: none asked for), logits after the last, the
+    time of a decoded token)"""
+    if not prompts or min(len(t) for t in prompts) < 1 or chunk < 1 or tokens < 0:
+        raise ValueError("at least one prompt, of one token or more, chunks of one or more, and no fewer than 0 tokens")
     page_size = kw.setdefault("page_size", 128)
     need = sum(-(-(len(t) + tokens) // page_size) for t in prompts)
     model = Model(pages=need, device=device, seed=seed, positions=max(len(t) for t in prompts) + tokens, **kw)
@@ -137,14 +140,16 @@ def generate(prompts, chunk, tokens, seed=0, device="cuda", **kw):
     return first, torch.stack(out, dim=1) if out else None, logits, each
 
 
-def main():
+def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("--prompts", type=int, nargs="+", default=[700, 130, 1])
     ap.add_argument("--chunk", type=int, default=256)
     ap.add_argument("--tokens", type=int, default=8)
     ap.add_argument("--window", type=int, default=0)
     ap.add_argument("--softcap", type=float, default=0.0)
-    a = ap.parse_args()
+    a = ap.parse_args(argv)
+    if min(a.prompts) < 1 or a.chunk < 1 or a.tokens < 0:
+        ap.error("prompts and chunks have one token or more, and --tokens is 0 or more")
     gen = torch.Generator().manual_seed(1)
     prompts = [torch.randint(0, 1024, (n,), generator=gen).to("cuda") for n in a.prompts]
     kw = dict(window=a.window, softcap=a.softcap)
@@ -152,9 +157,10 @@ def main():
     whole = generate(prompts, max(a.prompts), 0, **kw)[0]
     diff = ((first - whole).float().norm() / whole.float().norm()).item()
     print(f"{len(prompts)} prompts in chunks of {a.chunk}: logits within {diff:.1e} of the prompts fed whole")
-    print(f"{a.tokens} tokens decoded, {1e3 * each:.2f} ms each")
-    for t in out.tolist():
-        print(" ", *t)
+    if out is not None:
+        print(f"{a.tokens} tokens decoded, {1e3 * each:.2f} ms each")
+        for t in out.tolist():
+            print(" ", *t)
 
 
 if __name__ == "__main__":
