@@ -68,7 +68,8 @@ def _cache(k_cache, v_cache, page_indices, page_indptr, page_size, last_page_len
     if v_cache.shape != k_cache.shape:
         raise ValueError(f"v_cache must have the shape of k_cache, got {tuple(v_cache.shape)}")
     stride = k_cache.stride()
-    if v_cache.stride() != stride:
+    # (a dimension of one has no step, whatever its stride says)
+    if v_cache.stride() != stride and any(a != b and n > 1 for a, b, n in zip(stride, v_cache.stride(), k_cache.shape)):
         raise ValueError("k_cache and v_cache must have the same strides")
     if stride[3] != 1 and dim > 1:
         raise ValueError("the last dimension of the caches must be dense")
@@ -81,7 +82,7 @@ def _cache(k_cache, v_cache, page_indices, page_indptr, page_size, last_page_len
     # an empty tensor has no storage: a stand-in that is never read
     idx = page_indices if page_indices.numel() else page_indptr
     k, v = (c if c.numel() else page_indptr for c in (k_cache, v_cache))
-    return _CacheC(k.data_ptr(), v.data_ptr(), stride[0], stride[1], stride[2], page_size, B,
+    return _CacheC(k.data_ptr(), v.data_ptr(), stride[0] if k_cache.shape[0] > 1 else 0, stride[1], stride[2], page_size, B,
                    idx.data_ptr(), page_indptr.data_ptr(), last_page_len.data_ptr())
 
 
