@@ -285,6 +285,12 @@ def _workspace(ws, nbytes, dev):
     if ws is None:
         # 256-byte aligned: torch's caching allocator returns 512-byte aligned blocks
         return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+    if not isinstance(ws, torch.Tensor):
+        raise TypeError("workspace must be a tensor")
+    if ws.device != dev:
+        raise ValueError(f"workspace is on {ws.device}, expected {dev}")
+    if not ws.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     if ws.numel() * ws.element_size() < nbytes:
         raise ValueError(f"workspace needs {nbytes} bytes")
     return ws
