@@ -11,8 +11,8 @@
  * The page table is the CSR form of the recurrent layers: sequence b owns the
  * pages page_indices[page_indptr[b] .. page_indptr[b+1]) and holds, after the
  * call's new tokens, (pages - 1) * page_size + last_page_len[b] tokens (none
- * when it has no page).  Its n new tokens are the last n of them.  Any
- * page_size >= 1 is served.
+ * when it has no page; fewer than 2^31 - 4096 in all).  Its n new tokens are the
+ * last n of them.  Any page_size >= 1 is served.
  */
 #ifndef GDN_ATTENTION_H
 #define GDN_ATTENTION_H
@@ -182,8 +182,8 @@ size_t gdn_attention_workspace_size(const gdn_attention_dims_t* dims, int64_t to
  * cu_seqlens[b] .. cu_seqlens[b+1], any count per sequence, none included) over
  * everything their sequences hold in the cache, the new tokens themselves
  * among it: append first, then attend.
- *   out: rows of total_tokens tokens that share no memory with q;
- *   lse [total_tokens, num_q_heads] or NULL.
+ *   out: rows of total_tokens tokens that share no memory with q (with strides other
+ *   than q's: nor lie among its rows); lse [total_tokens, num_q_heads] or NULL.
  * Errors: GDN_EINVAL (null pointers, negative sizes or window, page_size < 1,
  * rows or a cache that are not 16-byte aligned in every stride and address, out
  * over q),

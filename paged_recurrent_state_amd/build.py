@@ -68,7 +68,7 @@ def _compile(src: str, csrc: str = CSRC, objdir: str = OBJDIR) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed on {src}:\n{r.stderr}")
-    # the kernels are laid out to fit the registers (the chunk attention's instances take up to 477 of 512):
+    # the kernels are laid out to fit the registers (the chunk attention's instances take up to 472 of 512):
     # one that no longer does is an error of its source, not only slower
     if bad := spills(r.stderr):
         os.remove(obj)

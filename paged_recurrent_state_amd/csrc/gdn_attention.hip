@@ -218,14 +218,18 @@ __device__ __forceinline__ float score(const AttnParams& p, float x) {
 // Bound by the matrix unit and, beside it, the vector operations: at D 128 a wave
 // has 64 products of 32 cycles a tile, and beside them 64 exponentials of 12 cycles
 // and 167 other operations of 4 to 8.
-// Measured, bf16: 2,048 tokens over 32,768, 32 q-heads on 8 of 128 values, 928 us,
-// 1,222 TFLOP/s (a library matrix product of 8192^3 reaches 1,347); 4 ragged
-// prompts, 16 q-heads on 2 of 256 values, 232 us, 955 TFLOP/s; 17 tokens over 1,000
-// 21 us, most of it start and join.
+// Measured over several cards, bf16: 2,048 tokens over 32,768, 32 q-heads on 8 of 128
+// values, 911 to 959 us, 1,182 to 1,244 TFLOP/s (a library matrix product of 8192^3
+// reaches 1,347), of 64 values 600 to 605 us, 938 to 943; 4 ragged prompts, 16 q-heads
+// on 2 of 256 values, 231 to 244 us, 909 to 960; 17 tokens over 1,000 21 us, most of
+// it start and join.  In fp16, whose references move: 1,040 to 1,096 us (1,034 to
+// 1,090 TFLOP/s), 655 to 670 and 252 to 261.
 //
 // Weights enter the product with V rounded to the element type: a second product
 // for what the rounding loses would cost a third of the time, and the rounding adds
-// 1.5e-3 of the output (bf16; in the mean) to the 1.6e-3 of the output's own.
+// 1.5e-3 of the output (bf16; in the mean) to the 1.6e-3 of the output's own.  In fp16
+// it adds 1.7e-4 to 2.1e-4, and besides up to 2^-32 of the row's sum a weight, the
+// type's least step: 2^17 keys that share 2% of a row are off by 1.5e-3 at most.
 
 // Sizes of the chunk kernel.
 template <int D>
@@ -1159,7 +1163,7 @@ hipError_t launch_chunk(AttnParams p, void* workspace, hipStream_t s) {
   p.records = w.tiles * p.Hkv <= device_cus() ? (int)w.tiles * p.Hkv : 0;
   // A wave's rows of a tile start at a multiple of 16 (or 8) keys: pages of a multiple of 16 tokens hold
   // them whole, and a load goes by one place and 32-bit offsets; otherwise every row's place is staged
-  // (1,024 tokens over 8,192, pages of 64 and of 100: 152 and 156 us at D 128; with its
+  // (1,024 tokens over 8,192, pages of 64 and of 100: 147 and 153 us at D 128; with its
   // tiles checked like the last ones, 232).
   const bool even = p.kv.page.d % 16 == 0 && p.kv.ts >= 0 && p.kv.ts * p.kv.page.d < (int64_t(1) << 30);
   if (p.cap > kMostShort / kLn2)
@@ -1187,11 +1191,14 @@ hipError_t launch_chunk(AttnParams p, void* workspace, hipStream_t s) {
 // sum of two 16-bit parts (the matrix units idle anyway), so what it adds to the
 // output's own rounding is invisible.
 //
-// Bound by memory: 512 sequences of up to 4,096 tokens (3.09 GB) 512 us, 6.0 TB/s;
-// 4 of 131,072 tokens 353 us, 6.1 TB/s (a copy reaches 5.7 to 6.0).  Where runs are
-// short their start (page table, page ids, first keys) shows: 512 sequences of up to
-// 150 tokens on 8 heads 38 us, against 62 when four waves shared each run and
-// waited for each other; long runs lose 1% to the parts they write.
+// Bound by memory: 512 sequences of up to 4,096 tokens (3.09 GB) 514 us, 6.0 TB/s, at
+// D 64 270 us, 5.7 TB/s, at D 256 on 4 heads 523 us, 5.9 TB/s; 4 of 131,072 tokens
+// 355 us, 6.0 TB/s (a copy reaches 5.7 to 6.0).  Where runs are short their start
+// (page table, page ids, first keys) shows: 512 sequences of up to 150 tokens on 8
+// heads 38 us, against 62 when four waves shared each run and waited for each other;
+// long runs lose 1% to the parts they write.  A run holds 16 query rows: more q-heads
+// on a kv-head read its keys and values again for every 16 (64 sequences of up to
+// 8,192 tokens, 16 and 32 q-heads on one: 62 and 106 us).
 
 constexpr int kDecTile = 32;   // keys of a tile
 constexpr int kDecRows = 16;   // query rows of a run
@@ -1640,8 +1647,8 @@ hipError_t launch_decode_cap(const AttnParams& p, hipStream_t s) {
   decode_kernel<E, D, CAP><<<dim3(shares / kWaves), dim3(64 * kWaves), kDecLds<D>, s>>>(p);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int rows = std::min<int>(kDecRows, (int)p.group.d), groups = 1024 / D;
-  // (runs of 4 parts and fewer by rows: 64 sequences of 2,000 tokens on 8 heads 40 us in all, 44 by values;
-  // runs of 8 parts and more by values: 32 of 8,000 on 8 heads 48 us, 52 by rows)
+  // (runs of 4 parts and fewer by rows: 64 sequences of up to 2,000 tokens on 8 heads 40 us in all, 44 by
+  // values; runs of 8 parts and more by values: 32 of up to 8,000 on 8 heads 48 us, 52 by rows)
   if (p.records && 8 * p.records <= shares)
     decode_join_kernel<E, D, true><<<dim3(p.records, rows, D / 32), dim3(256), 0, s>>>(p);
   else
