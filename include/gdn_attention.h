@@ -120,6 +120,52 @@ int gdn_rope(const gdn_rope_t* rope, int32_t dtype, int32_t head_dim, int32_t nu
              const gdn_rows_t* k_out, hipStream_t stream);
 
 /*
+ * Norms of query and key heads, before the rotation: a head's row x becomes
+ *     x (sum x^2 / head_dim + eps)^(-1/2) (offset + weight),
+ * sums in fp32, with one rounding after the rotation.  head_dim at most 512.
+ */
+typedef struct {
+  const void* q_weight; /* [head_dim], any alignment; NULL: queries are not normed */
+  const void* k_weight; /* [head_dim]; NULL: keys are not normed */
+  int32_t weight_dtype; /* the rows' type, or GDN_TYPE_F32 */
+  float eps;            /* >= 0 */
+  float offset;
+} gdn_norm_t;
+
+/*
+ * gdn_norm_rope -- gdn_rope of the normed rows of q and k, in one pass.  q_out
+ * and k_out may be the inputs.  Errors as gdn_rope, and GDN_EINVAL for a null
+ * norm, a null weight of a tensor that has heads, a weight_dtype that is neither
+ * the rows' nor fp32, eps < 0 or not finite, offset not finite;
+ * GDN_EUNSUPPORTED for a head_dim over 512.
+ */
+int gdn_norm_rope(const gdn_norm_t* norm, const gdn_rope_t* rope, int32_t dtype, int32_t head_dim,
+                  int32_t num_q_heads, int32_t num_k_heads, int64_t num_tokens, const void* positions,
+                  int32_t index_dtype, const gdn_rows_t* q, const gdn_rows_t* k,
+                  const gdn_rows_t* q_out, const gdn_rows_t* k_out, hipStream_t stream);
+
+/*
+ * gdn_norm_rope_backward -- from the inputs q and k of a gdn_norm_rope call and
+ * the gradients of its outputs, those of q and k (q_grad, k_grad: rows that may
+ * lie over the inputs' or the outputs' gradients', with the same strides, and
+ * otherwise share no memory with them) and of the weights (q_weight_grad,
+ * k_weight_grad: [head_dim] of the weights' type, sums over all rows in fp32 in
+ * an order that the sizes fix, so equal inputs give equal sums; zeros for no
+ * tokens).  The workspace is 256-byte aligned, of
+ * gdn_norm_rope_backward_workspace_size bytes (0 on bad sizes).
+ * Errors as gdn_norm_rope, GDN_EWORKSPACE.
+ */
+size_t gdn_norm_rope_backward_workspace_size(int32_t head_dim, int32_t num_q_heads,
+                                             int32_t num_k_heads, int64_t num_tokens);
+int gdn_norm_rope_backward(const gdn_norm_t* norm, const gdn_rope_t* rope, int32_t dtype,
+                           int32_t head_dim, int32_t num_q_heads, int32_t num_k_heads,
+                           int64_t num_tokens, const void* positions, int32_t index_dtype,
+                           const gdn_rows_t* q, const gdn_rows_t* k, const gdn_rows_t* q_out_grad,
+                           const gdn_rows_t* k_out_grad, const gdn_rows_t* q_grad,
+                           const gdn_rows_t* k_grad, void* q_weight_grad, void* k_weight_grad,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
  * gdn_kv_append_paged -- writes the keys and values of a batch's new tokens to
  * the cache, the keys rotated on the way when `rope` is not NULL, and rotates
  * the queries of the same tokens into q_out in the same launch when q is not
@@ -137,6 +183,63 @@ int gdn_kv_append_paged(const gdn_rope_t* rope, int32_t dtype, int32_t head_dim,
                         int64_t total_tokens, const gdn_rows_t* k, const gdn_rows_t* v,
                         const gdn_kv_cache_t* cache, const gdn_rows_t* q, const gdn_rows_t* q_out,
                         hipStream_t stream);
+
+/*
+ * A cache of 8 bits: the gdn_kv_cache_t holds e4m3 codes (1 sign, 4 exponent, 3
+ * fraction bits; no infinities), its strides in codes, rows 16-byte aligned, and
+ * a value is its code times the scale of its block of `block` tokens of a page
+ * and head: scale j of head h of page p, for the tokens j * block .. of the page,
+ * is at k (or v) + p * page_stride + j * block_stride + h * head_stride.  Scales
+ * are powers of two between 2^-100 and 2^120, as the append writes them; readers
+ * take nothing else.  The block is a multiple of 16 tokens that divides the page.
+ */
+typedef struct {
+  float* k;
+  float* v;
+  int64_t page_stride;
+  int64_t block_stride;
+  int64_t head_stride;
+  int32_t block;
+} gdn_kv_scales_t;
+
+/*
+ * gdn_kv_append_paged_ext -- gdn_kv_append_paged with the queries and keys normed
+ * before the rotation (norm; NULL: neither) and, where scales is not NULL, into a
+ * cache of 8 bits.  There a block's scale is the least power of two with which
+ * the largest magnitude of the new tokens' (normed, rotated) values in it is at
+ * most 448, and no less than the block's own where tokens before them lie in it:
+ * if the scale grows their codes are rounded to the new one.  A block that the
+ * new tokens open takes a new scale, whatever it held.  A value is rounded once,
+ * to nearest, ties to even; values that are not finite are stored as NaN and count
+ * for no scale, and from fp16 rows no magnitude over 61,440 is stored (the next code
+ * is beyond fp16).  Rows and slots behind the new tokens are left as they are.
+ * Errors as gdn_kv_append_paged and gdn_norm_rope (but that a null weight leaves
+ * its heads as they are), GDN_EINVAL for null or unaligned scales, a bad block,
+ * or a cache that is not 16-byte aligned in every stride and address;
+ * GDN_EUNSUPPORTED for an 8-bit cache of fp32 rows, of heads other than 64, 128
+ * or 256, of rows that are not 4-byte aligned, or with a rot_dim that is not a
+ * multiple of 4.
+ */
+int gdn_kv_append_paged_ext(const gdn_norm_t* norm, const gdn_rope_t* rope, int32_t dtype,
+                            int32_t head_dim, int32_t num_q_heads, int32_t num_kv_heads,
+                            const int32_t* cu_seqlens, int64_t total_tokens, const gdn_rows_t* k,
+                            const gdn_rows_t* v, const gdn_kv_cache_t* cache,
+                            const gdn_kv_scales_t* scales, const gdn_rows_t* q,
+                            const gdn_rows_t* q_out, hipStream_t stream);
+
+/*
+ * gdn_kv_read_paged -- the last tokens of each sequence, as the append counts its
+ * new ones, back from a cache of 8 bits: rows cu_seqlens[b] .. of k and v (of
+ * `dtype`, 16-byte aligned) get the values of the last cu_seqlens[b+1] -
+ * cu_seqlens[b] tokens of sequence b (cu_seqlens NULL: one each), exact in bf16 and
+ * fp32 and rounded in fp16.  A row whose sequence holds fewer tokens is zeros, rows
+ * behind the last sequence are left as they are.
+ * Errors as gdn_kv_append_paged_ext.
+ */
+int gdn_kv_read_paged(int32_t dtype, int32_t head_dim, int32_t num_kv_heads,
+                      const int32_t* cu_seqlens, int64_t total_tokens, const gdn_kv_cache_t* cache,
+                      const gdn_kv_scales_t* scales, const gdn_rows_t* k, const gdn_rows_t* v,
+                      hipStream_t stream);
 
 /*
  * What the attention calls compute, for query row i (position t in its
@@ -204,6 +307,28 @@ int gdn_attention_prefill_paged(const gdn_attention_dims_t* dims, const gdn_rows
 int gdn_attention_decode_paged(const gdn_attention_dims_t* dims, const gdn_rows_t* q,
                                const gdn_kv_cache_t* cache, const gdn_rows_t* out, float* lse,
                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The same calls with first tokens that stay visible beside a window, and over
+ * caches of 8 bits.
+ *   sinks: with a window a row sees token j <= t (causal) also if j < sinks.
+ *     Without one it means nothing.
+ *   scales: of an 8-bit cache, or NULL for one of dims->dtype.  The result is that
+ *     of a cache that holds the values, code times scale, rounded to dims->dtype
+ *     (exact in bf16; in fp16 magnitudes over 65,504 become infinite).
+ * Errors as the calls above, and GDN_EINVAL for sinks < 0 or over 2^30, null or
+ * unaligned scales or a bad block; GDN_EUNSUPPORTED for chunks over an 8-bit cache
+ * whose token stride is negative or reaches 2^30 / page_size.
+ */
+int gdn_attention_prefill_paged_ext(const gdn_attention_dims_t* dims, int32_t sinks,
+                                    const gdn_rows_t* q, const int32_t* cu_seqlens,
+                                    int64_t total_tokens, const gdn_kv_cache_t* cache,
+                                    const gdn_kv_scales_t* scales, const gdn_rows_t* out, float* lse,
+                                    void* workspace, size_t workspace_bytes, hipStream_t stream);
+int gdn_attention_decode_paged_ext(const gdn_attention_dims_t* dims, int32_t sinks,
+                                   const gdn_rows_t* q, const gdn_kv_cache_t* cache,
+                                   const gdn_kv_scales_t* scales, const gdn_rows_t* out, float* lse,
+                                   void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -10,6 +10,9 @@ from ._attention import (  # noqa: F401
     attention_prefill_paged,
     attention_workspace_size,
     kv_append_paged,
+    kv_read_paged,
+    norm_rope,
+    norm_rope_backward,
     rope,
     rope_backward,
     rope_table,

@@ -88,6 +88,16 @@ class _ScalingC(C.Structure):
                 ("magnitude", C.c_double)]
 
 
+class _NormC(C.Structure):
+    _fields_ = [("q_weight", C.c_void_p), ("k_weight", C.c_void_p), ("weight_dtype", C.c_int32),
+                ("eps", C.c_float), ("offset", C.c_float)]
+
+
+class _ScalesC(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("page_stride", C.c_int64),
+                ("block_stride", C.c_int64), ("head_stride", C.c_int64), ("block", C.c_int32)]
+
+
 class _AttentionC(C.Structure):
     _fields_ = [("num_q_heads", C.c_int32), ("num_kv_heads", C.c_int32), ("head_dim", C.c_int32),
                 ("dtype", C.c_int32), ("scale", C.c_float), ("softcap", C.c_float),
@@ -126,7 +136,9 @@ EXPORTS = ["gdn_check_paged", "gdn_prefill_slots", "gdn_decode_slots", "gdn_pref
            "gdn_prefill_paged", "gdn_prefill_paged_noalloc", "gdn_decode_paged", "gdn_prefill", "gdn_decode",
            "gdn_block_table_to_csr", "gdn_csr_to_block_table", "gdn_stream_copy", "gdn_last_error",
            "gdn_version", "gdn_rope_table", "gdn_rope", "gdn_kv_append_paged", "gdn_attention_workspace_size",
-           "gdn_attention_prefill_paged", "gdn_attention_decode_paged"]
+           "gdn_attention_prefill_paged", "gdn_attention_decode_paged", "gdn_norm_rope",
+           "gdn_norm_rope_backward_workspace_size", "gdn_norm_rope_backward", "gdn_kv_append_paged_ext",
+           "gdn_kv_read_paged", "gdn_attention_prefill_paged_ext", "gdn_attention_decode_paged_ext"]
 
 
 def lib_path() -> str:
@@ -143,6 +155,7 @@ def load():
     lib = C.CDLL(_LIB_PATH)
     P, I32, I64, SZ = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
     R, KV, RP, AT = (C.POINTER(x) for x in (_RowsC, _CacheC, _RopeC, _AttentionC))
+    NM, SC = C.POINTER(_NormC), C.POINTER(_ScalesC)
     sig = {
         "gdn_check_paged": (C.c_int, [P, P, P, P, I32, I32, I32, P, P]),
         "gdn_prefill_slots": (C.c_int, [P, P, P, P, I32, I32, C.POINTER(_PrefillSlotsC), P]),
@@ -168,6 +181,13 @@ def load():
         "gdn_attention_workspace_size": (SZ, [AT, I64, I32]),
         "gdn_attention_prefill_paged": (C.c_int, [AT, R, P, I64, KV, R, P, P, SZ, P]),
         "gdn_attention_decode_paged": (C.c_int, [AT, R, KV, R, P, P, SZ, P]),
+        "gdn_norm_rope": (C.c_int, [NM, RP, I32, I32, I32, I32, I64, P, I32, R, R, R, R, P]),
+        "gdn_norm_rope_backward_workspace_size": (SZ, [I32, I32, I32, I64]),
+        "gdn_norm_rope_backward": (C.c_int, [NM, RP, I32, I32, I32, I32, I64, P, I32, R, R, R, R, R, R, P, P, P, SZ, P]),
+        "gdn_kv_append_paged_ext": (C.c_int, [NM, RP, I32, I32, I32, I32, P, I64, R, R, KV, SC, R, R, P]),
+        "gdn_kv_read_paged": (C.c_int, [I32, I32, I32, P, I64, KV, SC, R, R, P]),
+        "gdn_attention_prefill_paged_ext": (C.c_int, [AT, I32, R, P, I64, KV, SC, R, P, P, SZ, P]),
+        "gdn_attention_decode_paged_ext": (C.c_int, [AT, I32, R, KV, SC, R, P, P, SZ, P]),
         "gdn_last_error": (C.c_char_p, []),
         "gdn_version": (C.c_char_p, []),
     }

@@ -20,7 +20,8 @@ OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgdn_paged.so")
 
 SOURCES = ["gdn_slots.hip", "gdn_tables.hip", "gdn_check.hip", "gdn_prefill.hip", "gdn_decode.hip",
-           "gdn_copy.hip", "gdn_rope.hip", "gdn_attention.hip", "gdn_api.hip"]
+           "gdn_copy.hip", "gdn_rope.hip", "gdn_norm.hip", "gdn_quant.hip", "gdn_attention_bf16.hip", "gdn_attention_f16.hip",
+           "gdn_attention8_bf16.hip", "gdn_attention8_f16.hip", "gdn_attention.hip", "gdn_api.hip"]
 
 ARCH = "gfx950"
 FLAGS = [
@@ -34,7 +35,8 @@ FLAGS = [
 SOURCE_FLAGS = {
     # matrix products write to ordinary registers: the softmax works on the scores, and with the
     # accumulation registers as their destination every score is copied over first
-    "gdn_attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    f"gdn_attention{t}.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+    for t in ("_bf16", "_f16", "8_bf16", "8_f16")
 }
 
 

@@ -822,6 +822,38 @@ void set_rope(RopeParams& p, const gdn_rope_t* r) {
   p.sign = r->transposed ? -1.f : 1.f;
 }
 
+// Norms of heads: null ones are left out (n stays empty).
+int check_norm(const gdn_norm_t* norm, int32_t dtype, int32_t head_dim, NormDev& n) {
+  if (!norm) return GDN_OK;
+  if (norm->weight_dtype != dtype && norm->weight_dtype != GDN_TYPE_F32)
+    return fail(GDN_EINVAL, "norm.weight_dtype must be the rows' type or GDN_TYPE_F32 (got %d)", norm->weight_dtype);
+  if (!(norm->eps >= 0.f) || std::isinf(norm->eps) || !std::isfinite(norm->offset))
+    return fail(GDN_EINVAL, "norm.eps must be finite and >= 0, norm.offset finite");
+  if (head_dim > kNormMaxDim)
+    return fail(GDN_EUNSUPPORTED, "normed heads have at most %d values (got %d)", kNormMaxDim, head_dim);
+  n.wq = norm->q_weight;
+  n.wk = norm->k_weight;
+  n.wide = norm->weight_dtype == GDN_TYPE_F32;
+  n.eps = norm->eps;
+  n.offset = norm->offset;
+  return GDN_OK;
+}
+
+// The scales of an 8-bit cache, and the cache itself.
+int check_scales(const gdn_kv_scales_t* sc, const gdn_kv_cache_t* cache, int32_t heads, int32_t head_dim, ScalesDev& out) {
+  if (!sc) return fail(GDN_EINVAL, "scales is NULL");
+  if (cache->num_seqs > 0 && (!sc->k || !sc->v)) return fail(GDN_EINVAL, "the scales must not be NULL");
+  if (sc->block < 16 || sc->block % 16 || cache->page_size % sc->block)
+    return fail(GDN_EINVAL, "a scale's block must be a multiple of 16 tokens that divides the page (got %d of %d)", sc->block,
+                cache->page_size);
+  if ((uintptr_t)sc->k % 4 || (uintptr_t)sc->v % 4) return fail(GDN_EINVAL, "scales must be 4-byte aligned");
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256)
+    return fail(GDN_EUNSUPPORTED, "heads of an 8-bit cache have 64, 128 or 256 values (got %d)", head_dim);
+  if (!aligned(cache, heads, 1, 16)) return fail(GDN_EINVAL, "rows of the cache must be 16-byte aligned");
+  out = ScalesDev{sc->k, sc->v, sc->page_stride, sc->block_stride, sc->head_stride, fast_div((uint32_t)sc->block)};
+  return GDN_OK;
+}
+
 int check_attention(const gdn_attention_dims_t* d) {
   if (!d) return fail(GDN_EINVAL, "dims is NULL");
   if (d->num_q_heads < 1 || d->num_kv_heads < 1)
@@ -838,16 +870,142 @@ int check_attention(const gdn_attention_dims_t* d) {
   return GDN_OK;
 }
 
-int run_attention(const gdn_attention_dims_t* dims, const gdn_rows_t* q, const int32_t* cu, int64_t T,
-                  const gdn_kv_cache_t* cache, const gdn_rows_t* out, float* lse, void* workspace,
-                  size_t workspace_bytes, hipStream_t stream) {
+int rotate_rows(const gdn_norm_t* norm, const gdn_rope_t* rope, int32_t dtype, int32_t head_dim, int32_t num_q_heads, int32_t num_k_heads,
+                int64_t num_tokens, const void* positions, int32_t index_dtype, const gdn_rows_t* q,
+                const gdn_rows_t* k, const gdn_rows_t* q_out, const gdn_rows_t* k_out, hipStream_t stream) {
+  if (!rope) return fail(GDN_EINVAL, "rope is NULL");
+  if (int rc = check_type(dtype, true)) return rc;
+  if (int rc = check_heads(head_dim, num_q_heads, num_k_heads)) return rc;
+  if (int rc = check_rope(rope, head_dim)) return rc;
+  NormDev n{};
+  if (int rc = check_norm(norm, dtype, head_dim, n)) return rc;
+  if (norm && ((num_q_heads > 0 && !n.wq) || (num_k_heads > 0 && !n.wk)))
+    return fail(GDN_EINVAL, "norm weights must not be NULL");
+  if (int rc = check_token_count(num_tokens)) return rc;
+  if (index_dtype != GDN_INDEX_INT32 && index_dtype != GDN_INDEX_INT64)
+    return fail(GDN_EINVAL, "index_dtype must be GDN_INDEX_INT32 or GDN_INDEX_INT64");
+  if (num_tokens > 0 && !positions) return fail(GDN_EINVAL, "positions must not be NULL");
+  if (num_q_heads > 0) {
+    if (int rc = check_rows(q, "q", num_tokens)) return rc;
+    if (int rc = check_rows(q_out, "q_out", num_tokens)) return rc;
+  }
+  if (num_k_heads > 0) {
+    if (int rc = check_rows(k, "k", num_tokens)) return rc;
+    if (int rc = check_rows(k_out, "k_out", num_tokens)) return rc;
+  }
+  RopeParams p{};
+  set_rope(p, rope);
+  p.D = head_dim;
+  p.Hq = num_q_heads;
+  p.Hk = num_k_heads;
+  p.q = rows_dev(q);
+  p.k = rows_dev(k);
+  p.q_out = rows_dev(q_out);
+  p.k_out = rows_dev(k_out);
+  p.T = num_tokens;
+  p.pos = positions;
+  p.pos64 = index_dtype == GDN_INDEX_INT64;
+  p.kv.page = fast_div(1);
+  const int sz = type_size(dtype);
+  auto fits = [&](int width) {
+    const int bytes = width * sz;  // 16 at most
+    return rope_pieces(p, rope, width) &&
+           (!num_q_heads || (aligned(q, num_tokens, num_q_heads, sz, bytes) && aligned(q_out, num_tokens, num_q_heads, sz, bytes))) &&
+           (!num_k_heads || (aligned(k, num_tokens, num_k_heads, sz, bytes) && aligned(k_out, num_tokens, num_k_heads, sz, bytes)));
+  };
+  const int width = sz == 2 && fits(8) ? 8 : fits(4) ? 4 : fits(2) ? 2 : 1;
+  if (int rc = check_token_threads(p, width)) return rc;
+  if (norm) {
+    if (int rc = launched(launch_norm_rope(p, n, dtype, rope->interleaved != 0, width, stream), "norm kernel")) return rc;
+    return ok();
+  }
+  if (int rc = launched(launch_rope(p, dtype, rope->interleaved != 0, width, stream), "rotary kernel")) return rc;
+  return ok();
+}
+
+int append_rows(const gdn_norm_t* norm, const gdn_rope_t* rope, int32_t dtype, int32_t head_dim, int32_t num_q_heads,
+                        int32_t num_kv_heads, const int32_t* cu_seqlens, int64_t total_tokens,
+                        const gdn_rows_t* k, const gdn_rows_t* v, const gdn_kv_cache_t* cache,
+                        const gdn_kv_scales_t* scales, const gdn_rows_t* q, const gdn_rows_t* q_out,
+                        hipStream_t stream) {
+  if (int rc = check_type(dtype, true)) return rc;
+  if (scales && dtype == GDN_TYPE_F32) return fail(GDN_EUNSUPPORTED, "an 8-bit cache takes rows of 16-bit types (got GDN_TYPE_F32)");
+  const int32_t Hq = q ? num_q_heads : 0;
+  if (int rc = check_heads(head_dim, Hq, num_kv_heads)) return rc;
+  if (num_kv_heads < 1) return fail(GDN_EINVAL, "num_kv_heads must be positive (got %d)", num_kv_heads);
+  if (int rc = check_cache(cache)) return rc;
+  if (rope)
+    if (int rc = check_rope(rope, head_dim)) return rc;
+  NormDev n{};
+  if (int rc = check_norm(norm, dtype, head_dim, n)) return rc;
+  if (!q) n.wq = nullptr;
+  ScalesDev sc{};
+  if (scales)
+    if (int rc = check_scales(scales, cache, num_kv_heads, head_dim, sc)) return rc;
+  if (int rc = check_token_count(total_tokens)) return rc;
+  if (!cu_seqlens && total_tokens != cache->num_seqs)
+    return fail(GDN_EINVAL, "without cu_seqlens there is one token per sequence (%lld tokens, %d sequences)",
+                (long long)total_tokens, cache->num_seqs);
+  if (int rc = check_rows(k, "k", total_tokens)) return rc;
+  if (int rc = check_rows(v, "v", total_tokens)) return rc;
+  if (q) {
+    if (int rc = check_rows(q, "q", total_tokens)) return rc;
+    if (int rc = check_rows(q_out, "q_out", total_tokens)) return rc;
+  }
+  if (total_tokens == 0 || cache->num_seqs == 0) return ok();
+  RopeParams p{};
+  set_rope(p, rope);
+  p.D = head_dim;
+  p.Hq = Hq;
+  p.Hk = p.Hv = num_kv_heads;
+  p.q = rows_dev(q);
+  p.k = rows_dev(k);
+  p.v = rows_dev(v);
+  p.q_out = rows_dev(q_out);
+  p.T = total_tokens;
+  p.cu = cu_seqlens;
+  p.kv = kv_dev(cache);
+  const int sz = type_size(dtype);
+  auto fits = [&](int width) {
+    const int bytes = width * sz;  // 16 at most
+    return rope_pieces(p, rope, width) && aligned(k, total_tokens, num_kv_heads, sz, bytes) &&
+           aligned(v, total_tokens, num_kv_heads, sz, bytes) && (scales || aligned(cache, num_kv_heads, sz, bytes)) &&
+           (!q || (aligned(q, total_tokens, Hq, sz, bytes) && aligned(q_out, total_tokens, Hq, sz, bytes)));
+  };
+  const bool near_ = rope && rope->interleaved != 0;
+  if (scales) {
+    if (!fits(2))
+      return fail(GDN_EUNSUPPORTED, "an 8-bit cache takes 4-byte aligned rows of k, v and q, a rot_dim that is a multiple of 4 "
+                                    "and an 8-byte aligned table");
+    if (int rc = launched(launch_quant_append(p, n, sc, dtype, near_, fits(8) ? 8 : 2, stream), "quantising append kernel")) return rc;
+    return ok();
+  }
+  const int width = sz == 2 && fits(8) ? 8 : fits(4) ? 4 : fits(2) ? 2 : 1;
+  if (int rc = check_token_threads(p, width)) return rc;
+  if (n.wq || n.wk) {
+    if (int rc = launched(launch_norm_rope(p, n, dtype, near_, width, stream), "append kernel")) return rc;
+    return ok();
+  }
+  if (int rc = launched(launch_rope(p, dtype, near_, width, stream), "append kernel")) return rc;
+  return ok();
+}
+
+int run_attention(const gdn_attention_dims_t* dims, int32_t sinks, const gdn_rows_t* q, const int32_t* cu, int64_t T,
+                  const gdn_kv_cache_t* cache, const gdn_kv_scales_t* scales, const gdn_rows_t* out, float* lse,
+                  void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (sinks < 0 || sinks > 1 << 30) return fail(GDN_EINVAL, "sinks must be 0 .. 2^30 (got %d)", sinks);
+  AttnParams p{};
+  if (scales)
+    if (int rc = check_scales(scales, cache, dims->num_kv_heads, dims->head_dim, p.scales)) return rc;
+  if (scales && cu && (cache->token_stride < 0 || cache->token_stride >= (1 << 30) / cache->page_size))
+    return fail(GDN_EUNSUPPORTED, "chunks over an 8-bit cache take token strides of 0 .. 2^30 / page_size codes");
   if (T == 0 || cache->num_seqs == 0) return ok();
   const int32_t group = dims->num_q_heads / dims->num_kv_heads;
   if (T * group >= (int64_t(1) << 31) - 4096)  // (32-bit row numbers, to the end of the last tile)
     return fail(GDN_EINVAL, "query rows of a kv-head (%lld) must stay below 2^31 - 4096", (long long)(T * group));
   if (!aligned(q, T, dims->num_q_heads, 2, 16)) return fail(GDN_EINVAL, "rows of q must be 16-byte aligned");
   if (!aligned(out, T, dims->num_q_heads, 2, 16)) return fail(GDN_EINVAL, "rows of out must be 16-byte aligned");
-  if (!aligned(cache, dims->num_kv_heads, 2, 16))
+  if (!scales && !aligned(cache, dims->num_kv_heads, 2, 16))
     return fail(GDN_EINVAL, "rows of the cache must be 16-byte aligned");
   const size_t need = gdn_attention_workspace_size(dims, T, cache->num_seqs);
   if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255))
@@ -860,7 +1018,6 @@ int run_attention(const gdn_attention_dims_t* dims, const gdn_rows_t* q, const i
   if (!(same && !cu) && share_memory(q, out, T, dims->num_q_heads, dims->head_dim, 2))
     return fail(GDN_EINVAL, cu ? "out must not share memory with q"
                                : "out must be q itself or not share memory with it");
-  AttnParams p{};
   p.q = rows_dev(q);
   p.o = rows_dev(out);
   p.lse = lse;
@@ -871,6 +1028,7 @@ int run_attention(const gdn_attention_dims_t* dims, const gdn_rows_t* q, const i
   p.Hkv = dims->num_kv_heads;
   p.group = fast_div((uint32_t)group);
   p.window = dims->window;
+  p.sinks = dims->window > 0 ? sinks : 0;  // (without a window every token is visible)
   p.causal = dims->causal != 0;
   const double scale = dims->scale > 0.f ? dims->scale : 1.0 / std::sqrt((double)dims->head_dim);
   const double log2e = 1.4426950408889634074;
@@ -921,45 +1079,91 @@ int gdn_rope_table(const gdn_rope_scaling_t* scaling, float* table, int64_t rows
 int gdn_rope(const gdn_rope_t* rope, int32_t dtype, int32_t head_dim, int32_t num_q_heads, int32_t num_k_heads,
              int64_t num_tokens, const void* positions, int32_t index_dtype, const gdn_rows_t* q,
              const gdn_rows_t* k, const gdn_rows_t* q_out, const gdn_rows_t* k_out, hipStream_t stream) {
+  return rotate_rows(nullptr, rope, dtype, head_dim, num_q_heads, num_k_heads, num_tokens, positions, index_dtype, q, k, q_out,
+                     k_out, stream);
+}
+
+int gdn_norm_rope(const gdn_norm_t* norm, const gdn_rope_t* rope, int32_t dtype, int32_t head_dim, int32_t num_q_heads,
+                  int32_t num_k_heads, int64_t num_tokens, const void* positions, int32_t index_dtype,
+                  const gdn_rows_t* q, const gdn_rows_t* k, const gdn_rows_t* q_out, const gdn_rows_t* k_out,
+                  hipStream_t stream) {
+  if (!norm) return fail(GDN_EINVAL, "norm is NULL");
+  return rotate_rows(norm, rope, dtype, head_dim, num_q_heads, num_k_heads, num_tokens, positions, index_dtype, q, k, q_out,
+                     k_out, stream);
+}
+
+size_t gdn_norm_rope_backward_workspace_size(int32_t head_dim, int32_t num_q_heads, int32_t num_k_heads, int64_t num_tokens) {
+  if (check_heads(head_dim, num_q_heads, num_k_heads) || check_token_count(num_tokens) || head_dim > kNormMaxDim) return 0;
+  return std::max<size_t>(256, norm_rope_grad_bytes(head_dim, num_tokens, num_q_heads, num_k_heads));
+}
+
+int gdn_norm_rope_backward(const gdn_norm_t* norm, const gdn_rope_t* rope, int32_t dtype, int32_t head_dim, int32_t num_q_heads,
+                           int32_t num_k_heads, int64_t num_tokens, const void* positions, int32_t index_dtype,
+                           const gdn_rows_t* q, const gdn_rows_t* k, const gdn_rows_t* q_out_grad, const gdn_rows_t* k_out_grad,
+                           const gdn_rows_t* q_grad, const gdn_rows_t* k_grad, void* q_weight_grad, void* k_weight_grad,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!norm) return fail(GDN_EINVAL, "norm is NULL");
   if (!rope) return fail(GDN_EINVAL, "rope is NULL");
   if (int rc = check_type(dtype, true)) return rc;
   if (int rc = check_heads(head_dim, num_q_heads, num_k_heads)) return rc;
+  if (num_q_heads + num_k_heads == 0) return ok();
   if (int rc = check_rope(rope, head_dim)) return rc;
+  NormDev n{};
+  if (int rc = check_norm(norm, dtype, head_dim, n)) return rc;
   if (int rc = check_token_count(num_tokens)) return rc;
   if (index_dtype != GDN_INDEX_INT32 && index_dtype != GDN_INDEX_INT64)
     return fail(GDN_EINVAL, "index_dtype must be GDN_INDEX_INT32 or GDN_INDEX_INT64");
   if (num_tokens > 0 && !positions) return fail(GDN_EINVAL, "positions must not be NULL");
-  if (num_q_heads > 0) {
-    if (int rc = check_rows(q, "q", num_tokens)) return rc;
-    if (int rc = check_rows(q_out, "q_out", num_tokens)) return rc;
+  const int sz = type_size(dtype);
+  // the rows of one kind of head
+  struct Kind {
+    const char* name;
+    int32_t heads;
+    const void *weight, *weight_grad;
+    const gdn_rows_t *x, *out_grad, *x_grad;
+  };
+  const Kind kinds[2] = {{"q", num_q_heads, n.wq, q_weight_grad, q, q_out_grad, q_grad},
+                         {"k", num_k_heads, n.wk, k_weight_grad, k, k_out_grad, k_grad}};
+  bool wide[9] = {};
+  for (int width : {8, 4, 2}) wide[width] = sz * width <= 16;
+  for (const Kind& a : kinds) {
+    if (!a.heads) continue;
+    if (!a.weight || !a.weight_grad) return fail(GDN_EINVAL, "the weights of %s and their gradient must not be NULL", a.name);
+    for (const gdn_rows_t* r : {a.x, a.out_grad, a.x_grad}) {
+      if (int rc = check_rows(r, a.name, num_tokens)) return rc;
+      for (int width : {8, 4, 2}) wide[width] = wide[width] && aligned(r, num_tokens, a.heads, sz, width * sz);
+    }
+    // a workgroup reads rows that others have written by then
+    for (const gdn_rows_t* r : {a.x, a.out_grad}) {
+      const bool same = r->data == a.x_grad->data && (num_tokens < 2 || r->token_stride == a.x_grad->token_stride) &&
+                        (a.heads < 2 || r->head_stride == a.x_grad->head_stride);
+      if (num_tokens > 0 && !same && share_memory(r, a.x_grad, num_tokens, a.heads, head_dim, sz))
+        return fail(GDN_EINVAL, "the gradient of %s must lie over the rows it is of, their outputs' gradient, or neither", a.name);
+    }
   }
-  if (num_k_heads > 0) {
-    if (int rc = check_rows(k, "k", num_tokens)) return rc;
-    if (int rc = check_rows(k_out, "k_out", num_tokens)) return rc;
-  }
+  const size_t need = gdn_norm_rope_backward_workspace_size(head_dim, num_q_heads, num_k_heads, num_tokens);
+  if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255))
+    return fail(GDN_EWORKSPACE, "workspace needs %zu bytes, 256-byte aligned (got %zu)", need, workspace ? workspace_bytes : 0);
   RopeParams p{};
   set_rope(p, rope);
   p.D = head_dim;
   p.Hq = num_q_heads;
   p.Hk = num_k_heads;
-  p.q = rows_dev(q);
-  p.k = rows_dev(k);
-  p.q_out = rows_dev(q_out);
-  p.k_out = rows_dev(k_out);
   p.T = num_tokens;
   p.pos = positions;
   p.pos64 = index_dtype == GDN_INDEX_INT64;
   p.kv.page = fast_div(1);
-  const int sz = type_size(dtype);
-  auto fits = [&](int width) {
-    const int bytes = width * sz;  // 16 at most
-    return rope_pieces(p, rope, width) &&
-           (!num_q_heads || (aligned(q, num_tokens, num_q_heads, sz, bytes) && aligned(q_out, num_tokens, num_q_heads, sz, bytes))) &&
-           (!num_k_heads || (aligned(k, num_tokens, num_k_heads, sz, bytes) && aligned(k_out, num_tokens, num_k_heads, sz, bytes)));
-  };
-  const int width = sz == 2 && fits(8) ? 8 : fits(4) ? 4 : fits(2) ? 2 : 1;
+  NormGradDev g{};
+  for (int i = 0; i < 2; ++i)
+    g.kind[i] = NormGradDev::Kind{rows_dev(kinds[i].x), rows_dev(kinds[i].out_grad), rows_dev(kinds[i].x_grad),
+                                  fast_div((uint32_t)std::max(1, kinds[i].heads)), kinds[i].weight, 0, 0};
+  auto fits = [&](int width) { return wide[width] && rope_pieces(p, rope, width); };
+  const int width = fits(8) ? 8 : fits(4) ? 4 : fits(2) ? 2 : 1;
   if (int rc = check_token_threads(p, width)) return rc;
-  if (int rc = launched(launch_rope(p, dtype, rope->interleaved != 0, width, stream), "rotary kernel")) return rc;
+  if (int rc = launched(launch_norm_rope_grad(p, n, g, dtype, rope->interleaved != 0, width, q_weight_grad, k_weight_grad,
+                                              (float*)workspace, stream),
+                        "norm gradient kernel"))
+    return rc;
   return ok();
 }
 
@@ -967,46 +1171,46 @@ int gdn_kv_append_paged(const gdn_rope_t* rope, int32_t dtype, int32_t head_dim,
                         int32_t num_kv_heads, const int32_t* cu_seqlens, int64_t total_tokens,
                         const gdn_rows_t* k, const gdn_rows_t* v, const gdn_kv_cache_t* cache,
                         const gdn_rows_t* q, const gdn_rows_t* q_out, hipStream_t stream) {
+  return append_rows(nullptr, rope, dtype, head_dim, num_q_heads, num_kv_heads, cu_seqlens, total_tokens, k, v, cache, nullptr,
+                     q, q_out, stream);
+}
+
+int gdn_kv_append_paged_ext(const gdn_norm_t* norm, const gdn_rope_t* rope, int32_t dtype, int32_t head_dim, int32_t num_q_heads,
+                            int32_t num_kv_heads, const int32_t* cu_seqlens, int64_t total_tokens, const gdn_rows_t* k,
+                            const gdn_rows_t* v, const gdn_kv_cache_t* cache, const gdn_kv_scales_t* scales,
+                            const gdn_rows_t* q, const gdn_rows_t* q_out, hipStream_t stream) {
+  return append_rows(norm, rope, dtype, head_dim, num_q_heads, num_kv_heads, cu_seqlens, total_tokens, k, v, cache, scales, q,
+                     q_out, stream);
+}
+
+int gdn_kv_read_paged(int32_t dtype, int32_t head_dim, int32_t num_kv_heads, const int32_t* cu_seqlens, int64_t total_tokens,
+                      const gdn_kv_cache_t* cache, const gdn_kv_scales_t* scales, const gdn_rows_t* k, const gdn_rows_t* v,
+                      hipStream_t stream) {
   if (int rc = check_type(dtype, true)) return rc;
-  const int32_t Hq = q ? num_q_heads : 0;
-  if (int rc = check_heads(head_dim, Hq, num_kv_heads)) return rc;
+  if (int rc = check_heads(head_dim, 0, num_kv_heads)) return rc;
   if (num_kv_heads < 1) return fail(GDN_EINVAL, "num_kv_heads must be positive (got %d)", num_kv_heads);
   if (int rc = check_cache(cache)) return rc;
-  if (rope)
-    if (int rc = check_rope(rope, head_dim)) return rc;
+  ScalesDev sc{};
+  if (int rc = check_scales(scales, cache, num_kv_heads, head_dim, sc)) return rc;
   if (int rc = check_token_count(total_tokens)) return rc;
   if (!cu_seqlens && total_tokens != cache->num_seqs)
     return fail(GDN_EINVAL, "without cu_seqlens there is one token per sequence (%lld tokens, %d sequences)",
                 (long long)total_tokens, cache->num_seqs);
   if (int rc = check_rows(k, "k", total_tokens)) return rc;
   if (int rc = check_rows(v, "v", total_tokens)) return rc;
-  if (q) {
-    if (int rc = check_rows(q, "q", total_tokens)) return rc;
-    if (int rc = check_rows(q_out, "q_out", total_tokens)) return rc;
-  }
+  const int sz = type_size(dtype);
+  if (!aligned(k, total_tokens, num_kv_heads, sz, 16) || !aligned(v, total_tokens, num_kv_heads, sz, 16))
+    return fail(GDN_EINVAL, "rows of k and v must be 16-byte aligned");
   if (total_tokens == 0 || cache->num_seqs == 0) return ok();
   RopeParams p{};
-  set_rope(p, rope);
   p.D = head_dim;
-  p.Hq = Hq;
   p.Hk = p.Hv = num_kv_heads;
-  p.q = rows_dev(q);
   p.k = rows_dev(k);
   p.v = rows_dev(v);
-  p.q_out = rows_dev(q_out);
   p.T = total_tokens;
   p.cu = cu_seqlens;
   p.kv = kv_dev(cache);
-  const int sz = type_size(dtype);
-  auto fits = [&](int width) {
-    const int bytes = width * sz;  // 16 at most
-    return rope_pieces(p, rope, width) && aligned(k, total_tokens, num_kv_heads, sz, bytes) &&
-           aligned(v, total_tokens, num_kv_heads, sz, bytes) && aligned(cache, num_kv_heads, sz, bytes) &&
-           (!q || (aligned(q, total_tokens, Hq, sz, bytes) && aligned(q_out, total_tokens, Hq, sz, bytes)));
-  };
-  const int width = sz == 2 && fits(8) ? 8 : fits(4) ? 4 : fits(2) ? 2 : 1;
-  if (int rc = check_token_threads(p, width)) return rc;
-  if (int rc = launched(launch_rope(p, dtype, rope && rope->interleaved != 0, width, stream), "append kernel")) return rc;
+  if (int rc = launched(launch_quant_read(p, sc, dtype, stream), "cache read kernel")) return rc;
   return ok();
 }
 
@@ -1015,26 +1219,40 @@ size_t gdn_attention_workspace_size(const gdn_attention_dims_t* dims, int64_t to
   return attention_bytes(dims->head_dim, total_tokens, num_seqs, dims->num_q_heads / dims->num_kv_heads);
 }
 
-int gdn_attention_prefill_paged(const gdn_attention_dims_t* dims, const gdn_rows_t* q, const int32_t* cu_seqlens,
-                                int64_t total_tokens, const gdn_kv_cache_t* cache, const gdn_rows_t* out, float* lse,
-                                void* workspace, size_t workspace_bytes, hipStream_t stream) {
+int gdn_attention_prefill_paged_ext(const gdn_attention_dims_t* dims, int32_t sinks, const gdn_rows_t* q,
+                                    const int32_t* cu_seqlens, int64_t total_tokens, const gdn_kv_cache_t* cache,
+                                    const gdn_kv_scales_t* scales, const gdn_rows_t* out, float* lse, void* workspace,
+                                    size_t workspace_bytes, hipStream_t stream) {
   if (int rc = check_attention(dims)) return rc;
   if (int rc = check_cache(cache)) return rc;
   if (int rc = check_token_count(total_tokens)) return rc;
   if (!cu_seqlens) return fail(GDN_EINVAL, "cu_seqlens must not be NULL");
   if (int rc = check_rows(q, "q", total_tokens)) return rc;
   if (int rc = check_rows(out, "out", total_tokens)) return rc;
-  return run_attention(dims, q, cu_seqlens, total_tokens, cache, out, lse, workspace, workspace_bytes, stream);
+  return run_attention(dims, sinks, q, cu_seqlens, total_tokens, cache, scales, out, lse, workspace, workspace_bytes, stream);
+}
+
+int gdn_attention_decode_paged_ext(const gdn_attention_dims_t* dims, int32_t sinks, const gdn_rows_t* q,
+                                   const gdn_kv_cache_t* cache, const gdn_kv_scales_t* scales, const gdn_rows_t* out,
+                                   float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (int rc = check_attention(dims)) return rc;
+  if (int rc = check_cache(cache)) return rc;
+  if (int rc = check_rows(q, "q", cache->num_seqs)) return rc;
+  if (int rc = check_rows(out, "out", cache->num_seqs)) return rc;
+  return run_attention(dims, sinks, q, nullptr, cache->num_seqs, cache, scales, out, lse, workspace, workspace_bytes, stream);
+}
+
+int gdn_attention_prefill_paged(const gdn_attention_dims_t* dims, const gdn_rows_t* q, const int32_t* cu_seqlens,
+                                int64_t total_tokens, const gdn_kv_cache_t* cache, const gdn_rows_t* out, float* lse,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return gdn_attention_prefill_paged_ext(dims, 0, q, cu_seqlens, total_tokens, cache, nullptr, out, lse, workspace,
+                                         workspace_bytes, stream);
 }
 
 int gdn_attention_decode_paged(const gdn_attention_dims_t* dims, const gdn_rows_t* q, const gdn_kv_cache_t* cache,
                                const gdn_rows_t* out, float* lse, void* workspace, size_t workspace_bytes,
                                hipStream_t stream) {
-  if (int rc = check_attention(dims)) return rc;
-  if (int rc = check_cache(cache)) return rc;
-  if (int rc = check_rows(q, "q", cache->num_seqs)) return rc;
-  if (int rc = check_rows(out, "out", cache->num_seqs)) return rc;
-  return run_attention(dims, q, nullptr, cache->num_seqs, cache, out, lse, workspace, workspace_bytes, stream);
+  return gdn_attention_decode_paged_ext(dims, 0, q, cache, nullptr, out, lse, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

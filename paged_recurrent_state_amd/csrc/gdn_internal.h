@@ -221,6 +221,47 @@ hipError_t launch_rope(RopeParams p, int dtype, bool interleaved, int width, hip
 hipError_t launch_rope_table(float* table, int64_t rows, int rot, double base, double factor, int bands,
                              double original, double low, double high, double magnitude, hipStream_t s);
 
+// Norms of query and key heads before the rotation (gdn_norm_rope, the append).
+constexpr int kNormMaxDim = 512;  // values of a normed head at most
+struct NormDev {
+  const void* wq;  // weights [D] of the queries, of the keys; null: not normed
+  const void* wk;
+  int wide;  // the weights are fp32
+  float eps, offset;
+  // set by the launch
+  int units, shift;  // units of a row (see RopeParams.row_units) and log2 of its lanes
+  float inv_dim;
+};
+// The gradient: for the queries and the keys the inputs, the outputs' gradients and the
+// inputs', and, set by the launch, workgroups and how many tokens one takes at a time.
+struct NormGradDev {
+  struct Kind {
+    RowsDev x, g, dx;
+    FastDiv heads;
+    const void* w;
+    int blocks, tokens;
+  } kind[2];
+};
+hipError_t launch_norm_rope(const RopeParams& p, const NormDev& n, int dtype, bool interleaved, int width, hipStream_t s);
+// partial: norm_rope_grad_bytes; dwq, dwk: [D], of the weights' type
+hipError_t launch_norm_rope_grad(const RopeParams& p, const NormDev& n, const NormGradDev& g, int dtype, bool interleaved,
+                                 int width, void* dwq, void* dwk, float* partial, hipStream_t s);
+size_t norm_rope_grad_bytes(int D, int64_t T, int Hq, int Hk);
+
+// Scales of an 8-bit cache, one for each block of tokens of a page and head (strides
+// in elements).
+struct ScalesDev {
+  float* k;  // null: the cache holds 16-bit values
+  float* v;
+  int64_t ps, bs, hs;
+  FastDiv block;  // tokens of a block
+};
+// width: 8 or 2
+hipError_t launch_quant_append(const RopeParams& p, const NormDev& n, const ScalesDev& sc, int dtype, bool interleaved, int width,
+                               hipStream_t s);
+// p.k, p.v: the rows written
+hipError_t launch_quant_read(RopeParams p, const ScalesDev& sc, int dtype, hipStream_t s);
+
 // Attention over the paged cache.
 struct AttnParams {
   RowsDev q, o;
@@ -231,6 +272,8 @@ struct AttnParams {
   int Hq, Hkv;
   FastDiv group;  // q-heads per kv-head
   int window;     // 0: none
+  int sinks;      // first tokens that stay visible beside a window
+  ScalesDev scales;  // of an 8-bit cache
   int causal;
   float scale;    // of the raw scores, in log2 units (softcap: 2 log2(e) scale / softcap)
   float cap;      // softcap in log2 units, 0: none
@@ -246,6 +289,11 @@ struct AttnParams {
   void* seqs;      // [B]: the sequences, when they are more than 1024
   void* head;       // PlanHead; null: few tiles, every workgroup plans for itself
 };
+// by the type of the queries and of the cache (8: e4m3 with p.scales), each in a source of its own
+hipError_t launch_attention_bf16(const AttnParams& p, int D, void* workspace, hipStream_t s);
+hipError_t launch_attention_f16(const AttnParams& p, int D, void* workspace, hipStream_t s);
+hipError_t launch_attention8_bf16(const AttnParams& p, int D, void* workspace, hipStream_t s);
+hipError_t launch_attention8_f16(const AttnParams& p, int D, void* workspace, hipStream_t s);
 hipError_t launch_attention(const AttnParams& p, int D, int dtype, void* workspace, hipStream_t s);
 size_t attention_bytes(int D, int64_t T, int64_t B, int64_t group);  // workspace of launch_attention
 

@@ -17,82 +17,14 @@
 // page table are looked up once per token, by one lane each.
 #include <algorithm>
 
-#include "gdn_internal.h"
+#include "gdn_rows.h"
 
 namespace gdn {
 
 namespace {
 
-struct Bf16 {
-  typedef u16 type;
-};
-struct Half {
-  typedef _Float16 type;
-};
-struct Single {
-  typedef float type;
-};
-
-__device__ __forceinline__ float to_f(u16 x) { return bf2f(x); }
-__device__ __forceinline__ float to_f(_Float16 x) { return (float)x; }
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ void from_f(float x, u16& y) { y = f2bf(x); }
-__device__ __forceinline__ void from_f(float x, _Float16& y) { y = (_Float16)x; }
-__device__ __forceinline__ void from_f(float x, float& y) { y = x; }
-
-// W values at once, 16 bytes at most.
-template <int W, typename E>
-struct Piece {
-  typedef E type __attribute__((ext_vector_type(W)));
-};
-template <bool NT, typename V>
-__device__ __forceinline__ void put(V* p, V w) {
-  if constexpr (NT)
-    __builtin_nontemporal_store(w, p);
-  else
-    *p = w;
-}
-template <bool NT, typename V>
-__device__ __forceinline__ V get(const V* p) {
-  if constexpr (NT)
-    return __builtin_nontemporal_load(p);
-  else
-    return *p;
-}
-template <int W, bool NT = false, typename E>
-__device__ __forceinline__ void load(const E* p, float (&x)[W]) {
-  const typename Piece<W, E>::type w = get<NT>((const typename Piece<W, E>::type*)p);
-#pragma unroll
-  for (int i = 0; i < W; ++i) x[i] = to_f(w[i]);
-}
-template <bool NT, int W, typename E>
-__device__ __forceinline__ void store(E* p, const float (&x)[W]) {
-  typename Piece<W, E>::type w;
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    E y;
-    from_f(x[i], y);
-    w[i] = y;
-  }
-  put<NT>((typename Piece<W, E>::type*)p, w);
-}
-
-// (a c - b s, b c + a s), one product of each rounded and the other fused, the
-// same in every path
-__device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) {
-  const float x = a;
-  a = __builtin_fmaf(x, c, -(b * s));
-  b = __builtin_fmaf(b, c, x * s);
-}
-
 constexpr int kRopeThreads = 256;
 constexpr int kRopeTokens = 64;  // most tokens of a workgroup
-
-// A token of the workgroup: its position, and where its key and value go in the
-// cache (elements; -1: nowhere).
-struct Place {
-  int64_t pos, dst;
-};
 
 // Loads and stores pass the caches (NT) when the call writes more than the L2s hold
 // together; below that the next kernel may find the rows there.  Other rows in every
@@ -109,42 +41,7 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeParams p) {
   const int64_t t0 = (int64_t)blockIdx.x * p.tokens_per_block;
   const int tokens = (int)min((int64_t)p.tokens_per_block, p.T - t0);
 
-  if (threadIdx.x < 64) {
-    const int lane = threadIdx.x;
-    const int64_t t = t0 + lane;
-    if (p.pos) {
-      if (lane < tokens)
-        place[lane] = Place{p.pos64 ? ((const int64_t*)p.pos)[t] : (int64_t)((const int32_t*)p.pos)[t], -1};
-    } else {
-      int b = (int)t;
-      if (p.cu) {
-        int lo = wave_find_seq(p.cu, p.kv.B, (int)t0);
-        int hi = tokens > 1 ? wave_find_seq(p.cu, p.kv.B, (int)(t0 + tokens - 1)) : lo;
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (p.cu[mid] <= (int)t)
-            lo = mid;
-          else
-            hi = mid - 1;
-        }
-        b = lo;
-      }
-      if (lane < tokens) {
-        Place pl{-1, -1};
-        if (b < p.kv.B) {
-          const int first = p.kv.ptr[b], pages = p.kv.ptr[b + 1] - first;
-          const int64_t len = pages > 0 ? (int64_t)(pages - 1) * p.kv.page.d + p.kv.lpl[b] : 0;
-          const int64_t pos = p.cu ? t - p.cu[b + 1] + len : len - 1;
-          pl.pos = pos;
-          if (pos >= 0 && pos < len) {
-            const int pg = (int)div_by((uint32_t)pos, p.kv.page);
-            pl.dst = (int64_t)p.kv.idx[first + pg] * p.kv.ps + (pos - (int64_t)pg * p.kv.page.d) * p.kv.ts;
-          }
-        }
-        place[lane] = pl;
-      }
-    }
-  }
+  if (threadIdx.x < 64) find_places(p, t0, tokens, place);
   __syncthreads();
 
   const int rot = p.rot, half = rot >> 1;
