@@ -211,8 +211,9 @@ typedef struct {
  * if the scale grows their codes are rounded to the new one.  A block that the
  * new tokens open takes a new scale, whatever it held.  A value is rounded once,
  * to nearest, ties to even; values that are not finite are stored as NaN and count
- * for no scale, and from fp16 rows no magnitude over 61,440 is stored (the next code
- * is beyond fp16).  Rows and slots behind the new tokens are left as they are.
+ * for no scale, and none is stored over 15/8 of the rows' type's highest power of two
+ * (61,440 in fp16: the next code is beyond it).  Rows and slots behind the new tokens
+ * are left as they are.
  * Errors as gdn_kv_append_paged and gdn_norm_rope (but that a null weight leaves
  * its heads as they are), GDN_EINVAL for null or unaligned scales, a bad block,
  * or a cache that is not 16-byte aligned in every stride and address;

@@ -14,6 +14,8 @@ Everything here is plain, slow and meant to be read against the pages:
   prefill/decode and the paged wrappers.
 * ``attention`` -- rotary positions, the append and attention over a paged
   key/value cache, from their definitions.
+* ``norms`` -- norms of query and key heads before the rotation, and their gradient.
+* ``quantised`` -- rounding to e4m3, and the append to a cache of 8 bits, block by block.
 
 Pins (see ``tests/test_oracle_*.py``): the worked examples the pages print,
 closed forms, special cases and brute force on tiny inputs; every function
@@ -24,4 +26,4 @@ by invariants (split invariance, linearity in the start state, decode as a
 one-token prefill) rather than by printed numbers.
 """
 
-from . import attention, csr, slots, gdn  # noqa: F401
+from . import attention, csr, gdn, norms, quantised, slots  # noqa: F401

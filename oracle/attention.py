@@ -57,7 +57,7 @@ def slots(page_indices, page_indptr, last_page_len, page_size: int, b: int):
 
 
 def softmax_rows(q: np.ndarray, k: np.ndarray, v: np.ndarray, positions, scale: Optional[float] = None,
-                 softcap: float = 0.0, window: int = 0, causal: bool = True):
+                 softcap: float = 0.0, window: int = 0, causal: bool = True, sinks: int = 0):
     """q [n, D] at ``positions`` against k, v [L, D]: (o [n, D], lse [n], magnitude [n, D] =
     sum p |v|, spread [n] = largest sum |q_d k_d| times the scale, reach [n] = largest |x|)."""
     n, D = q.shape
@@ -70,7 +70,8 @@ def softmax_rows(q: np.ndarray, k: np.ndarray, v: np.ndarray, positions, scale: 
         hi = min(t, L - 1) if causal else L - 1
         if hi < lo:
             continue
-        kk, vv = k[lo:hi + 1], v[lo:hi + 1]
+        at = [j for j in range(hi + 1) if j >= lo or j < sinks] if sinks else slice(lo, hi + 1)
+        kk, vv = k[at], v[at]
         x = scale * (kk @ q[i])
         if softcap:
             x = softcap * np.tanh(x / softcap)
@@ -85,7 +86,7 @@ def softmax_rows(q: np.ndarray, k: np.ndarray, v: np.ndarray, positions, scale: 
 
 
 def attention_paged(q, cu_seqlens, k_cache, v_cache, page_indices, page_indptr, page_size, last_page_len,
-                    scale=None, softcap=0.0, window=0, causal=True):
+                    scale=None, softcap=0.0, window=0, causal=True, sinks=0):
     """The five arrays of softmax_rows for q [T, Hq, D], caches [pages, page_size, Hkv, D].
     Only slots that a sequence holds are read."""
     T, Hq, D = q.shape
@@ -105,7 +106,7 @@ def attention_paged(q, cu_seqlens, k_cache, v_cache, page_indices, page_indptr, 
             v = np.asarray(v_cache[pg, off, h], dtype=np.float64)
             for g in range(G):
                 got = softmax_rows(np.asarray(q[t0:t1, h * G + g], dtype=np.float64), k, v, pos, scale, softcap,
-                                   window, causal)
+                                   window, causal, sinks)
                 for dst, x in zip((o, lse, mag, spread, reach), got):
                     dst[t0:t1, h * G + g] = x
     return o, lse, mag, spread, reach

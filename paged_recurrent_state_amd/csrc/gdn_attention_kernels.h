@@ -305,12 +305,15 @@ struct Chunk {
 
 // A tile of query rows: its first row in its sequence, the keys it sees, and the
 // sequence's new tokens, tokens and first page.  Where first tokens stay visible
-// beside a window (sinks), the tiles of keys before it are left out: key numbers
-// from the first tokens' tiles on (after_firsts) lie `gap` below the tokens'.
+// beside a window (sinks) and the window of some row begins behind them, the tile has
+// their tiles of keys first, which show them alone, and then the window's, which show
+// the rest: key numbers from `firsts` on, the end of their tiles, are the tokens' less
+// `gap` (kNoGap: not so; -1 tile: one of both is read twice).
 struct TileRec {
   int row0, key_begin, key_end, tok0, n, len, first_page, gap;
 };
-__device__ __forceinline__ int after_firsts(const AttnParams& p, int keys) { return (p.sinks + keys - 1) / keys * keys; }
+constexpr int kNoGap = INT32_MIN;
+__device__ __forceinline__ int end_of_firsts(const AttnParams& p, int keys) { return (p.sinks + keys - 1) / keys * keys; }
 // What plan_kernel says of the list: tiles, what each costs besides its key tiles,
 // and what one kv-head costs in all.
 struct PlanHead {
@@ -370,15 +373,17 @@ __device__ __forceinline__ PlanHead make_plan(const AttnParams& p, int rows, int
           hi = mid - 1;
       }
       const SeqRec q = seqs[lo];
-      TileRec r{(i - q.before) * rows, 0, 0, q.tok0, q.n, q.len, q.first_page, 0};
+      TileRec r{(i - q.before) * rows, 0, 0, q.tok0, q.n, q.len, q.first_page, kNoGap};
       const int past = r.len - r.n;
       const int first = (int)div_by((uint32_t)r.row0, p.group);
       const int last = min(r.n - 1, (int)div_by((uint32_t)r.row0 + rows - 1, p.group));
       r.key_end = p.causal ? max(0, min(past + last + 1, r.len)) : r.len;
       r.key_begin = p.window > 0 ? min(r.key_end, max(0, past + first - p.window + 1) / keys * keys) : 0;
-      if (p.sinks > 0 && r.key_begin > 0) {
-        r.gap = max(0, r.key_begin - after_firsts(p, keys));
-        r.key_end -= r.gap;
+      if (p.sinks > 0) {  // (with a window)
+        if (past + last - p.window + 1 > p.sinks && r.key_end > p.sinks) {
+          r.gap = max(r.key_begin, p.sinks / keys * keys) - end_of_firsts(p, keys);
+          r.key_end -= r.gap;
+        }
         r.key_begin = 0;
       }
       tiles[i] = r;
@@ -455,11 +460,22 @@ __device__ __forceinline__ void store_rows(const AttnParams& p, const TileRec& r
   }
 }
 
+// The first argument of the kernel, its fields loaded anew where they are asked for:
+// what is needed once a run does not stay in scalar registers in between, of which the
+// chunk kernel with sinks has too few.
+__device__ __forceinline__ const AttnParams& reloaded() {
+  typedef const AttnParams __attribute__((address_space(4))) * Args;
+  Args p = (Args)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const AttnParams*)p;
+}
+
 // EVEN: a wave's rows of a tile lie in one page (see launch_chunk).
 // Q8: the cache holds e4m3 codes.  A wave loads its rows' codes into LDS of its own,
 // and a tile ahead writes them as values, times their scales, to the slots that the
 // products read.
-template <class E, int D, Cap CAP, bool EVEN, bool Q8>
+// SINKS: first tokens stay visible beside a window.
+template <class E, int D, Cap CAP, bool EVEN, bool Q8, bool SINKS>
 __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
   typedef Chunk<D, Q8> C;
   static_assert(EVEN || !Q8);
@@ -550,6 +566,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
     TileRec rec = tile_recs[ti];
     rec = TileRec{uniform(rec.row0), uniform(rec.key_begin), uniform(rec.key_end), uniform(rec.tok0),
                   uniform(rec.n), uniform(rec.len), uniform(rec.first_page), uniform(rec.gap)};
+    const bool apart = SINKS && rec.gap != kNoGap;
+    const int firsts = apart ? end_of_firsts(p, C::kKeys) : 0, gap = apart ? rec.gap : 0;
     // this share's part of the tile's key tiles: from `done` on (those before are the share before's)
     const int64_t start = hk * per_head + uniform64(tile_before[ti]) + (int64_t)ti * cost;
     const int tiles = uniform((int)(tile_before[ti + 1] - tile_before[ti]));
@@ -559,7 +577,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
       const int tok0 = rec.tok0, n = rec.n, first_page = rec.first_page, len = rec.len, past = len - n;
 
       // this lane's rows
-      int lim[NQ], low[NQ];  // keys low .. lim, and where low > 0 the sinks, which lie before low
+      int lim[NQ], low[NQ];  // keys low .. lim (SINKS: of those from `firsts` on)
       u32x4 q[NQ][kSteps];
 #pragma unroll
       for (int a = 0; a < NQ; ++a) {
@@ -567,9 +585,11 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
         const int tok = (int)div_by(row, p.group), g = row - tok * G;
         const bool real = tok < n;
         lim[a] = real ? (p.causal ? min(past + tok, len - 1) : len - 1) : -1;
-        low[a] = real && p.window > 0 ? past + tok - p.window + 1 : 0;
-        low[a] = low[a] <= p.sinks ? 0 : low[a] - rec.gap;
-        if (real) lim[a] -= rec.gap;
+        low[a] = real && p.window > 0 ? max(0, past + tok - p.window + 1) : 0;
+        if constexpr (SINKS) {
+          low[a] = apart ? max(low[a], p.sinks) - gap : 0;  // (the sinks reach every row's window)
+          lim[a] = lim[a] < 0 ? -1 : lim[a] - gap;
+        }
         const u16* src = (const u16*)p.q.p + (int64_t)(tok0 + (real ? tok : 0)) * p.q.ts +
                          (int64_t)(hk * G + (real ? g : 0)) * p.q.hs + 8 * half;
 #pragma unroll
@@ -610,21 +630,30 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
           for (int i = 0; i < 16; ++i) o[a][d][i] = 0.f;
       }
 
-      // as many tiles at a time as the staged places reach
+      // as many tiles at a time as the staged places reach, and the first tokens' by themselves
       for (int a0 = key_a; a0 < key_b;) {
-        const int a1 = (int)min((int64_t)key_b, a0 + (int64_t)C::kPlaces * step);
+        const bool few = SINKS && a0 < firsts;
+        const int sinks = SINKS ? p.sinks : 0;
+        const int a1 = (int)min((int64_t)(few ? min(sinks, key_b) : key_b), a0 + (int64_t)C::kPlaces * step);
         const int count = (a1 - a0 + C::kKeys - 1) / C::kKeys;
         __syncthreads();
-        for (int x = tid; a0 + x * step < a1; x += 64 * kWaves) {
+        // (codes: a place for every wave's rows of the last tile, past the end with a scale of one for its zeros)
+        const AttnParams& args = SINKS ? reloaded() : p;
+        const int staged = Q8 ? a0 + count * C::kKeys : a1;
+        for (int x = tid; a0 + x * step < staged; x += 64 * kWaves) {
           int key = a0 + x * step;
-          if (rec.gap && key >= after_firsts(p, C::kKeys)) key += rec.gap;
-          const int pg = (int)div_by(key, p.kv.page), off = key - pg * (int)p.kv.page.d;
-          const int64_t id = p.kv.idx[first_page + pg];
+          if (Q8 && key >= a1) {
+            places8[x] = Place8{0, 1.f, 1.f};
+            continue;
+          }
+          if (SINKS && key >= firsts) key += gap;
+          const int pg = (int)div_by(key, args.kv.page), off = key - pg * (int)args.kv.page.d;
+          const int64_t id = args.kv.idx[first_page + pg];
           if constexpr (Q8) {
-            const int64_t sc = id * p.scales.ps + (int64_t)div_by(off, p.scales.block) * p.scales.bs + hk * p.scales.hs;
-            places8[x] = Place8{id * p.kv.ps + (int64_t)off * p.kv.ts, p.scales.k[sc], p.scales.v[sc]};
+            const int64_t sc = id * args.scales.ps + (int64_t)div_by(off, args.scales.block) * args.scales.bs + hk * args.scales.hs;
+            places8[x] = Place8{id * args.kv.ps + (int64_t)off * args.kv.ts, args.scales.k[sc], args.scales.v[sc]};
           } else {
-            places[x] = 2 * (id * p.kv.ps + (int64_t)off * p.kv.ts);
+            places[x] = 2 * (id * args.kv.ps + (int64_t)off * args.kv.ts);
           }
         }
         __syncthreads();
@@ -781,13 +810,16 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
             }
         };
         // whether row block a sees the key of value e in the block of keys from key0 (this lane's keys are
-        // 4 half + 8 (e / 4) + e % 4): those up to last[a] from low[a] on, and the sinks
-        int last[NQ];
+        // 4 half + 8 (e / 4) + e % 4): span[a] keys from begin[a] on
+        int begin[NQ];
+        uint32_t span[NQ];
 #pragma unroll
-        for (int a = 0; a < NQ; ++a) last[a] = min(lim[a], a1 - 1);
+        for (int a = 0; a < NQ; ++a) {
+          begin[a] = few ? 0 : low[a];
+          span[a] = (uint32_t)max(0, few ? (lim[a] < 0 ? 0 : min(sinks, lim[a] + gap + 1)) : min(lim[a], a1 - 1) + 1 - low[a]);
+        }
         auto seen = [&](int a, int e, int key0) __attribute__((always_inline)) {
-          const int key = 8 * (e >> 2) + (e & 3) + (key0 + 4 * half);
-          return key <= last[a] && (key >= low[a] || key < p.sinks);
+          return (uint32_t)(8 * (e >> 2) + (e & 3) + (key0 + 4 * half - begin[a])) < span[a];
         };
         u32x4 pt[NQ][2], pw[NQ][2];
         float sum[NQ];
@@ -875,8 +907,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
           // values, are read a part before; the codes asked for then take their places
           constexpr int kUnits = 2 * C::kCodeLoads, kParts = 4 * KB;
           u32x4 held{};
-          float scale_k = 1.f, scale_v = 1.f;
-          int64_t from_k = 0, from_v = 0;
+          float scale = 1.f;
+          int64_t from = 0;
           // (the queries stay in accumulation registers, which the products read directly)
 #pragma unroll
           for (int a = 0; a < NQ; ++a)
@@ -884,10 +916,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
             for (int t = 0; t < kSteps; ++t) asm volatile("" : "+a"(q[a][t]));
           arrive();
           if constexpr (Q8) {
-            scale_k = place8(i + 2).k;
-            scale_v = place8(i + 1).v;
-            from_k = place8(i + 4).at;
-            from_v = place8(i + 3).at;
+            scale = place8(i + 2).k;
+            from = place8(i + 4).at;
             held = codes(false, i + 2, 0);
           }
 #pragma unroll
@@ -913,16 +943,20 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
                 if (part * kUnits % kParts == 0) {
                   const int u = part * kUnits / kParts;
                   const bool V = u >= C::kCodeLoads;
-                  put(V, V ? v_free : k_free, V ? u - C::kCodeLoads : u, held, V ? scale_v : scale_k);
+                  put(V, V ? v_free : k_free, V ? u - C::kCodeLoads : u, held, scale);
                 }
                 if ((part + 1) * kUnits % kParts == 0 && part + 1 < kParts) {
                   const int u = (part + 1) * kUnits / kParts;
                   const bool V = u >= C::kCodeLoads;
                   held = codes(V, V ? i + 1 : i + 2, V ? u - C::kCodeLoads : u);
+                  if (u == C::kCodeLoads) scale = place8(i + 1).v;
                 }
-                if (part == (kUnits == kParts ? kParts / 2 : kParts / 2 - 1))
-                  ask(std::bool_constant<kInner>(), false, i + 4, (const char*)uniform64(from_k));
-                if (part == kParts - 1) ask(std::bool_constant<kInner>(), true, i + 3, (const char*)uniform64(from_v));
+                constexpr int kAskK = kUnits == kParts ? kParts / 2 : kParts / 2 - 1;
+                if (part == kAskK) {
+                  ask(std::bool_constant<kInner>(), false, i + 4, (const char*)uniform64(from));
+                  from = place8(i + 3).at;
+                }
+                if (part == kParts - 1) ask(std::bool_constant<kInner>(), true, i + 3, (const char*)uniform64(from));
                 if constexpr (kInner) {
 #pragma unroll
                   for (int y = 0; y < kSteps * NQ / 2; ++y) {
@@ -1027,7 +1061,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
         // Tiles inner0 .. inner1 are seen whole by every row of the wave, and every row has its reference
         // (those that see the first block have it now, the others from the tile that `all_low` lies in);
         // the loads they ask for are of whole tiles or of none.
-        const int inner0 = all_low <= a0 ? 0 : min(count, (all_low - a0) / C::kKeys + 1);
+        const int inner0 = few ? count : all_low <= a0 ? 0 : min(count, (all_low - a0) / C::kKeys + 1);
         const int inner1 = min(full < count ? full - (Q8 ? 4 : 3) : full, (min(all_lim, a1 - 1) - a0 + 1) / C::kKeys);
         int i = 0;
         for (; i < inner0; ++i) tile(std::false_type(), i);
@@ -1039,9 +1073,10 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
         product(0);
         product(1);
         wait_vm<0>();
-        a0 = a1;
+        a0 = few && a1 == p.sinks ? firsts : a1;
       }
 
+      const AttnParams& args = SINKS ? reloaded() : p;
       const bool whole = done == 0 && todo == tiles;
       const bool head = done > 0;  // a part that continues a run: slot 0, one that starts it: slot 1
       const int64_t part = whole ? -1 : 2 * (int64_t)me + (head ? 0 : 1);
@@ -1061,12 +1096,12 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
       }
 #pragma unroll
       for (int a = 0; a < NQ; ++a)
-        store_rows<E, D>(p, rec, hk, wave * 32 * NQ + a * 32 + col, part, o[a], m[a], l[a]);
-      if (!head && (!whole || p.records)) {
+        store_rows<E, D>(args, rec, hk, wave * 32 * NQ + a * 32 + col, part, o[a], m[a], l[a]);
+      if (!head && (!whole || args.records)) {
         left = true;
         const int parts = whole ? 0 : (int)div_units(start + cost + tiles - 1, share) - me + 1;
         if (tid == 0)
-          records[p.records ? hk * num_tiles + ti : me] = Unfinished{parts, me, rec.row0, rec.tok0, rec.n, hk, {}};
+          records[args.records ? hk * num_tiles + ti : me] = Unfinished{parts, me, rec.row0, rec.tok0, rec.n, hk, {}};
       }
     }
     if (start + cost + tiles >= end) break;
@@ -1103,9 +1138,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
         const int tok = (int)div_by(row, p.group), g = row - tok * G;
         const bool real = tok < n;
         const int lim = real ? (p.causal ? min(past + tok, len - 1) : len - 1) : -1;
-        int low = real && p.window > 0 ? past + tok - p.window + 1 : 0;
-        if (low <= p.sinks) low = 0;
-        const int firsts = low > 0 ? p.sinks : 0;
+        const int low = real && p.window > 0 ? max(0, past + tok - p.window + 1) : 0;
         const int64_t h = (int64_t)hk * G + (real ? g : 0);
         u32x4 q[kSteps];
 #pragma unroll
@@ -1123,8 +1156,9 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
           for (int x = tid; x < 32 * D / 8; x += 64 * kWaves) {
             const int r = x / (D / 8), c = x % (D / 8), key = key0 + r;
             u32x4 wk{0u, 0u, 0u, 0u}, wv = wk;
-            if (key < key_b) {
-              const int token = rec.gap && key >= after_firsts(p, C::kKeys) ? key + rec.gap : key;
+            const bool apart = SINKS && rec.gap != kNoGap, window = apart && key >= end_of_firsts(p, C::kKeys);
+            if (key < key_b && (!apart || window || key < p.sinks)) {
+              const int token = window ? key + rec.gap : key;
               const int pg = (int)div_by(token, p.kv.page), off = token - pg * (int)p.kv.page.d;
               const int64_t id = p.kv.idx[first_page + pg], at = id * p.kv.ps + (int64_t)off * p.kv.ts + hk * p.kv.hs + 8 * c;
               if constexpr (Q8) {
@@ -1148,9 +1182,11 @@ __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
           // value e is of key 4 half + 8 (e / 4) + e % 4
           auto seen = [&](int e) __attribute__((always_inline)) {
             const int key = key0 + 4 * half + 8 * (e >> 2) + (e & 3);
-            if (key < firsts) return true;
-            const int token = rec.gap && key >= after_firsts(p, C::kKeys) ? key + rec.gap : key;
-            return key < key_b && token <= lim && token >= low;
+            if constexpr (!SINKS) return (key <= min(lim, key_b - 1)) & (key >= low);
+            // before the window's tiles the sinks, or every key where those reach each row's window
+            const bool apart = rec.gap != kNoGap, window = apart && key >= end_of_firsts(p, C::kKeys);
+            const int token = window ? key + rec.gap : key;
+            return (key < key_b) & (token <= lim) & (window ? token >= max(low, p.sinks) : !apart || token < p.sinks);
           };
           float top = -INFINITY;
 #pragma unroll
@@ -1297,17 +1333,17 @@ hipError_t allow_lds(Kernel* k, int bytes, std::atomic<bool> (&raised)[kMaxDevic
   return e;
 }
 
-template <class E, int D, Cap CAP, bool EVEN, bool Q8>
+template <class E, int D, Cap CAP, bool EVEN, bool Q8, bool SINKS>
 hipError_t launch_chunk_kernel(const AttnParams& p, hipStream_t s) {
   static std::atomic<bool> raised[kMaxDevices];
-  hipError_t e = allow_lds(chunk_kernel<E, D, CAP, EVEN, Q8>, Chunk<D, Q8>::kLds, raised);
+  hipError_t e = allow_lds(chunk_kernel<E, D, CAP, EVEN, Q8, SINKS>, Chunk<D, Q8>::kLds, raised);
   if (e != hipSuccess) return e;
   const int shares = device_cus();
   if (p.head) {
     plan_kernel<<<dim3(1), dim3(1024), 0, s>>>(p, Chunk<D, Q8>::kRows, Chunk<D, Q8>::kKeys, shares);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  chunk_kernel<E, D, CAP, EVEN, Q8><<<dim3(shares), dim3(64 * kWaves), Chunk<D, Q8>::kLds, s>>>(p);
+  chunk_kernel<E, D, CAP, EVEN, Q8, SINKS><<<dim3(shares), dim3(64 * kWaves), Chunk<D, Q8>::kLds, s>>>(p);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int groups = 256 / (D / 4);
   chunk_join_kernel<E, D><<<dim3(p.records ? p.records : shares, (p.part_rows + groups - 1) / groups), dim3(256), 0,
@@ -1315,7 +1351,7 @@ hipError_t launch_chunk_kernel(const AttnParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <class E, int D, bool Q8>
+template <class E, int D, bool Q8, bool SINKS>
 hipError_t launch_chunk(AttnParams p, void* workspace, hipStream_t s) {
   const ChunkWs w = chunk_ws<D>(p.T, p.kv.B, p.group.d);
   char* base = (char*)workspace;
@@ -1337,16 +1373,16 @@ hipError_t launch_chunk(AttnParams p, void* workspace, hipStream_t s) {
   const bool even = p.kv.page.d % 16 == 0 && p.kv.ts >= 0 && p.kv.ts * p.kv.page.d < (int64_t(1) << 30);
   if constexpr (Q8) {
     // (blocks of a multiple of 16 tokens divide the pages)
-    if (p.cap > kMostShort / kLn2) return launch_chunk_kernel<E, D, kCap, true, true>(p, s);
-    if (p.cap > 0.f) return launch_chunk_kernel<E, D, kCapShort, true, true>(p, s);
-    return launch_chunk_kernel<E, D, kNoCap, true, true>(p, s);
+    if (p.cap > kMostShort / kLn2) return launch_chunk_kernel<E, D, kCap, true, true, SINKS>(p, s);
+    if (p.cap > 0.f) return launch_chunk_kernel<E, D, kCapShort, true, true, SINKS>(p, s);
+    return launch_chunk_kernel<E, D, kNoCap, true, true, SINKS>(p, s);
   } else {
     if (p.cap > kMostShort / kLn2)
-      return even ? launch_chunk_kernel<E, D, kCap, true, false>(p, s) : launch_chunk_kernel<E, D, kCap, false, false>(p, s);
+      return even ? launch_chunk_kernel<E, D, kCap, true, false, SINKS>(p, s) : launch_chunk_kernel<E, D, kCap, false, false, SINKS>(p, s);
     if (p.cap > 0.f)
-      return even ? launch_chunk_kernel<E, D, kCapShort, true, false>(p, s)
-                  : launch_chunk_kernel<E, D, kCapShort, false, false>(p, s);
-    return even ? launch_chunk_kernel<E, D, kNoCap, true, false>(p, s) : launch_chunk_kernel<E, D, kNoCap, false, false>(p, s);
+      return even ? launch_chunk_kernel<E, D, kCapShort, true, false, SINKS>(p, s)
+                  : launch_chunk_kernel<E, D, kCapShort, false, false, SINKS>(p, s);
+    return even ? launch_chunk_kernel<E, D, kNoCap, true, false, SINKS>(p, s) : launch_chunk_kernel<E, D, kNoCap, false, false, SINKS>(p, s);
   }
 }
 
@@ -1907,17 +1943,18 @@ size_t decode_bytes() {
   return (size_t)decode_shares<D>() * (2 * kDecRows * (D + 2) * sizeof(float) + 4 * sizeof(int));
 }
 
-// Attention of one element type, over a cache of the same type or (Q8) of 8 bits.
+// Chunks of one element type, over a cache of the same type or (Q8) of 8 bits; decode of it.
+template <class E, bool Q8, bool SINKS>
+hipError_t chunk_of_type(const AttnParams& p, int D, void* workspace, hipStream_t s) {
+  if (D == 64) return launch_chunk<E, 64, Q8, SINKS>(p, workspace, s);
+  if (D == 128) return launch_chunk<E, 128, Q8, SINKS>(p, workspace, s);
+  return launch_chunk<E, 256, Q8, SINKS>(p, workspace, s);
+}
 template <class E, bool Q8>
-hipError_t launch_type(const AttnParams& p, int D, void* workspace, hipStream_t s) {
-  if (!p.cu) {
-    if (D == 64) return launch_dec<E, 64, Q8>(p, workspace, s);
-    if (D == 128) return launch_dec<E, 128, Q8>(p, workspace, s);
-    return launch_dec<E, 256, Q8>(p, workspace, s);
-  }
-  if (D == 64) return launch_chunk<E, 64, Q8>(p, workspace, s);
-  if (D == 128) return launch_chunk<E, 128, Q8>(p, workspace, s);
-  return launch_chunk<E, 256, Q8>(p, workspace, s);
+hipError_t decode_of_type(const AttnParams& p, int D, void* workspace, hipStream_t s) {
+  if (D == 64) return launch_dec<E, 64, Q8>(p, workspace, s);
+  if (D == 128) return launch_dec<E, 128, Q8>(p, workspace, s);
+  return launch_dec<E, 256, Q8>(p, workspace, s);
 }
 
 }  // namespace

@@ -1,0 +1,10 @@
+// Chunks of bf16 queries over 8-bit caches, with first tokens that stay visible beside a window.
+#include "gdn_attention_kernels.h"
+
+namespace gdn {
+
+hipError_t launch_chunk8_sinks_bf16(const AttnParams& p, int D, void* workspace, hipStream_t s) {
+  return chunk_of_type<Bf, true, true>(p, D, workspace, s);
+}
+
+}  // namespace gdn

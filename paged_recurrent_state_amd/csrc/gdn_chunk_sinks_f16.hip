@@ -1,0 +1,10 @@
+// Chunks of f16 queries over f16 caches, with first tokens that stay visible beside a window.
+#include "gdn_attention_kernels.h"
+
+namespace gdn {
+
+hipError_t launch_chunk_sinks_f16(const AttnParams& p, int D, void* workspace, hipStream_t s) {
+  return chunk_of_type<Hf, false, true>(p, D, workspace, s);
+}
+
+}  // namespace gdn

@@ -289,11 +289,16 @@ struct AttnParams {
   void* seqs;      // [B]: the sequences, when they are more than 1024
   void* head;       // PlanHead; null: few tiles, every workgroup plans for itself
 };
-// by the type of the queries and of the cache (8: e4m3 with p.scales), each in a source of its own
-hipError_t launch_attention_bf16(const AttnParams& p, int D, void* workspace, hipStream_t s);
-hipError_t launch_attention_f16(const AttnParams& p, int D, void* workspace, hipStream_t s);
-hipError_t launch_attention8_bf16(const AttnParams& p, int D, void* workspace, hipStream_t s);
-hipError_t launch_attention8_f16(const AttnParams& p, int D, void* workspace, hipStream_t s);
+// chunks by the type of the queries and of the cache (8: e4m3 with p.scales), with sinks or without, each in a source of
+// its own
+hipError_t launch_chunk_bf16(const AttnParams& p, int D, void* workspace, hipStream_t s);
+hipError_t launch_chunk_sinks_bf16(const AttnParams& p, int D, void* workspace, hipStream_t s);
+hipError_t launch_chunk8_bf16(const AttnParams& p, int D, void* workspace, hipStream_t s);
+hipError_t launch_chunk8_sinks_bf16(const AttnParams& p, int D, void* workspace, hipStream_t s);
+hipError_t launch_chunk_f16(const AttnParams& p, int D, void* workspace, hipStream_t s);
+hipError_t launch_chunk_sinks_f16(const AttnParams& p, int D, void* workspace, hipStream_t s);
+hipError_t launch_chunk8_f16(const AttnParams& p, int D, void* workspace, hipStream_t s);
+hipError_t launch_chunk8_sinks_f16(const AttnParams& p, int D, void* workspace, hipStream_t s);
 hipError_t launch_attention(const AttnParams& p, int D, int dtype, void* workspace, hipStream_t s);
 size_t attention_bytes(int D, int64_t T, int64_t B, int64_t group);  // workspace of launch_attention
 

@@ -84,12 +84,13 @@ __device__ __forceinline__ float scale_for(float top) {
 }
 __device__ __forceinline__ float inverse(float scale) { return __uint_as_float(0x7f000000u - __float_as_uint(scale)); }
 
-// What is stored of a value: NaN for those that are not finite; in fp16, whose largest
-// value lies between two codes, no more than the lower of them.
+// What is stored of a value: NaN for those that are not finite, and no magnitude whose
+// code would stand for more than the rows' type holds: 15/8 of its highest power of
+// two (240 codes times 2^8 in fp16, 2^120 in bf16).
 template <class Tag>
 __device__ __forceinline__ float storable(float x) {
-  if constexpr (Tag::kFp16) x = __builtin_isfinite(x) ? fminf(fmaxf(x, -61440.f), 61440.f) : x;
-  return __builtin_isfinite(x) ? x : __builtin_nanf("");
+  constexpr float most = Tag::kFp16 ? 0x1.ep15f : 0x1.ep127f;
+  return __builtin_isfinite(x) ? fminf(fmaxf(x, -most), most) : __builtin_nanf("");
 }
 
 // 4 values as codes
