@@ -5,7 +5,9 @@
 //   r = (sum x^2 / D + eps)^(-1/2),   out = R (x r w').
 // For the gradient g of out, with y = R^T g (the opposite angles) and n = y w':
 //   dx = r (n - x r^2 (sum n x) / D),   dw = sum over the rows of y x r.
-// Every value is read once and written once, so both are bound by memory.
+// Every value is read once and written once, so both are bound by memory: the gradient
+// of 32,768 tokens (40 heads of 128, bf16, 1.02 GB) 190 us, 5.4 TB/s, about 6 of them
+// the sum over the workgroups (an elementwise sum of two tensors into a third: 5.9).
 //
 // A row is a power of two of neighbouring lanes', each with the two pieces of W
 // values that the rotation pairs (as in rope_kernel), so the row's sums are
@@ -102,7 +104,6 @@ __global__ __launch_bounds__(kNormThreads) void norm_rope_grad_kernel(RopeParams
                                                                      float* partial) {
   typedef typename Tag::type E;
   constexpr int R = kNormUnits<W>;
-  __shared__ Place place[kNormTokens];
   extern __shared__ float sums[];  // [rows at a time][D]
   const int which = (int)blockIdx.x < g.kind[0].blocks ? 0 : 1;
   const NormGradDev::Kind& kind = g.kind[which];
@@ -117,14 +118,13 @@ __global__ __launch_bounds__(kNormThreads) void norm_rope_grad_kernel(RopeParams
 
   for (int64_t t0 = (int64_t)me * per; t0 < p.T; t0 += (int64_t)kind.blocks * per) {
     const int tokens = (int)min((int64_t)per, p.T - t0);
-    __syncthreads();
-    if (threadIdx.x < 64) find_places(p, t0, tokens, place);
-    __syncthreads();
-    const uint32_t rows = (uint32_t)tokens * kind.heads.d;
-    for (uint32_t row = threadIdx.x >> n.shift; row < rows; row += kNormThreads >> n.shift) {
+    const uint32_t rows = (uint32_t)tokens * kind.heads.d, groups = kNormThreads >> n.shift;
+    for (uint32_t row = threadIdx.x >> n.shift; row < rows; row += groups) {
       const uint32_t tok = div_by(row, kind.heads);
       const int h = (int)(row - tok * kind.heads.d);
-      const int64_t t = t0 + tok, pos = place[tok].pos;
+      const int64_t t = t0 + tok;
+      // (32 rows of a position and more: from the cache, sooner than by way of LDS and a barrier)
+      const int64_t pos = p.pos64 ? ((const int64_t*)p.pos)[t] : (int64_t)((const int32_t*)p.pos)[t];
       const E* src = (const E*)kind.x.p + t * kind.x.ts + h * kind.x.hs;
       const E* grad = (const E*)kind.g.p + t * kind.g.ts + h * kind.g.hs;
       float x[R][2][W], y[R][2][W], square = 0.f, along = 0.f;
@@ -135,6 +135,12 @@ __global__ __launch_bounds__(kNormThreads) void norm_rope_grad_kernel(RopeParams
         const Columns<NEAR, W> c(w, p.D, p.rot);
         load_unit<W, NT>(src, c.a, c.b, x[r]);
         load_unit<W, NT>(grad, c.a, c.b, y[r]);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int w = sub + r * L;
+        if (w >= n.units) continue;
+        const Columns<NEAR, W> c(w, p.D, p.rot);
         if (c.turned) turn_unit<NEAR, W>(p, pos, c.a, c.b, -p.sign, y[r]);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
@@ -242,7 +248,8 @@ hipError_t launch_norm_width(RopeParams p, NormDev n, hipStream_t s) {
 }
 
 // Workgroups of the gradient: what the compute units hold at once, fewer for few rows; the keys' share
-// of them by heads.
+// of them by heads.  They take turns of two rows a thread (32,768 tokens: 190 us; four rows 197, sixteen 215:
+// neighbours in memory are best read at once); two rows on the way in a thread leave room for fewer waves (203).
 struct GradGrid {
   int q_blocks, k_blocks;
 };
@@ -262,7 +269,7 @@ hipError_t launch_grad_width(RopeParams p, NormDev n, NormGradDev g, void* dwq, 
   const int groups = kNormThreads >> n.shift;
   const GradGrid grid = grad_grid(p.T, p.Hq, p.Hk, groups);
   auto deal = [&](NormGradDev::Kind& k, int H, int blocks) {
-    const int64_t share = blocks ? (p.T + blocks - 1) / blocks : 1, few = std::max(1, 4 * groups / std::max(1, H));
+    const int64_t share = blocks ? (p.T + blocks - 1) / blocks : 1, few = std::max(1, 2 * groups / std::max(1, H));
     k.blocks = blocks;
     k.tokens = (int)std::max<int64_t>(1, std::min<int64_t>({share, kNormTokens, few}));
   };

@@ -220,9 +220,19 @@ __device__ __forceinline__ void load_weights(const NormDev& n, const void* w, in
   }
 }
 
-// The sum over a row's lanes.
+// x of the lane that a DPP control names (quad_perm, half_mirror, mirror: within 16 lanes).
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+// The sum over a row's lanes, a power of two of neighbours (up to 16 of them without LDS: the
+// sums of pairs, quads and eights are all their lanes', so any lane of the other one will do).
 __device__ __forceinline__ float row_sum(float x, int lanes) {
-  for (int m = 1; m < lanes; m <<= 1) x += __shfl_xor(x, m, 64);
+  if (lanes > 1) x += dpp<0xb1>(x);   // quad_perm 1 0 3 2
+  if (lanes > 2) x += dpp<0x4e>(x);   // quad_perm 2 3 0 1
+  if (lanes > 4) x += dpp<0x141>(x);  // row_half_mirror
+  if (lanes > 8) x += dpp<0x140>(x);  // row_mirror
+  for (int m = 16; m < lanes; m <<= 1) x += __shfl_xor(x, m, 64);
   return x;
 }
 
