@@ -103,15 +103,15 @@ def _scales(k_scale, v_scale, k_cache, page_size: int, dev) -> _ScalesC:
         raise ValueError("an 8-bit cache needs k_scale and v_scale, and no other takes them")
     _need(k_scale, "k_scale", torch.float32, dev, contiguous=False)
     _need(v_scale, "v_scale", torch.float32, dev, contiguous=False)
-    pages, _, heads, _ = k_cache.shape
-    if k_scale.dim() != 3 or k_scale.shape[0] != pages or k_scale.shape[2] != heads or not k_scale.shape[1]:
-        raise ValueError(f"k_scale must be [{pages}, blocks of a page, {heads}], got {tuple(k_scale.shape)}")
-    if v_scale.shape != k_scale.shape:
+    shape, (pages, _, heads, _) = k_scale.shape, k_cache.shape
+    if len(shape) != 3 or shape[0] != pages or shape[2] != heads or not shape[1]:
+        raise ValueError(f"k_scale must be [{pages}, blocks of a page, {heads}], got {tuple(shape)}")
+    if v_scale.shape != shape:
         raise ValueError(f"v_scale must have the shape of k_scale, got {tuple(v_scale.shape)}")
     stride = k_scale.stride()
-    if any(a != b and n > 1 for a, b, n in zip(stride, v_scale.stride(), k_scale.shape)):
+    if v_scale.stride() != stride and any(a != b and n > 1 for a, b, n in zip(stride, v_scale.stride(), shape)):
         raise ValueError("k_scale and v_scale must have the same strides")
-    blocks = k_scale.shape[1]
+    blocks = shape[1]
     if page_size % blocks:
         raise ValueError(f"pages of {page_size} tokens do not divide into {blocks} blocks")
     # (no pages: stand-ins that are never read)
@@ -121,19 +121,21 @@ def _scales(k_scale, v_scale, k_cache, page_size: int, dev) -> _ScalesC:
 
 def _norm(q_weight, k_weight, eps: float, offset: float, dtype, dim: int, dev) -> _NormC:
     """Weights [dim] of one type, the rows' or fp32; None: not normed."""
-    given = [w for w in (q_weight, k_weight) if w is not None]
-    for w, name in ((q_weight, "q"), (k_weight, "k")):
+    # (as few questions as there can be: at one token the host's time is all there is)
+    first = q_weight if q_weight is not None else k_weight
+    for w in (q_weight, k_weight):
         if w is None:
             continue
         if not isinstance(w, torch.Tensor):
-            raise TypeError(f"the norm's weight of {name} must be a tensor")
-        if w.dtype not in (dtype, torch.float32) or w.dtype != given[0].dtype:
+            raise TypeError("the norm's weights must be tensors")
+        if w.dtype != first.dtype or (w.dtype != dtype and w.dtype != torch.float32):
             raise TypeError(f"the norm's weights must be of one type, {dtype} or torch.float32, got {w.dtype}")
-        _need(w, f"the norm's weight of {name}", w.dtype, dev)
-        if tuple(w.shape) != (dim,):
-            raise ValueError(f"the norm's weight of {name} must be [{dim}], got {tuple(w.shape)}")
-    ptr = [None if w is None else w.data_ptr() for w in (q_weight, k_weight)]
-    return _NormC(*ptr, DTYPES[given[0].dtype] if given else DTYPES[dtype], float(eps), float(offset))
+        if w.device != dev:
+            raise ValueError(f"the norm's weights are on {w.device}, expected {dev}")
+        if w.shape != (dim,) or not w.is_contiguous():
+            raise ValueError(f"the norm's weights must be contiguous [{dim}], got {tuple(w.shape)}")
+    return _NormC(None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
+                  DTYPES[dtype if first is None else first.dtype], float(eps), float(offset))
 
 
 def _rope(table, interleaved: bool, transposed: bool, dev) -> _RopeC:
@@ -275,8 +277,11 @@ def norm_rope(q, k, q_weight, k_weight, table, positions, eps: float = 1e-6, wei
     ``q_weight`` and ``k_weight`` [D] are of the rows' type or fp32, both alike (D at most 512).  q, k and
     the weights that require a gradient get it; ``q_out`` or ``k_out`` (they may be q and k) exclude
     that, and the table has no gradient."""
-    given = (q, k, q_weight, k_weight, table, q_out, k_out)
-    if torch.is_grad_enabled() and any(getattr(x, "requires_grad", False) for x in given):
+    if torch.is_grad_enabled() and (
+            getattr(q, "requires_grad", False) or getattr(k, "requires_grad", False)
+            or getattr(q_weight, "requires_grad", False) or getattr(k_weight, "requires_grad", False)
+            or getattr(table, "requires_grad", False) or getattr(q_out, "requires_grad", False)
+            or getattr(k_out, "requires_grad", False)):
         if getattr(table, "requires_grad", False):
             raise RuntimeError("norm_rope: the table has no gradient")
         if q_out is not None or k_out is not None:

@@ -1415,11 +1415,17 @@ hipError_t launch_chunk(AttnParams p, void* workspace, hipStream_t s) {
 
 constexpr int kDecTile = 32;   // keys of a tile
 constexpr int kDecRows = 16;   // query rows of a run
-constexpr int kDecPages = 512; // page ids a wave stages at a time
+template <bool Q8>
+constexpr int kDecPages = Q8 ? 256 : 512;  // page ids a wave stages at a time
+template <int D>
+constexpr int kDecStages = D == 64 ? 2 : 1;  // tiles of keys (and of values) in a wave's ring
+// Workgroups a compute unit holds.  A tile of codes takes as many instructions as one of 16-bit values and half the
+// time on the way, so more waves carry them, with one tile each in place of two (4 of 131,072 tokens 212 -> 187 us,
+// 512 of up to 300 50 -> 44 us, at D 256 299 -> 291 us; 512 of up to 4,096 alike; with 4 the registers do not suffice).
 template <int D, bool Q8>
-constexpr int kDecStages = (D == 64 ? 2 : 1) * (Q8 ? 2 : 1);  // tiles of keys (and of values) in a wave's ring
+constexpr int kDecPerCu = Q8 ? (D == 256 ? 2 : 3) : D == 256 ? 1 : 2;
 template <int D, bool Q8>
-constexpr int kDecLds = kWaves * kDecStages<D, Q8> * 2 * kDecTile * D * (Q8 ? 1 : 2);
+constexpr int kDecLds = kWaves * kDecStages<D> * 2 * kDecTile * D * (Q8 ? 1 : 2);
 // Which 16-byte piece of row r of a tile lies in its place c: the turns are their own inverses.  Rows of codes are
 // read 16 keys' piece at a time, and transposed 8 keys' of two groups (keys 4 g .. and 16 + 4 g ..), which the turns
 // spread over the banks.
@@ -1477,8 +1483,8 @@ __device__ __forceinline__ int dec_tiles(const Span& s) {
   return s.len <= s.begin ? 0 : dec_first_tiles(s) + (s.len + kDecTile - 1) / kDecTile - s.begin / kDecTile;
 }
 template <class E, int D, Cap CAP, bool Q8>
-__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(AttnParams p) {
-  constexpr int NS = kDecStages<D, Q8>;
+__global__ __launch_bounds__(64 * kWaves, (kDecPerCu<D, Q8>)) void decode_kernel(AttnParams p) {
+  constexpr int NS = kDecStages<D>;
   constexpr int kBytes = Q8 ? 1 : 2;          // of a value in the cache
   constexpr int kRow = kBytes * D, kPieces = kRow / 16;
   constexpr int kSlot = kDecTile * kRow;      // bytes of a tile's keys
@@ -1487,7 +1493,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
   constexpr int kRowsPerLoad = 1024 / kRow;
   constexpr int kSteps = D / 32, kBlocks = D / 16;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
-  __shared__ int staged_ids[kWaves][kDecPages];
+  __shared__ int staged_ids[kWaves][kDecPages<Q8>];
   __shared__ __attribute__((aligned(16))) float staged_scales[Q8 ? kWaves * NS * 64 : 1];
   __shared__ int s_where[kWaves][3];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), grp = lane >> 4, col = lane & 15;
@@ -1595,7 +1601,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode_kernel(A
     // as many tiles at a time as the staged page ids reach
     for (int a0 = part ? max(tile_a * kDecTile, sp.begin) : tile_a * kDecTile; a0 < key_b;) {
       const int page0 = (int)div_by(a0, p.kv.page);
-      const int64_t reach = (int64_t)(page0 + kDecPages) * p.kv.page.d;  // first key past the staged pages
+      const int64_t reach = (int64_t)(page0 + kDecPages<Q8>) * p.kv.page.d;  // first key past the staged pages
       // (whole tiles; kDecPages pages are more than a tile's keys)
       const int a1 = reach >= key_b ? key_b : (int)reach / kDecTile * kDecTile;
       const int last = (int)div_by(a1 - 1, p.kv.page);
@@ -1903,9 +1909,9 @@ __global__ __launch_bounds__(256) void decode_join_kernel(AttnParams p) {
 }
 
 // Waves of a decode: as many as the compute units hold at once.
-template <int D>
+template <int D, bool Q8>
 int decode_shares() {
-  return kWaves * device_cus() * (D == 256 ? 1 : 2);
+  return kWaves * device_cus() * kDecPerCu<D, Q8>;
 }
 
 template <class E, int D, Cap CAP, bool Q8>
@@ -1913,7 +1919,7 @@ hipError_t launch_decode_cap(const AttnParams& p, hipStream_t s) {
   static std::atomic<bool> raised[kMaxDevices];
   hipError_t e = allow_lds(decode_kernel<E, D, CAP, Q8>, kDecLds<D, Q8>, raised);
   if (e != hipSuccess) return e;
-  const int shares = decode_shares<D>();
+  const int shares = decode_shares<D, Q8>();
   decode_kernel<E, D, CAP, Q8><<<dim3(shares / kWaves), dim3(64 * kWaves), kDecLds<D, Q8>, s>>>(p);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int rows = std::min<int>(kDecRows, (int)p.group.d), groups = 1024 / D;
@@ -1929,7 +1935,7 @@ hipError_t launch_decode_cap(const AttnParams& p, hipStream_t s) {
 
 template <class E, int D, bool Q8>
 hipError_t launch_dec(AttnParams p, void* workspace, hipStream_t s) {
-  const int shares = decode_shares<D>();
+  const int shares = decode_shares<D, Q8>();
   p.part_o = (float*)workspace;
   p.part_ml = p.part_o + (int64_t)2 * shares * kDecRows * D;
   p.parts = (int*)(p.part_ml + (int64_t)2 * shares * kDecRows * 2);
@@ -1940,7 +1946,8 @@ hipError_t launch_dec(AttnParams p, void* workspace, hipStream_t s) {
 
 template <int D>
 size_t decode_bytes() {
-  return (size_t)decode_shares<D>() * (2 * kDecRows * (D + 2) * sizeof(float) + 4 * sizeof(int));
+  const int shares = std::max(decode_shares<D, false>(), decode_shares<D, true>());
+  return (size_t)shares * (2 * kDecRows * (D + 2) * sizeof(float) + 4 * sizeof(int));
 }
 
 // Chunks of one element type, over a cache of the same type or (Q8) of 8 bits; decode of it.
