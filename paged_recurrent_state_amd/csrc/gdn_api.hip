@@ -834,6 +834,7 @@ int check_norm(const gdn_norm_t* norm, int32_t dtype, int32_t head_dim, NormDev&
   n.wq = norm->q_weight;
   n.wk = norm->k_weight;
   n.wide = norm->weight_dtype == GDN_TYPE_F32;
+  n.vector = (uintptr_t)norm->q_weight % 16 == 0 && (uintptr_t)norm->k_weight % 16 == 0;
   n.eps = norm->eps;
   n.offset = norm->offset;
   return GDN_OK;

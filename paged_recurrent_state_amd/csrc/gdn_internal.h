@@ -226,7 +226,8 @@ constexpr int kNormMaxDim = 512;  // values of a normed head at most
 struct NormDev {
   const void* wq;  // weights [D] of the queries, of the keys; null: not normed
   const void* wk;
-  int wide;  // the weights are fp32
+  int wide;    // the weights are fp32
+  int vector;  // and start at multiples of 16 bytes
   float eps, offset;
   // set by the launch
   int units, shift;  // units of a row (see RopeParams.row_units) and log2 of its lanes

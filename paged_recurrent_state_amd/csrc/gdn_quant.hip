@@ -244,9 +244,12 @@ __global__ __launch_bounds__(kQuantThreads, 3) void quant_append_kernel(RopePara
     return top;
   };
   // A block's scale with the new tokens' largest value; codes that were there are taken to it.
-  auto settle = [&](bool V, int h, const Lead& l, float top, int row, int step) __attribute__((always_inline)) {
-    float* at = (V ? sc.v : sc.k) + l.scale + h * sc.hs;
-    const float old = l.before ? *at : 0.f, scale = fmaxf(old, scale_for(top));
+  // (`old` is read as early as may be: it is a wait of its own)
+  auto old_scale = [&](bool V, int h, const Lead& l) __attribute__((always_inline)) {
+    return l.before ? ((V ? sc.v : sc.k) + l.scale)[h * sc.hs] : 0.f;
+  };
+  auto settle = [&](bool V, int h, const Lead& l, float old, float top, int row, int step) __attribute__((always_inline)) {
+    const float scale = fmaxf(old, scale_for(top));
     if (l.before && scale > old) {
       char* base = (V ? p.kv.v : p.kv.k) + l.dst + h * p.kv.hs;
 #pragma unroll 1
@@ -306,6 +309,7 @@ __global__ __launch_bounds__(kQuantThreads, 3) void quant_append_kernel(RopePara
       const int j = i - q_items, tok = few[j / (2 * hn)], k = j % (2 * hn), h = h0 + (k >> 1);
       const bool V = k & 1;
       const Lead l = leads[tok];
+      const float old = old_scale(V, h, l);
       float top = 0.f;
 #pragma unroll 1
       for (int r = 0; r < l.rows; ++r) {
@@ -324,7 +328,7 @@ __global__ __launch_bounds__(kQuantThreads, 3) void quant_append_kernel(RopePara
         }
         for (int m = 1; m < L; m <<= 1) top = fmaxf(top, __shfl_xor(top, m, 64));
       }
-      const float scale = settle(V, h, l, top, 0, 1);
+      const float scale = settle(V, h, l, old, top, 0, 1);
       // (the row's lanes are of one wave: they have all read the old scale)
       if (sub == 0) ((V ? sc.v : sc.k) + l.scale)[h * sc.hs] = scale;
       const float inv = inverse(scale);
@@ -356,6 +360,7 @@ __global__ __launch_bounds__(kQuantThreads, 3) void quant_append_kernel(RopePara
       const int item = i * teams + wave / team;  // (those past the last only wait)
       const bool mine = item < 2 * hn, V = item & 1;
       const int h = h0 + min(item >> 1, hn - 1);
+      const float old = mine ? old_scale(V, h, l) : 0.f;
       float x[kKept][2][W], top = 0.f, inv = 1.f;
       bool change = false;
       // first the largest value, once more where some cannot be stored as they are, then the codes
@@ -413,7 +418,7 @@ __global__ __launch_bounds__(kQuantThreads, 3) void quant_append_kernel(RopePara
           phase = 1;
         }
         float scale = 1.f;
-        if (mine) scale = settle(V, h, l, top, row, step);
+        if (mine) scale = settle(V, h, l, old, top, row, step);
         if (team > 1) __syncthreads();  // (everyone has read the old scale)
         if (mine && row == 0 && sub == 0) ((V ? sc.v : sc.k) + l.scale)[h * sc.hs] = scale;
         inv = inverse(scale);

@@ -206,6 +206,24 @@ __device__ __forceinline__ void load_weights(const NormDev& n, const void* w, in
     for (int i = 0; i < W; ++i) x[r][0][i] = x[r][1][i] = 0.f;
     if (w && sub + r * L < n.units) {
       const Columns<NEAR, W> c(sub + r * L, D, rot);
+      if (W > 1 && n.vector) {
+        if (n.wide) {
+#pragma unroll
+          for (int i = 0; i < W; i += W < 4 ? W : 4) {
+            load<(W < 4 ? W : 4)>((const float*)w + c.a + i, *(float(*)[W < 4 ? W : 4])(x[r][0] + i));
+            load<(W < 4 ? W : 4)>((const float*)w + c.b + i, *(float(*)[W < 4 ? W : 4])(x[r][1] + i));
+          }
+        } else {
+          load<W>((const typename Tag::type*)w + c.a, x[r][0]);
+          load<W>((const typename Tag::type*)w + c.b, x[r][1]);
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          x[r][0][i] += n.offset;
+          x[r][1][i] += n.offset;
+        }
+        continue;
+      }
       // (one by one: the weights may start anywhere)
 #pragma unroll
       for (int i = 0; i < W; ++i) {
