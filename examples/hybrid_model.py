@@ -2,11 +2,14 @@
 and every fourth layer attention on a paged key/value cache.
 
     python examples/hybrid_model.py [--prompts 700 130 1] [--chunk 256] [--tokens 8]
+                                    [--norms] [--cache8] [--window 200 --sinks 4]
 
 The prompts are fed in chunks (append with rotary positions, attention of the
 chunk's tokens; the recurrent layers from the states their pages hold), then one
 token per sequence is decoded at a time, greedily.  Weights and prompts are random.
 The same prompts fed whole end in the same logits up to rounding, which the command prints.
+``--norms`` norms the heads of queries and keys before they turn, ``--cache8`` keeps keys and values in 8
+bits with a scale for each 16 tokens and head, ``--sinks`` keeps first tokens visible beside a window.
 """
 
 from __future__ import annotations
@@ -54,14 +57,15 @@ class Pages:
 
 class Model:
     def __init__(self, layers=4, hidden=512, heads=8, kv_heads=2, dim=128, rot=64, vocab=1024, pages=64,
-                 page_size=128, window=0, softcap=0.0, positions=8192, device="cuda", seed=0):
+                 page_size=128, window=0, softcap=0.0, positions=8192, device="cuda", seed=0, sinks=0, norms=False,
+                 cache8=False):
         gen = torch.Generator(device=device).manual_seed(seed)
 
         def weight(n_in, n_out):
             return (torch.randn(n_in, n_out, generator=gen, device=device) * n_in ** -0.5).to(BF16)
 
         self.heads, self.kv_heads, self.dim = heads, kv_heads, dim
-        self.attention = dict(window=window, softcap=softcap)
+        self.attention = dict(window=window, softcap=softcap, sinks=sinks)
         self.table = gdn.rope_table(positions, rot, device=device)
         self.embedding = weight(vocab, hidden) * vocab ** 0.5
         self.head = weight(hidden, vocab)
@@ -69,8 +73,16 @@ class Model:
         for i in range(layers):
             if i % 4 == 3:
                 kv = torch.zeros(2, pages, page_size, kv_heads, dim, dtype=BF16, device=device)
-                self.layers.append(dict(kind="attention", qkv=weight(hidden, (heads + 2 * kv_heads) * dim),
-                                        out=weight(heads * dim, hidden), kv=kv))
+                layer = dict(kind="attention", qkv=weight(hidden, (heads + 2 * kv_heads) * dim),
+                             out=weight(heads * dim, hidden), kv=kv, scales={}, norms={})
+                if cache8:
+                    layer["kv"] = kv.to(torch.float8_e4m3fn)
+                    layer["scales"] = {n: torch.ones(pages, page_size // 16, kv_heads, device=device)
+                                       for n in ("k_scale", "v_scale")}
+                if norms:
+                    layer["norms"] = {n: 1.0 + 0.1 * torch.randn(dim, generator=gen, device=device)
+                                      for n in ("q_norm", "k_norm")}
+                self.layers.append(layer)
             else:
                 state = torch.zeros(pages, heads, dim, dim, device=device)
                 self.layers.append(dict(kind="recurrent", qkv=weight(hidden, 3 * heads * dim),
@@ -80,10 +92,10 @@ class Model:
         H, Hk = self.heads, self.kv_heads
         qkv = (x @ w["qkv"]).view(-1, H + 2 * Hk, self.dim)
         q, k, v = qkv.split([H, Hk, Hk], dim=1)  # views: the calls take their strides
-        q = gdn.kv_append_paged(k, v, cu, *w["kv"], *where, table=self.table, q=q)
+        q = gdn.kv_append_paged(k, v, cu, *w["kv"], *where, table=self.table, q=q, **w["norms"], **w["scales"])
         if cu is None:
-            return gdn.attention_decode_paged(q, *w["kv"], *where, **self.attention)
-        return gdn.attention_prefill_paged(q, cu, *w["kv"], *where, **self.attention)
+            return gdn.attention_decode_paged(q, *w["kv"], *where, **self.attention, **w["scales"])
+        return gdn.attention_prefill_paged(q, cu, *w["kv"], *where, **self.attention, **w["scales"])
 
     def _recur(self, w, x, where, cu):
         q, k, v = (x @ w["qkv"]).view(-1, 3, self.heads, self.dim).unbind(1)
@@ -147,12 +159,15 @@ def main(argv=None):
     ap.add_argument("--tokens", type=int, default=8)
     ap.add_argument("--window", type=int, default=0)
     ap.add_argument("--softcap", type=float, default=0.0)
+    ap.add_argument("--sinks", type=int, default=0)
+    ap.add_argument("--norms", action="store_true")
+    ap.add_argument("--cache8", action="store_true")
     a = ap.parse_args(argv)
     if min(a.prompts) < 1 or a.chunk < 1 or a.tokens < 0:
         ap.error("prompts and chunks have one token or more, and --tokens is 0 or more")
     gen = torch.Generator().manual_seed(1)
     prompts = [torch.randint(0, 1024, (n,), generator=gen).to("cuda") for n in a.prompts]
-    kw = dict(window=a.window, softcap=a.softcap)
+    kw = dict(window=a.window, softcap=a.softcap, sinks=a.sinks, norms=a.norms, cache8=a.cache8)
     first, out, _, each = generate(prompts, a.chunk, a.tokens, **kw)
     whole = generate(prompts, max(a.prompts), 0, **kw)[0]
     diff = ((first - whole).float().norm() / whole.float().norm()).item()
