@@ -274,7 +274,7 @@ typedef struct {
 } gdn_attention_dims_t;
 
 /*
- * Workspace bytes of either attention call for at most total_tokens query rows
+ * Workspace bytes of any attention call for at most total_tokens query rows
  * in at most num_seqs sequences (an upper bound that never decreases as either
  * grows), 256-byte aligned.  0 on bad dims.
  */
@@ -316,7 +316,8 @@ int gdn_attention_decode_paged(const gdn_attention_dims_t* dims, const gdn_rows_
  *     Without one it means nothing.
  *   scales: of an 8-bit cache, or NULL for one of dims->dtype.  The result is that
  *     of a cache that holds the values, code times scale, rounded to dims->dtype
- *     (exact in bf16; in fp16 magnitudes over 65,504 become infinite).
+ *     (exact in bf16; in fp16 magnitudes over 65,504 become infinite, and an output
+ *     that sees one infinite or NaN).
  * Errors as the calls above, and GDN_EINVAL for sinks < 0 or over 2^30, null or
  * unaligned scales or a bad block; GDN_EUNSUPPORTED for chunks over an 8-bit cache
  * whose token stride is negative or reaches 2^30 / page_size.

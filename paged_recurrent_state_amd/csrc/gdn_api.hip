@@ -1008,7 +1008,7 @@ int run_attention(const gdn_attention_dims_t* dims, int32_t sinks, const gdn_row
   if (!aligned(out, T, dims->num_q_heads, 2, 16)) return fail(GDN_EINVAL, "rows of out must be 16-byte aligned");
   if (!scales && !aligned(cache, dims->num_kv_heads, 2, 16))
     return fail(GDN_EINVAL, "rows of the cache must be 16-byte aligned");
-  const size_t need = gdn_attention_workspace_size(dims, T, cache->num_seqs);
+  const size_t need = attention_bytes(dims->head_dim, T, cache->num_seqs, group, scales != nullptr);
   if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255))
     return fail(GDN_EWORKSPACE, "workspace needs %zu bytes, 256-byte aligned (got %zu)", need,
                 workspace ? workspace_bytes : 0);
@@ -1217,7 +1217,7 @@ int gdn_kv_read_paged(int32_t dtype, int32_t head_dim, int32_t num_kv_heads, con
 
 size_t gdn_attention_workspace_size(const gdn_attention_dims_t* dims, int64_t total_tokens, int32_t num_seqs) {
   if (check_attention(dims) || total_tokens < 0 || num_seqs < 0) return 0;
-  return attention_bytes(dims->head_dim, total_tokens, num_seqs, dims->num_q_heads / dims->num_kv_heads);
+  return attention_bytes(dims->head_dim, total_tokens, num_seqs, dims->num_q_heads / dims->num_kv_heads, true);
 }
 
 int gdn_attention_prefill_paged_ext(const gdn_attention_dims_t* dims, int32_t sinks, const gdn_rows_t* q,

@@ -1945,8 +1945,8 @@ hipError_t launch_dec(AttnParams p, void* workspace, hipStream_t s) {
 }
 
 template <int D>
-size_t decode_bytes() {
-  const int shares = std::max(decode_shares<D, false>(), decode_shares<D, true>());
+size_t decode_bytes(bool codes) {
+  const int shares = codes ? decode_shares<D, true>() : decode_shares<D, false>();
   return (size_t)shares * (2 * kDecRows * (D + 2) * sizeof(float) + 4 * sizeof(int));
 }
 
