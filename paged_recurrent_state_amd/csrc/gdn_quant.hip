@@ -18,8 +18,9 @@
 //
 // Bound by memory and by the waits of a workgroup's start (sequence, page, page id) and of
 // each block (rows, largest value, scale): 32 ragged prompts (14,652 tokens, 32 q-heads
-// on 8 of 128, 338 MB) 82 us, 4.1 TB/s, of which the queries alone take 45 in rope_kernel;
-// with every row read twice and half of a workgroup a block 107 us.
+// on 8 of 128, 338 MB) 77 us, 4.4 TB/s, of which the queries alone take 45 in rope_kernel.
+// Blocks of one wave dealt out one lead after another, two waves idle: 82 us, 492 sequences
+// of up to 49 tokens 30 us against 19; every row read twice and half of a workgroup a block: 107.
 #include <algorithm>
 #include <type_traits>
 
@@ -169,7 +170,7 @@ __global__ __launch_bounds__(kQuantThreads, 3) void quant_append_kernel(RopePara
                                                                     int q_per) {
   typedef typename Tag::type E;
   __shared__ Lead leads[kQuantTokens];
-  __shared__ int few[kQuantTokens], many[kQuantTokens], counts[2];
+  __shared__ int few[kQuantTokens], many[kQuantTokens], counts[3];  // many: first those that one wave takes
   __shared__ float tops[kQuantThreads / 64];
   const int64_t t0 = (int64_t)blockIdx.x * p.tokens_per_block;
   const int tokens = (int)min((int64_t)p.tokens_per_block, p.T - t0);
@@ -177,13 +178,17 @@ __global__ __launch_bounds__(kQuantThreads, 3) void quant_append_kernel(RopePara
     find_leads(p, sc, t0, tokens, leads);
     const int rows = threadIdx.x < tokens ? leads[threadIdx.x].rows : 0;
     const int shortest = FEW ? kShortBlock : 0;  // (of those a wave takes, less one)
-    const uint64_t s = __ballot(rows > 0 && rows <= shortest), l = __ballot(rows > shortest);
-    const uint64_t below = (uint64_t(1) << threadIdx.x) - 1;
-    if (rows > 0 && rows <= shortest) few[__popcll(s & below)] = threadIdx.x;
-    if (rows > shortest) many[__popcll(l & below)] = threadIdx.x;
+    const int longest = kKept * (64 >> n.shift);  // of one wave
+    const uint64_t s = __ballot(rows > 0 && rows <= shortest), m = __ballot(rows > shortest && rows <= longest);
+    const uint64_t l = __ballot(rows > shortest && rows > longest), below = (uint64_t(1) << threadIdx.x) - 1;
+    if (rows > 0 && rows <= shortest)
+      few[__popcll(s & below)] = threadIdx.x;
+    else if (rows > 0)
+      many[rows <= longest ? __popcll(m & below) : __popcll(m) + __popcll(l & below)] = threadIdx.x;
     if (threadIdx.x == 0) {
       counts[0] = __popcll(s);
-      counts[1] = __popcll(l);
+      counts[1] = __popcll(m);
+      counts[2] = __popcll(m) + __popcll(l);
     }
   }
   const int L = 1 << n.shift, sub = threadIdx.x & (L - 1);
@@ -344,22 +349,24 @@ __global__ __launch_bounds__(kQuantThreads, 3) void quant_append_kernel(RopePara
   }
 
   // Blocks of more: one, two or all waves each, as many as keep its rows in registers (kKept a lane); beyond
-  // that half of the workgroup, which reads the rows twice.  Where more than one wave has a part, all wait for
-  // each other (every wave goes through the same turns).
+  // that half of the workgroup, which reads the rows twice.  Those of one wave are dealt out together; where more
+  // than one wave has a part, all wait for each other (every wave goes through the same turns).
   constexpr int kWaves = kQuantThreads / 64;
-  const int many_leads = __builtin_amdgcn_readfirstlane(counts[1]);
+  const int alone = __builtin_amdgcn_readfirstlane(counts[1]), many_leads = __builtin_amdgcn_readfirstlane(counts[2]);
+  int together = alone ? alone : 1;
 #pragma unroll 1
-  for (int j = 0; j < many_leads; ++j) {
-    const int tok = __builtin_amdgcn_readfirstlane(many[j]);
-    const Lead l = uniform_lead(leads[tok]);
-    const int team = l.rows <= kept ? 1 : l.rows > 2 * kept && l.rows <= kWaves * kept ? kWaves : 2;  // waves
+  for (int j = 0; j < many_leads; j += together, together = 1) {
+    const int rows = __builtin_amdgcn_readfirstlane(leads[many[j]].rows);
+    const int team = j < alone ? 1 : rows > 2 * kept && rows <= kWaves * kept ? kWaves : 2;  // waves
     const int step = team * at_once, row = (wave & (team - 1)) * at_once + lane_row, most = kKept * step;
-    const int teams = kWaves / team, turns = (2 * hn + teams - 1) / teams;
+    const int teams = kWaves / team, work = 2 * hn * together, turns = (work + teams - 1) / teams;
 #pragma unroll 1
     for (int i = 0; i < turns; ++i) {
-      const int item = i * teams + wave / team;  // (those past the last only wait)
-      const bool mine = item < 2 * hn, V = item & 1;
-      const int h = h0 + min(item >> 1, hn - 1);
+      const int item = i * teams + wave / team, at = min(item, work - 1);  // (those past the last only wait)
+      const int lead = at / (2 * hn), k2 = at - lead * 2 * hn, h = h0 + (k2 >> 1);
+      const bool mine = item < work, V = k2 & 1;
+      const int tok = __builtin_amdgcn_readfirstlane(many[j + lead]);
+      const Lead l = uniform_lead(leads[tok]);
       const float old = mine ? old_scale(V, h, l) : 0.f;
       float x[kKept][2][W], top = 0.f, inv = 1.f;
       bool change = false;
@@ -498,13 +505,14 @@ hipError_t launch_append_width(RopeParams p, NormDev n, const ScalesDev& sc, hip
   while ((1 << n.shift) < n.units) ++n.shift;
   n.inv_dim = 1.f / (float)p.D;
   // one token per sequence: as many as keep the workgroup's threads busy; otherwise a workgroup a kv-head, of 64
-  // tokens where that fills the chip (prompts of 14,652 tokens in blocks of 32, 64, 128: 82, 79, 82 us; of 32 tokens
-  // 82, 88, 89)
+  // tokens where that fills the chip (prompts of 14,652 tokens in blocks of 32, 64, 128: 77, 79, 78 us; of 32 tokens
+  // 79, 86, 86) and no fewer than 4 (21 sequences of up to 11 tokens, 36 q-heads on 3: 12.7 us; with no fewer than 16,
+  // which share the search for their sequence, 20.5)
   const int64_t per_token = (int64_t)(p.Hq + 2 * p.Hk) << n.shift;
   const bool decode = !p.cu;
   const int y = decode ? 1 : p.Hk;
   p.tokens_per_block = decode ? (int)std::max<int64_t>(1, std::min<int64_t>(kQuantTokens, kQuantThreads / per_token))
-                              : (int)std::max<int64_t>(16, std::min<int64_t>(kQuantTokens, p.T * y / (2 * device_cus())));
+                              : (int)std::max<int64_t>(4, std::min<int64_t>(kQuantTokens, p.T * y / (2 * device_cus())));
   const dim3 grid((uint32_t)((p.T + p.tokens_per_block - 1) / p.tokens_per_block), y);
   const int heads = decode ? p.Hk : 1, q_heads = (p.Hq + y - 1) / y;
   const bool norm = n.wq || n.wk, nt = W == 8 && p.T * (p.Hq + 2 * p.Hk) * p.D * 2 > kQuantCacheBytes;

@@ -143,6 +143,13 @@ def test_many_sequences():
     check_exact([1] * 300, [(i * 13) % 90 for i in range(300)], 32, 32, 1, 128, HF, 63, decode=True)
 
 
+@pytest.mark.parametrize("D,block", [(64, 896), (256, 896), (64, 128), (256, 64)])
+def test_blocks_of_every_length_among_one_workgroups_tokens(D, block):
+    """Sixty-four tokens a workgroup, whose blocks one, two or all of its waves take, or read twice."""
+    new = [3, 1, 300, 20, 2, 0, 130, 70, 17, 1100, 5, 40, 9, 33, 257, 64, 128, 16, 1, 1] * 2
+    check_exact(new, [(i * 37) % 120 for i in range(len(new))], 896, block, 8, D, HF if D == 64 else BF, 68)
+
+
 def test_odd_values():
     H, D = 1, 64
     for dtype in (BF, HF):
