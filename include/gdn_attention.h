@@ -212,8 +212,8 @@ typedef struct {
  * new tokens open takes a new scale, whatever it held.  A value is rounded once,
  * to nearest, ties to even; values that are not finite are stored as NaN and count
  * for no scale, and none is stored over 15/8 of the rows' type's highest power of two
- * (61,440 in fp16: the next code is beyond it).  Rows and slots behind the new tokens
- * are left as they are.
+ * (61,440 in fp16: the next code is beyond it).  Slots behind the new tokens are left as
+ * they are, and with norm or scales also rows of q_out behind the last sequence.
  * Errors as gdn_kv_append_paged and gdn_norm_rope (but that a null weight leaves
  * its heads as they are), GDN_EINVAL for null or unaligned scales, a bad block,
  * or a cache that is not 16-byte aligned in every stride and address;

@@ -385,7 +385,8 @@ def kv_append_paged(k, v, cu_seqlens, k_cache, v_cache, page_indices, page_indpt
     types) take ``k_scale`` and ``v_scale`` [pages, page_size / block, Hkv] fp32, written with them: a power of
     two for each ``block`` tokens of a page and head (a multiple of 16), with which the block's largest
     value is at most 448.  A block that tokens are added to keeps its scale or takes the larger new one,
-    its codes rounded to it; one that they open takes a new one."""
+    its codes rounded to it; one that they open takes a new one.  With norms or scales, rows of ``q_out``
+    behind ``cu_seqlens[-1]`` are left as they are."""
     lib = load()
     code, dev = _dtype(k, "k"), k.device
     stream = _stream(dev)

@@ -473,8 +473,19 @@ __device__ __forceinline__ const AttnParams& reloaded() {
 // EVEN: a wave's rows of a tile lie in one page (see launch_chunk).
 // Q8: the cache holds e4m3 codes.  A wave loads its rows' codes into LDS of its own,
 // and a tile ahead writes them as values, times their scales, to the slots that the
-// products read.
-// SINKS: first tokens stay visible beside a window.
+// products read: exact (a power of two times 4 bits), once a tile and workgroup, where
+// codes as operands would be converted by each of the four waves.  The results are
+// those of a 16-bit cache of the same values, bit for bit.  The conversions and their
+// LDS traffic stand beside the products: 2,048 tokens over 32,768 978 to 1,070 us over
+// several cards, 980 where a 16-bit cache takes 927 (188 M vector instructions against
+// 165 M).  Their writes of V meet in the banks; laid
+// out so that they do not, they took the same time.
+// SINKS: first tokens stay visible beside a window.  A run is then its first tokens' key
+// tiles and those of the window, in one row of tiles (TileRec): the parts of one run
+// share a softmax and need no join of their own.  Kernels of their own: the questions
+// cost the scalar registers that calls without sinks need (their chunks were 2% slower).
+// 3,007 new tokens of two sequences with a window of 2,000 and 64 first tokens 132 to 143
+// us, 0 to 4 of them the first tokens'.
 template <class E, int D, Cap CAP, bool EVEN, bool Q8, bool SINKS>
 __global__ __launch_bounds__(64 * kWaves, 1) void chunk_kernel(AttnParams p) {
   typedef Chunk<D, Q8> C;
@@ -1409,7 +1420,12 @@ hipError_t launch_chunk(AttnParams p, void* workspace, hipStream_t s) {
 // 355 us, 6.0 TB/s (a copy reaches 5.7 to 6.0).  Where runs are short their start
 // (page table, page ids, first keys) shows: 512 sequences of up to 150 tokens on 8
 // heads 38 us, against 62 when four waves shared each run and waited for each other;
-// long runs lose 1% to the parts they write.  A run holds 16 query rows: more q-heads
+// long runs lose 1% to the parts they write.  Codes of a cache of 8 bits become values,
+// times their scales, in the registers that feed a product (the values' out of a
+// transposed read of 8-bit elements): 512 sequences of up to 4,096 tokens (1.55 GB) 291
+// to 298 us, 5.2 to 5.3 TB/s, 4 of 131,072 tokens 187 us, 5.7 TB/s.  With first tokens
+// beside a window of 2,048, 256 sequences of up to 16,384 tokens (1.38 GB) 257 to 260 us,
+// 5.3 TB/s (the window alone 255).  A run holds 16 query rows: more q-heads
 // on a kv-head read its keys and values again for every 16 (64 sequences of up to
 // 8,192 tokens, 16 and 32 q-heads on one: 62 and 106 us).
 

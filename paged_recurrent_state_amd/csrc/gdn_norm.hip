@@ -6,7 +6,7 @@
 // For the gradient g of out, with y = R^T g (the opposite angles) and n = y w':
 //   dx = r (n - x r^2 (sum n x) / D),   dw = sum over the rows of y x r.
 // Every value is read once and written once, so both are bound by memory: the gradient
-// of 32,768 tokens (40 heads of 128, bf16, 1.02 GB) 190 us, 5.4 TB/s, about 6 of them
+// of 32,768 tokens (40 heads of 128, bf16, 1.02 GB) 187 to 190 us, 5.4 TB/s, 6 of them
 // the sum over the workgroups (an elementwise sum of two tensors into a third: 5.9).
 //
 // A row is a power of two of neighbouring lanes', each with the two pieces of W
@@ -55,6 +55,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_rope_kernel(RopeParams p, N
     bool is_q = false, is_v = false;
     if (h < p.Hq) {
       is_q = true;
+      if (p.cu && pl.pos == kBehind) continue;
       src = (const E*)p.q.p + t * p.q.ts + h * p.q.hs;
       dst = (E*)p.q_out.p + t * p.q_out.ts + h * p.q_out.hs;
     } else if ((h -= p.Hq) < p.Hk) {

@@ -78,6 +78,7 @@ __device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) 
 struct Place {
   int64_t pos, dst;
 };
+constexpr int64_t kBehind = INT64_MIN;  // the position of a row behind the last sequence
 
 // Finds the places of tokens t0 .. t0 + tokens (64 at most), one a lane; the whole first wave calls it.
 __device__ __forceinline__ void find_places(const RopeParams& p, int64_t t0, int tokens, Place* place) {
@@ -101,7 +102,7 @@ __device__ __forceinline__ void find_places(const RopeParams& p, int64_t t0, int
       b = lo;
     }
     if (lane < tokens) {
-      Place pl{-1, -1};
+      Place pl{kBehind, -1};
       if (b < p.kv.B) {
         const int first = p.kv.ptr[b], pages = p.kv.ptr[b + 1] - first;
         const int64_t len = pages > 0 ? (int64_t)(pages - 1) * p.kv.page.d + p.kv.lpl[b] : 0;

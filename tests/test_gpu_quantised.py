@@ -183,6 +183,31 @@ def test_more_tokens_than_the_table_holds_writes_none_of_the_excess():
     assert (back[0][:2] == 0).all() and (back[1][:2] == 0).all()
 
 
+@pytest.mark.parametrize("new", [[1, 2, 0, 1], [40, 3, 0, 7]])
+@pytest.mark.parametrize("normed,coded", [(True, False), (False, True), (True, True)])
+def test_rows_behind_the_last_sequence_stay(new, normed, coded):
+    m, past, H, D, page, block = lib(), [5, 0, 3, 16], 2, 64, 32, 16
+    lens, T = [a + b for a, b in zip(new, past)], sum(new)
+    tab = m.rope_table(64, 32, device=DEV)
+    cu = au.i32([0] + np.cumsum(new).tolist(), DEV)
+    k, v, q = (au.queries(T + 9, h, D, BF, 70 + i, DEV) for i, h in enumerate((H, H, 6)))
+    w = torch.ones(D, device=DEV) if normed else None
+
+    def run(rows):
+        a = Cache(lens, page, block, H, D, 73)
+        kv = a.c if coded else {n: torch.full(c.shape, 7.0, dtype=BF, device=DEV) for n, c in a.c.items()}
+        out = torch.full((T + 9, 6, D), 3.0, dtype=BF, device=DEV)
+        m.kv_append_paged(k[:rows], v[:rows], cu, **kv, **a.where, **(a.s if coded else {}), table=tab, q=q[:rows], q_out=out[:rows],
+                          q_norm=w, k_norm=w)
+        torch.cuda.synchronize()
+        return [out, *(x.view(torch.uint8) for x in kv.values()), *(a.s.values() if coded else ())]
+
+    exact, padded = run(T), run(T + 9)
+    assert (padded[0][T:] == 3.0).all() and torch.isfinite(padded[0]).all()
+    for x, y in zip(exact, padded):
+        assert torch.equal(x, y)
+
+
 def half_step(x):
     return 2.0 ** (np.floor(np.log2(np.maximum(np.abs(x), 2.0 ** -6))) - 4)
 
