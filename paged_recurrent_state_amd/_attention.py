@@ -499,8 +499,9 @@ def _attention(fn, q, cu_seqlens, k_cache, v_cache, page_indices, page_indptr, p
     if not coded and not sinks:
         _check(plain(d, *head, cache, *tail))
     else:
+        sinks = max(-1, min(int(sinks), (1 << 31) - 1))  # (the argument's 32 bits: the call refuses what is past its range)
         sc = _scales(k_scale, v_scale, k_cache, int(page_size), dev) if coded else None
-        _run(dev, ext, d, int(sinks), *head, cache, sc, *tail)
+        _run(dev, ext, d, sinks, *head, cache, sc, *tail)
     return (out, lse) if return_lse else out
 
 

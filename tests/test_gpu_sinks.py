@@ -128,3 +128,12 @@ def test_random_batches(seed):
     H, G = int(r.integers(1, 4)), int(r.integers(1, 6))
     check_prefill(new, past, page, H, G, D, dtype, 200 + seed, bool(r.integers(2)), **kw)
     check_decode([p + 1 for p in past], page, H, G, D, dtype, 300 + seed, **kw)
+
+
+@pytest.mark.parametrize("sinks", [-1, (1 << 30) + 1, 1 << 32, (1 << 32) + 4])
+def test_numbers_of_sinks_past_the_calls_range_are_refused(sinks):
+    q, cu, c = case([5], [20], 16, 1, 1, 64, BF, 95)
+    with pytest.raises(lib().GDNError, match="sinks"):
+        lib().attention_prefill_paged(q, au.i32(cu, DEV), **c, window=4, sinks=sinks)
+    with pytest.raises(lib().GDNError, match="sinks"):
+        lib().attention_decode_paged(q[:1], **c, window=4, sinks=sinks)
