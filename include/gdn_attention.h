@@ -276,10 +276,13 @@ typedef struct {
 /*
  * Workspace bytes of any attention call for at most total_tokens query rows
  * in at most num_seqs sequences (an upper bound that never decreases as either
- * grows), 256-byte aligned.  0 on bad dims.
+ * grows), 256-byte aligned.  0 on bad dims.  The second form: of calls over 16-bit
+ * caches alone (codes 0), or over 8-bit caches alone.
  */
 size_t gdn_attention_workspace_size(const gdn_attention_dims_t* dims, int64_t total_tokens,
                                     int32_t num_seqs);
+size_t gdn_attention_workspace_size_ext(const gdn_attention_dims_t* dims, int32_t codes,
+                                        int64_t total_tokens, int32_t num_seqs);
 
 /*
  * gdn_attention_prefill_paged -- attention of the batch's new tokens (q rows

@@ -452,16 +452,21 @@ def kv_read_paged(cu_seqlens, total_tokens: int, k_cache, v_cache, page_indices,
 
 @lru_cache(maxsize=256)
 def _workspace_size(total_tokens: int, num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
-                    device: int) -> int:
+                    device: int, coded: bool) -> int:
     d = _AttentionC(num_q_heads, num_kv_heads, head_dim, 0, 0.0, 0.0, 0, 1)
-    return int(load().gdn_attention_workspace_size(d, total_tokens, num_seqs))
+    return int(load().gdn_attention_workspace_size_ext(d, coded, total_tokens, num_seqs))
 
 
 def attention_workspace_size(total_tokens: int, num_seqs: int, num_q_heads: int, num_kv_heads: int,
-                             head_dim: int) -> int:
-    """Bytes either attention call needs for at most that many query rows and sequences."""
+                             head_dim: int, cache_dtype: Optional[torch.dtype] = None) -> int:
+    """Bytes either attention call needs for at most that many query rows and sequences, over caches of any
+    type, or of ``cache_dtype`` alone (those of 8 bits need less for up to 8 q-heads on a kv-head, and more beyond)."""
     d = _AttentionC(num_q_heads, num_kv_heads, head_dim, 0, 0.0, 0.0, 0, 1)
-    return int(load().gdn_attention_workspace_size(d, int(total_tokens), int(num_seqs)))
+    if cache_dtype is None:
+        return int(load().gdn_attention_workspace_size(d, int(total_tokens), int(num_seqs)))
+    if cache_dtype not in (torch.bfloat16, torch.float16, E4M3):
+        raise TypeError(f"cache_dtype must be bfloat16, float16 or {E4M3}, got {cache_dtype}")
+    return int(load().gdn_attention_workspace_size_ext(d, cache_dtype == E4M3, int(total_tokens), int(num_seqs)))
 
 
 def _attention(fn, q, cu_seqlens, k_cache, v_cache, page_indices, page_indptr, page_size, last_page_len,
@@ -486,7 +491,7 @@ def _attention(fn, q, cu_seqlens, k_cache, v_cache, page_indices, page_indptr, p
     else:
         o = _rows(out, "out", q.dtype, dev, Hq, T, D)
     lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if return_lse else None
-    ws = _workspace(workspace, _workspace_size(T, cache.num_seqs, Hq, k_cache.shape[2], D, dev.index), dev)
+    ws = _workspace(workspace, _workspace_size(T, cache.num_seqs, Hq, k_cache.shape[2], D, dev.index, coded), dev)
     tail = (o, lse.data_ptr() if return_lse else None, ws.data_ptr(), ws.numel() * ws.element_size(),
             stream)
     if fn == "prefill":

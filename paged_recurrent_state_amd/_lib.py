@@ -136,6 +136,7 @@ EXPORTS = ["gdn_check_paged", "gdn_prefill_slots", "gdn_decode_slots", "gdn_pref
            "gdn_prefill_paged", "gdn_prefill_paged_noalloc", "gdn_decode_paged", "gdn_prefill", "gdn_decode",
            "gdn_block_table_to_csr", "gdn_csr_to_block_table", "gdn_stream_copy", "gdn_last_error",
            "gdn_version", "gdn_rope_table", "gdn_rope", "gdn_kv_append_paged", "gdn_attention_workspace_size",
+           "gdn_attention_workspace_size_ext",
            "gdn_attention_prefill_paged", "gdn_attention_decode_paged", "gdn_norm_rope",
            "gdn_norm_rope_backward_workspace_size", "gdn_norm_rope_backward", "gdn_kv_append_paged_ext",
            "gdn_kv_read_paged", "gdn_attention_prefill_paged_ext", "gdn_attention_decode_paged_ext"]
@@ -179,6 +180,7 @@ def load():
         "gdn_rope": (C.c_int, [RP, I32, I32, I32, I32, I64, P, I32, R, R, R, R, P]),
         "gdn_kv_append_paged": (C.c_int, [RP, I32, I32, I32, I32, P, I64, R, R, KV, R, R, P]),
         "gdn_attention_workspace_size": (SZ, [AT, I64, I32]),
+        "gdn_attention_workspace_size_ext": (SZ, [AT, I32, I64, I32]),
         "gdn_attention_prefill_paged": (C.c_int, [AT, R, P, I64, KV, R, P, P, SZ, P]),
         "gdn_attention_decode_paged": (C.c_int, [AT, R, KV, R, P, P, SZ, P]),
         "gdn_norm_rope": (C.c_int, [NM, RP, I32, I32, I32, I32, I64, P, I32, R, R, R, R, P]),

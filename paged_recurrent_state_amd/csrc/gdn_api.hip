@@ -1215,9 +1215,14 @@ int gdn_kv_read_paged(int32_t dtype, int32_t head_dim, int32_t num_kv_heads, con
   return ok();
 }
 
-size_t gdn_attention_workspace_size(const gdn_attention_dims_t* dims, int64_t total_tokens, int32_t num_seqs) {
+size_t gdn_attention_workspace_size_ext(const gdn_attention_dims_t* dims, int32_t codes, int64_t total_tokens, int32_t num_seqs) {
   if (check_attention(dims) || total_tokens < 0 || num_seqs < 0) return 0;
-  return attention_bytes(dims->head_dim, total_tokens, num_seqs, dims->num_q_heads / dims->num_kv_heads, true);
+  return attention_bytes(dims->head_dim, total_tokens, num_seqs, dims->num_q_heads / dims->num_kv_heads, codes != 0);
+}
+
+size_t gdn_attention_workspace_size(const gdn_attention_dims_t* dims, int64_t total_tokens, int32_t num_seqs) {
+  return std::max(gdn_attention_workspace_size_ext(dims, 0, total_tokens, num_seqs),
+                  gdn_attention_workspace_size_ext(dims, 1, total_tokens, num_seqs));
 }
 
 int gdn_attention_prefill_paged_ext(const gdn_attention_dims_t* dims, int32_t sinks, const gdn_rows_t* q,

@@ -17,10 +17,13 @@ hipError_t launch_attention(const AttnParams& p, int D, int dtype, void* workspa
   return bf16 ? launch_chunk_bf16(p, D, workspace, s) : launch_chunk_f16(p, D, workspace, s);
 }
 
+template <int D>
+static size_t bytes_of(int64_t T, int64_t B, int64_t G, bool codes) {
+  return std::max(codes ? decode_bytes<D, true>(G) : decode_bytes<D, false>(G), chunk_ws<D>(T, B, G).total);
+}
+
 size_t attention_bytes(int D, int64_t T, int64_t B, int64_t G, bool codes) {
-  if (D == 64) return std::max(decode_bytes<64>(codes), chunk_ws<64>(T, B, G).total);
-  if (D == 128) return std::max(decode_bytes<128>(codes), chunk_ws<128>(T, B, G).total);
-  return std::max(decode_bytes<256>(codes), chunk_ws<256>(T, B, G).total);
+  return D == 64 ? bytes_of<64>(T, B, G, codes) : D == 128 ? bytes_of<128>(T, B, G, codes) : bytes_of<256>(T, B, G, codes);
 }
 
 }  // namespace gdn

@@ -1825,7 +1825,7 @@ __global__ __launch_bounds__(64 * kWaves, (kDecPerCu<D, Q8>)) void decode_kernel
           *(u32x2*)(dst + 16 * d) = u32x2{E::pack(o[d][0] * inv, o[d][1] * inv), E::pack(o[d][2] * inv, o[d][3] * inv)};
         if (p.lse && grp == 0) p.lse[(int64_t)b * p.Hq + hq] = (m + __builtin_amdgcn_logf(l)) * kLn2;
       } else {
-        const int64_t row = (2 * (int64_t)me + (head ? 0 : 1)) * kDecRows + col;
+        const int64_t row = (2 * (int64_t)me + (head ? 0 : 1)) * (Q8 ? p.part_rows : kDecRows) + col;
 #pragma unroll
         for (int d = 0; d < kBlocks; ++d) *(f32x4*)(p.part_o + row * D + 16 * d + 4 * grp) = o[d];
         if (grp == 0) *(float2*)(p.part_ml + row * 2) = float2{m, l};
@@ -1891,7 +1891,7 @@ __global__ __launch_bounds__(256) void decode_join_kernel(AttnParams p) {
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       const int i = min(i0 + x * kStep, parts - 1);
-      const int64_t row = (int64_t)(i == 0 ? 2 * w + 1 : 2 * (w + i)) * kDecRows + r;
+      const int64_t row = (int64_t)(i == 0 ? 2 * w + 1 : 2 * (w + i)) * p.part_rows + r;
       ml[x] = *(const float2*)(p.part_ml + row * 2);
       o[x] = *(const f32x4*)(p.part_o + row * D + d);
     }
@@ -1930,6 +1930,14 @@ int decode_shares() {
   return kWaves * device_cus() * kDecPerCu<D, Q8>;
 }
 
+// Rows of a part in the workspace.  Over codes as many as a run has: they have 1.5 to 2 times the waves, and need
+// no more than 16-bit calls for groups of up to 8 q-heads (a caller's buffer serves both; 4 q-heads on one of 128
+// 12.8 MB, over 16 bits 34.1).
+template <bool Q8>
+int dec_part_rows(int64_t group) {
+  return Q8 ? (int)std::min<int64_t>(kDecRows, group) : kDecRows;
+}
+
 template <class E, int D, Cap CAP, bool Q8>
 hipError_t launch_decode_cap(const AttnParams& p, hipStream_t s) {
   static std::atomic<bool> raised[kMaxDevices];
@@ -1952,18 +1960,18 @@ hipError_t launch_decode_cap(const AttnParams& p, hipStream_t s) {
 template <class E, int D, bool Q8>
 hipError_t launch_dec(AttnParams p, void* workspace, hipStream_t s) {
   const int shares = decode_shares<D, Q8>();
+  p.part_rows = dec_part_rows<Q8>(p.group.d);
   p.part_o = (float*)workspace;
-  p.part_ml = p.part_o + (int64_t)2 * shares * kDecRows * D;
-  p.parts = (int*)(p.part_ml + (int64_t)2 * shares * kDecRows * 2);
+  p.part_ml = p.part_o + (int64_t)2 * shares * p.part_rows * D;
+  p.parts = (int*)(p.part_ml + (int64_t)2 * shares * p.part_rows * 2);
   const int64_t items = (int64_t)p.kv.B * p.Hkv * ((p.group.d + kDecRows - 1) / kDecRows);
   p.records = items <= shares ? (int)items : 0;
   return p.cap > 0.f ? launch_decode_cap<E, D, kCap, Q8>(p, s) : launch_decode_cap<E, D, kNoCap, Q8>(p, s);
 }
 
-template <int D>
-size_t decode_bytes(bool codes) {
-  const int shares = codes ? decode_shares<D, true>() : decode_shares<D, false>();
-  return (size_t)shares * (2 * kDecRows * (D + 2) * sizeof(float) + 4 * sizeof(int));
+template <int D, bool Q8>
+size_t decode_bytes(int64_t group) {
+  return (size_t)decode_shares<D, Q8>() * (2 * dec_part_rows<Q8>(group) * (D + 2) * sizeof(float) + 4 * sizeof(int));
 }
 
 // Chunks of one element type, over a cache of the same type or (Q8) of 8 bits; decode of it.

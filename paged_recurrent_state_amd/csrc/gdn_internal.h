@@ -301,7 +301,7 @@ hipError_t launch_chunk_sinks_f16(const AttnParams& p, int D, void* workspace, h
 hipError_t launch_chunk8_f16(const AttnParams& p, int D, void* workspace, hipStream_t s);
 hipError_t launch_chunk8_sinks_f16(const AttnParams& p, int D, void* workspace, hipStream_t s);
 hipError_t launch_attention(const AttnParams& p, int D, int dtype, void* workspace, hipStream_t s);
-// workspace of launch_attention (codes: over an 8-bit cache, which needs the more)
+// workspace of launch_attention (codes: over an 8-bit cache)
 size_t attention_bytes(int D, int64_t T, int64_t B, int64_t group, bool codes);
 
 // Errors of the C-ABI layer (gdn_api.hip): the thread's message and a status.
