@@ -12,6 +12,7 @@ from functools import lru_cache
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 
 from ._lib import (GDN_INDEX_INT32, GDN_INDEX_INT64, _AttentionC, _CacheC, _check, _need, _NormC, _RopeC, _RowsC,
                    _ScalesC, _ScalingC, _workspace, load)
@@ -38,6 +39,12 @@ def _run(dev: torch.device, fn, *args):
     else:
         with torch.cuda.device(dev):
             _check(fn(*args))
+
+
+def _no_tangents(call: str, *tensors):
+    """Refuses dual tensors (those of forward-mode differentiation), whose tangents the kernels do not see."""
+    if any(isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise RuntimeError(f"{call} has no forward-mode derivative: its inputs must not be dual tensors")
 
 
 def _dense(shape, dtype, dev):
@@ -184,8 +191,11 @@ def rope(q, k, table, positions, interleaved: bool = False, transposed: bool = F
     transposed map.  A position outside the table gives NaN.
 
     q and k that require a gradient get it (the opposite map of the outputs' gradients); they and
-    ``q_out`` or ``k_out`` exclude each other, and the table has no gradient."""
+    ``q_out`` or ``k_out`` exclude each other, and the table has no gradient.  There is no forward-mode
+    derivative (dual tensors are refused)."""
     # (asked first and without a call: at one token the host's time is all there is)
+    if forward_ad._current_level >= 0:
+        _no_tangents("rope", q, k, table, q_out, k_out)
     if torch.is_grad_enabled() and (
             getattr(q, "requires_grad", False) or getattr(k, "requires_grad", False)
             or getattr(table, "requires_grad", False) or getattr(q_out, "requires_grad", False)
@@ -276,7 +286,9 @@ def norm_rope(q, k, q_weight, k_weight, table, positions, eps: float = 1e-6, wei
 
     ``q_weight`` and ``k_weight`` [D] are of the rows' type or fp32, both alike (D at most 512).  q, k and
     the weights that require a gradient get it; ``q_out`` or ``k_out`` (they may be q and k) exclude
-    that, and the table has no gradient."""
+    that, and the table has no gradient.  There is no forward-mode derivative (dual tensors are refused)."""
+    if forward_ad._current_level >= 0:
+        _no_tangents("norm_rope", q, k, q_weight, k_weight, table, q_out, k_out)
     if torch.is_grad_enabled() and (
             getattr(q, "requires_grad", False) or getattr(k, "requires_grad", False)
             or getattr(q_weight, "requires_grad", False) or getattr(k_weight, "requires_grad", False)
@@ -329,6 +341,8 @@ def norm_rope_backward(dq, dk, q, k, q_weight, k_weight, table, positions, eps: 
     """Gradients (of q, of k, of q_weight, of k_weight) from those of ``norm_rope``'s outputs, dq
     [T, Hq, D] and dk [T, Hk, D], and its inputs; dk, k and k_weight may be None together.  The weights'
     gradients are sums over all rows, in an order that depends on the sizes alone."""
+    if forward_ad._current_level >= 0:
+        _no_tangents("norm_rope_backward", dq, dk, q, k, q_weight, k_weight, table)
     lib = load()
     code, dev = _dtype(q, "q"), q.device
     stream = _stream(dev)
