@@ -153,7 +153,9 @@ int gdn_norm_rope(const gdn_norm_t* norm, const gdn_rope_t* rope, int32_t dtype,
  * an order that the sizes fix, so equal inputs give equal sums; zeros for no
  * tokens).  The workspace is 256-byte aligned, of
  * gdn_norm_rope_backward_workspace_size bytes (0 on bad sizes).
- * Errors as gdn_norm_rope, GDN_EWORKSPACE.
+ * Errors as gdn_norm_rope, GDN_EWORKSPACE, and GDN_EINVAL for gradients whose rows
+ * share memory they must not (where strides differ: whose spans do), the queries' with
+ * the keys' rows among it.
  */
 size_t gdn_norm_rope_backward_workspace_size(int32_t head_dim, int32_t num_q_heads,
                                              int32_t num_k_heads, int64_t num_tokens);

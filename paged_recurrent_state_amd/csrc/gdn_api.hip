@@ -723,30 +723,32 @@ bool aligned(const gdn_kv_cache_t* c, int32_t heads, int size, int bytes) {
          (heads < 2 || c->head_stride * size % bytes == 0);
 }
 
-// Whether rows of a and of b, each [tokens, heads, dim] of `size` bytes a value,
-// share memory.  Exact where the strides agree (one buffer's interleaved parts do not
-// share any), otherwise whether their spans do.
-bool share_memory(const gdn_rows_t* a, const gdn_rows_t* b, int64_t tokens, int32_t heads, int32_t dim, int size) {
+// Whether rows of a [tokens, heads, dim] and of b [tokens, b_heads, dim] of `size` bytes
+// a value share memory.  Exact where the strides agree (one buffer's interleaved parts do
+// not share any), otherwise whether their spans do.
+bool share_memory(const gdn_rows_t* a, int32_t heads, const gdn_rows_t* b, int32_t b_heads, int64_t tokens, int32_t dim, int size) {
   typedef __int128 Wide;
   struct Span {
     Wide lo, hi;
   };
   auto stride = [&](int64_t s, int64_t n) { return n > 1 ? (Wide)s * size : (Wide)0; };  // (one row: any stride)
-  auto span = [&](const gdn_rows_t* r) {
-    const Wide t = (tokens - 1) * stride(r->token_stride, tokens), h = (heads - 1) * stride(r->head_stride, heads);
+  auto span = [&](const gdn_rows_t* r, int32_t n) {
+    const Wide t = (tokens - 1) * stride(r->token_stride, tokens), h = (n - 1) * stride(r->head_stride, n);
     const Wide at = (Wide)(uintptr_t)r->data;
     return Span{at + std::min<Wide>(t, 0) + std::min<Wide>(h, 0),
                 at + std::max<Wide>(t, 0) + std::max<Wide>(h, 0) + (Wide)dim * size};
   };
-  const Span x = span(a), y = span(b);
+  const Span x = span(a, heads), y = span(b, b_heads);
   if (x.hi <= y.lo || y.hi <= x.lo) return false;
-  const Wide ts = stride(a->token_stride, tokens), hs = stride(a->head_stride, heads);
-  if (ts != stride(b->token_stride, tokens) || hs != stride(b->head_stride, heads)) return true;
+  // (a single head: any stride, the other's)
+  const Wide ts = stride(a->token_stride, tokens), hs = heads > 1 ? stride(a->head_stride, heads) : stride(b->head_stride, b_heads);
+  if (ts != stride(b->token_stride, tokens) || (b_heads > 1 && hs != stride(b->head_stride, b_heads))) return true;
   // rows i tokens and j heads apart: do they lie less than a row from each other for any i, j
   const Wide apart = (Wide)(uintptr_t)b->data - (Wide)(uintptr_t)a->data, row = (Wide)dim * size;
-  for (int64_t j = 1 - heads; j < heads; ++j) {
+  for (int64_t j = 1 - heads; j < b_heads; ++j) {
     const Wide r = apart + j * hs;
-    const Wide near_ = ts ? -r / ts : 0;  // (the i that brings them closest is this one or beside it)
+    // (the i that brings them closest is this one or beside it)
+    const Wide near_ = ts ? std::max<Wide>(1 - tokens, std::min<Wide>(tokens - 1, -r / ts)) : 0;
     for (Wide i = near_ - 1; i <= near_ + 1; ++i) {
       const Wide gap = r + i * ts;
       if (i > -tokens && i < tokens && gap < row && -gap < row) return true;
@@ -1016,7 +1018,7 @@ int run_attention(const gdn_attention_dims_t* dims, int32_t sinks, const gdn_row
   // writes it last.
   const bool same = q->data == out->data && (T < 2 || q->token_stride == out->token_stride) &&
                     (dims->num_q_heads < 2 || q->head_stride == out->head_stride);
-  if (!(same && !cu) && share_memory(q, out, T, dims->num_q_heads, dims->head_dim, 2))
+  if (!(same && !cu) && share_memory(q, dims->num_q_heads, out, dims->num_q_heads, T, dims->head_dim, 2))
     return fail(GDN_EINVAL, cu ? "out must not share memory with q"
                                : "out must be q itself or not share memory with it");
   p.q = rows_dev(q);
@@ -1138,8 +1140,19 @@ int gdn_norm_rope_backward(const gdn_norm_t* norm, const gdn_rope_t* rope, int32
     for (const gdn_rows_t* r : {a.x, a.out_grad}) {
       const bool same = r->data == a.x_grad->data && (num_tokens < 2 || r->token_stride == a.x_grad->token_stride) &&
                         (a.heads < 2 || r->head_stride == a.x_grad->head_stride);
-      if (num_tokens > 0 && !same && share_memory(r, a.x_grad, num_tokens, a.heads, head_dim, sz))
+      if (num_tokens > 0 && !same && share_memory(r, a.heads, a.x_grad, a.heads, num_tokens, head_dim, sz))
         return fail(GDN_EINVAL, "the gradient of %s must lie over the rows it is of, their outputs' gradient, or neither", a.name);
+    }
+  }
+  // (queries and keys are other workgroups')
+  if (num_tokens > 0 && num_q_heads > 0 && num_k_heads > 0) {
+    auto meet = [&](const Kind& a, const gdn_rows_t* r, const Kind& b) {
+      return share_memory(a.x_grad, a.heads, r, b.heads, num_tokens, head_dim, sz);
+    };
+    for (int i = 0; i < 2; ++i) {
+      const Kind &a = kinds[i], &b = kinds[1 - i];
+      if (meet(a, b.x, b) || meet(a, b.out_grad, b) || meet(a, b.x_grad, b))
+        return fail(GDN_EINVAL, "the gradient of %s must not share memory with the rows or gradients of %s", a.name, b.name);
     }
   }
   const size_t need = gdn_norm_rope_backward_workspace_size(head_dim, num_q_heads, num_k_heads, num_tokens);
