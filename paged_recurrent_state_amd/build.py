@@ -38,6 +38,11 @@ SOURCE_FLAGS = {
     src: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for src in (*CHUNKS, "gdn_attention.hip")
 }
 
+# Kernels that may move that many vector registers a thread to the other register file (none to memory): chunks of
+# capped scores over codes with sinks, bf16, heads of 128, where everything else fills both files.
+MOVED = {f"_ZN3gdn12_GLOBAL__N_112chunk_kernelINS0_2BfELi128ELNS0_3CapE{cap}ELb1ELb1ELb1EEEvNS_10AttnParamsE": 1
+         for cap in (1, 2)}
+
 
 def hipcc() -> str:
     cand = os.environ.get("HIPCC") or shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
@@ -47,8 +52,9 @@ def hipcc() -> str:
 
 
 def spills(remarks: str) -> dict:
-    """Kernels that keep vector registers in memory, from the compiler's resource remarks:
-    {name: (registers spilled, bytes of scratch a lane)}."""
+    """Kernels that do not keep every vector register where it is worked on, from the compiler's resource remarks:
+    {name: (registers spilled, bytes of scratch a lane)}.  Without scratch a spilled register is moved to the other
+    register file, not to memory."""
     found, name = {}, None
     for line in remarks.splitlines():
         m = re.search(r"remark:\s+(Function Name|VGPRs Spill|ScratchSize \[bytes/lane\]): (\S+)", line)
@@ -70,9 +76,8 @@ def _compile(src: str, csrc: str = CSRC, objdir: str = OBJDIR) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed on {src}:\n{r.stderr}")
     # the kernels are laid out to fit the registers (the chunk attention's instances take up to 480 of 512):
-    # one that no longer does is an error of its source, not only slower (without scratch a register moved
-    # between the two files, not to memory)
-    if bad := {name: s for name, s in spills(r.stderr).items() if s[1]}:
+    # one that no longer does is an error of its source, not only slower
+    if bad := {name: s for name, s in spills(r.stderr).items() if s[1] or s[0] > MOVED.get(name, 0)}:
         os.remove(obj)
         raise RuntimeError(f"kernels of {src} spill (vector registers, bytes of scratch a lane): {bad}")
     return obj
