@@ -92,7 +92,7 @@ __device__ __forceinline__ void find_leads(const RopeParams& p, const ScalesDev&
         l.dst = id * p.kv.ps + (int64_t)off * p.kv.ts;
         l.scale = id * sc.ps + (int64_t)blk * sc.bs;
         if (in == 0 || !p.cu || t == p.cu[b]) {
-          l.rows = (int)min((int64_t)sc.block.d - in, left);
+          l.rows = (int)min(min((int64_t)sc.block.d - in, left), p.T - t);  // (no row past the call's)
           l.before = in;
         }
       }
