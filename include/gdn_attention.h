@@ -42,7 +42,8 @@ typedef struct {
  * p is at k (or v) + p * page_stride + i * token_stride + h * head_stride + d,
  * in elements.  The keys and the values have the same strides, so pages laid
  * out [tokens, heads, dim] and [heads, tokens, dim], apart or interleaved in one
- * allocation, are all such caches.
+ * allocation, are all such caches.  page_stride and (of pages of more than one token)
+ * token_stride are 0 or more, GDN_EUNSUPPORTED otherwise; head_stride may be negative.
  */
 typedef struct {
   void* k;
@@ -325,7 +326,7 @@ int gdn_attention_decode_paged(const gdn_attention_dims_t* dims, const gdn_rows_
  *     that sees one infinite or NaN).
  * Errors as the calls above, and GDN_EINVAL for sinks < 0 or over 2^30, null or
  * unaligned scales or a bad block; GDN_EUNSUPPORTED for chunks over an 8-bit cache
- * whose token stride is negative or reaches 2^30 / page_size.
+ * whose token stride reaches 2^30 / page_size.
  */
 int gdn_attention_prefill_paged_ext(const gdn_attention_dims_t* dims, int32_t sinks,
                                     const gdn_rows_t* q, const int32_t* cu_seqlens,

@@ -769,6 +769,10 @@ int check_cache(const gdn_kv_cache_t* c) {
   if (c->page_size < 1) return fail(GDN_EINVAL, "page_size must be >= 1 (got %d)", c->page_size);
   if (c->num_seqs > 0 && (!c->k || !c->v || !c->page_indices || !c->page_indptr || !c->last_page_len))
     return fail(GDN_EINVAL, "the cache and its page table must not be NULL");
+  // (the kernels mark what is not there by a negative offset)
+  if (c->page_stride < 0 || (c->page_size > 1 && c->token_stride < 0))
+    return fail(GDN_EUNSUPPORTED, "caches take page and token strides of 0 and more (got %lld and %lld)", (long long)c->page_stride,
+                (long long)c->token_stride);
   return GDN_OK;
 }
 
@@ -1000,8 +1004,8 @@ int run_attention(const gdn_attention_dims_t* dims, int32_t sinks, const gdn_row
   AttnParams p{};
   if (scales)
     if (int rc = check_scales(scales, cache, dims->num_kv_heads, dims->head_dim, p.scales)) return rc;
-  if (scales && cu && (cache->token_stride < 0 || cache->token_stride >= (1 << 30) / cache->page_size))
-    return fail(GDN_EUNSUPPORTED, "chunks over an 8-bit cache take token strides of 0 .. 2^30 / page_size codes");
+  if (scales && cu && cache->token_stride >= (1 << 30) / cache->page_size)
+    return fail(GDN_EUNSUPPORTED, "chunks over an 8-bit cache take token strides below 2^30 / page_size codes");
   if (T == 0 || cache->num_seqs == 0) return ok();
   const int32_t group = dims->num_q_heads / dims->num_kv_heads;
   if (T * group >= (int64_t(1) << 31) - 4096)  // (32-bit row numbers, to the end of the last tile)

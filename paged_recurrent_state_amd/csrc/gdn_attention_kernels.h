@@ -1381,7 +1381,7 @@ hipError_t launch_chunk(AttnParams p, void* workspace, hipStream_t s) {
   // them whole, and a load goes by one place and 32-bit offsets; otherwise every row's place is staged
   // (1,024 tokens over 8,192, pages of 64 and of 100: 147 and 153 us at D 128; with its
   // tiles checked like the last ones, 232).
-  const bool even = p.kv.page.d % 16 == 0 && p.kv.ts >= 0 && p.kv.ts * p.kv.page.d < (int64_t(1) << 30);
+  const bool even = p.kv.page.d % 16 == 0 && p.kv.ts * p.kv.page.d < (int64_t(1) << 30);
   if constexpr (Q8) {
     // (blocks of a multiple of 16 tokens divide the pages)
     if (p.cap > kMostShort / kLn2) return launch_chunk_kernel<E, D, kCap, true, true, SINKS>(p, s);
