@@ -499,7 +499,10 @@ def _attention(fn, q, cu_seqlens, k_cache, v_cache, page_indices, page_indptr, p
     scale, softcap = 0.0 if scale is None else float(scale), 0.0 if softcap is None else float(softcap)
     if scale < 0.0 or softcap < 0.0:
         raise ValueError(f"scale and softcap must not be negative, got {scale} and {softcap}")
-    d = _AttentionC(Hq, k_cache.shape[2], D, code, scale, softcap, int(window), bool(causal))
+    window = int(window)
+    if window >> 31:  # (the argument's 32 bits: no sequence is longer, and a negative one is refused)
+        window = -1 if window < 0 else (1 << 31) - 1
+    d = _AttentionC(Hq, k_cache.shape[2], D, code, scale, softcap, window, bool(causal))
     if out is None:
         out, o = _dense((T, Hq, D), q.dtype, dev)
     else:
