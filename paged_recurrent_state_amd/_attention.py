@@ -14,8 +14,8 @@ from typing import Optional, Tuple
 import torch
 from torch.autograd import forward_ad
 
-from ._lib import (GDN_INDEX_INT32, GDN_INDEX_INT64, _AttentionC, _CacheC, _check, _need, _NormC, _RopeC, _RowsC,
-                   _ScalesC, _ScalingC, _workspace, load)
+from ._lib import (GDN_INDEX_INT32, GDN_INDEX_INT64, _AttentionC, _CacheC, _need, _NormC, _RopeC, _RowsC, _run, _ScalesC,
+                   _ScalingC, _workspace, load)
 from ._lib import _stream as _stream_of_device
 
 # element types (GDN_TYPE_*)
@@ -30,15 +30,6 @@ def _stream(dev: torch.device):
     if dev.type != "cuda" or dev.index is None:
         return _stream_of_device(dev)
     return torch._C._cuda_getCurrentRawStream(dev.index)
-
-
-def _run(dev: torch.device, fn, *args):
-    """A call of the library on the tensors' device, whichever is the current one."""
-    if dev.index == torch._C._cuda_getDevice():
-        _check(fn(*args))
-    else:
-        with torch.cuda.device(dev):
-            _check(fn(*args))
 
 
 def _no_tangents(call: str, *tensors):
@@ -176,7 +167,7 @@ def rope_table(positions: int, rot_dim: int, base: float = 10000.0, scaling: str
     stream = _stream(dev)
     sc = _ScalingC(ROPE_SCALINGS[scaling], base, factor, original, low_turns, high_turns, magnitude)
     table = torch.empty(max(int(positions), 0), max(int(rot_dim), 0), dtype=torch.float32, device=dev)
-    _check(lib.gdn_rope_table(sc, table.data_ptr(), int(positions), int(rot_dim), stream))
+    _run(dev, lib.gdn_rope_table, sc, table.data_ptr(), int(positions), int(rot_dim), stream)
     return table
 
 
@@ -261,7 +252,7 @@ def _rope_rows(q, k, table, positions, interleaved, transposed, q_out, k_out, no
     tail = (rp, code, D, Hq, Hk, T, positions.data_ptr(),
             GDN_INDEX_INT64 if positions.dtype == torch.int64 else GDN_INDEX_INT32, qr, kr, qo, ko, stream)
     if norm is None:
-        _check(lib.gdn_rope(*tail))
+        _run(dev, lib.gdn_rope, *tail)
     else:
         q_weight, k_weight, eps, offset = norm
         if q_weight is None or (k is not None and k_weight is None):
@@ -424,7 +415,7 @@ def kv_append_paged(k, v, cu_seqlens, k_cache, v_cache, page_indices, page_indpt
         else:
             qo = _rows(q_out, "q_out", k.dtype, dev, Hq, T, D)
     if q_norm is None and k_norm is None and not coded and k_scale is None and v_scale is None:
-        _check(lib.gdn_kv_append_paged(rp, code, D, Hq, Hk, cu, T, kr, vr, cache, qr, qo, stream))
+        _run(dev, lib.gdn_kv_append_paged, rp, code, D, Hq, Hk, cu, T, kr, vr, cache, qr, qo, stream)
         return q_out
     if q_norm is not None and q is None:
         raise ValueError("q_norm norms the queries: q is missing")
@@ -519,7 +510,7 @@ def _attention(fn, q, cu_seqlens, k_cache, v_cache, page_indices, page_indptr, p
             raise ValueError(f"q must have one row per sequence ({cache.num_seqs}), got {T}")
         head, plain, ext = (qr,), lib.gdn_attention_decode_paged, lib.gdn_attention_decode_paged_ext
     if not coded and not sinks:
-        _check(plain(d, *head, cache, *tail))
+        _run(dev, plain, d, *head, cache, *tail)
     else:
         sinks = max(-1, min(int(sinks), (1 << 31) - 1))  # (the argument's 32 bits: the call refuses what is past its range)
         sc = _scales(k_scale, v_scale, k_cache, int(page_size), dev) if coded else None

@@ -206,6 +206,15 @@ def _check(rc: int):
         raise GDNError(rc, load().gdn_last_error().decode())
 
 
+def _run(dev: torch.device, fn, *args):
+    """A call of the library on the tensors' device, whichever is the current one."""
+    if dev.index == torch._C._cuda_getDevice():
+        _check(fn(*args))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args))
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else C.c_void_p(t.data_ptr())
 
@@ -331,9 +340,8 @@ def prefill_slots(cu_seqlens, page_indices, page_indptr, last_page_len, page_siz
         buf = torch.empty(5, B, dtype=torch.int32, device=dev)
         out = PrefillSlots(*buf.unbind(0))
     sc = _PrefillSlotsC(*[t.data_ptr() for t in out])
-    _check(lib.gdn_prefill_slots(_ptr(cu_seqlens), _ptr(page_indices), _ptr(page_indptr),
-                                 _ptr(last_page_len), B, int(page_size), C.byref(sc),
-                                 _stream(dev)))
+    _run(dev, lib.gdn_prefill_slots, _ptr(cu_seqlens), _ptr(page_indices), _ptr(page_indptr),
+         _ptr(last_page_len), B, int(page_size), C.byref(sc), _stream(dev))
     return out
 
 
@@ -352,9 +360,8 @@ def check_paged(page_indices, page_indptr, last_page_len, page_size: int, num_pa
     word = out if out is not None else torch.empty(1, dtype=torch.int32, device=dev)
     B = last_page_len.shape[0]
     idx = page_indices if page_indices.numel() else page_indptr
-    _check(lib.gdn_check_paged(_ptr(cu_seqlens), _ptr(idx), _ptr(page_indptr),
-                               _ptr(last_page_len), B, int(page_size), int(num_pages), _ptr(word),
-                               _stream(dev)))
+    _run(dev, lib.gdn_check_paged, _ptr(cu_seqlens), _ptr(idx), _ptr(page_indptr),
+         _ptr(last_page_len), B, int(page_size), int(num_pages), _ptr(word), _stream(dev))
     return word
 
 
@@ -369,7 +376,7 @@ def stream_copy(dst: torch.Tensor, src: torch.Tensor) -> torch.Tensor:
     nbytes = src.numel() * src.element_size()
     if dst.numel() * dst.element_size() != nbytes:
         raise ValueError("dst and src differ in size")
-    _check(lib.gdn_stream_copy(_ptr(dst), _ptr(src), nbytes, _stream(src.device)))
+    _run(src.device, lib.gdn_stream_copy, _ptr(dst), _ptr(src), nbytes, _stream(src.device))
     return dst
 
 
@@ -386,8 +393,8 @@ def decode_slots(page_indices, page_indptr, last_page_len,
         buf = torch.empty(2, B, dtype=torch.int32, device=dev)
         out = DecodeSlots(*buf.unbind(0))
     sc = _DecodeSlotsC(*[t.data_ptr() for t in out])
-    _check(lib.gdn_decode_slots(_ptr(page_indices), _ptr(page_indptr), _ptr(last_page_len), B,
-                                C.byref(sc), _stream(dev)))
+    _run(dev, lib.gdn_decode_slots, _ptr(page_indices), _ptr(page_indptr), _ptr(last_page_len), B,
+         C.byref(sc), _stream(dev))
     return out
 
 
@@ -415,9 +422,9 @@ def block_table_to_csr(block_tables, ctx_lens, page_size: int, bad_rows: Optiona
     # empty tensors have no storage: stand-ins that are never read
     table = block_tables if block_tables.numel() else indices
     ctx = ctx_lens if B else lpl
-    _check(lib.gdn_block_table_to_csr(_ptr(table), max(block_tables.stride(0), mb), _ptr(ctx), B,
-                                      mb, int(page_size), _ptr(indptr), _ptr(indices), _ptr(lpl),
-                                      _ptr(bad_rows), _stream(dev)))
+    _run(dev, lib.gdn_block_table_to_csr, _ptr(table), max(block_tables.stride(0), mb), _ptr(ctx),
+         B, mb, int(page_size), _ptr(indptr), _ptr(indices), _ptr(lpl), _ptr(bad_rows),
+         _stream(dev))
     lpl = lpl[:B]
     return indptr, indices, lpl
 
@@ -440,9 +447,8 @@ def csr_to_block_table(page_indptr, page_indices, last_page_len, page_size: int,
     # empty tensors have no storage: stand-ins that are never read
     indices = page_indices if page_indices.numel() else ctx
     lpl = last_page_len if B else ctx
-    _check(lib.gdn_csr_to_block_table(_ptr(page_indptr), _ptr(indices), _ptr(lpl), B,
-                                      int(page_size), mb, _ptr(table), table.stride(0), _ptr(ctx),
-                                      _ptr(bad_rows), _stream(dev)))
+    _run(dev, lib.gdn_csr_to_block_table, _ptr(page_indptr), _ptr(indices), _ptr(lpl), B,
+         int(page_size), mb, _ptr(table), table.stride(0), _ptr(ctx), _ptr(bad_rows), _stream(dev))
     return table[:B, :mb], ctx[:B]
 
 
@@ -470,11 +476,10 @@ def prefill_paged(q, k, v, g, beta, cu_seqlens, state_pool, page_indices, page_i
         for t, nm in zip(slots, PrefillSlots._fields):
             _need(t, nm, torch.int32, dev)
         sc = C.byref(_PrefillSlotsC(*[t.data_ptr() for t in slots]))
-    _check(lib.gdn_prefill_paged(C.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
-                                 _ptr(cu_seqlens), B, T, _ptr(state_pool), stride,
-                                 _ptr(page_indices), _ptr(page_indptr), _ptr(last_page_len),
-                                 int(page_size), sc, _ptr(o), _ptr(ws),
-                                 ws.numel() * ws.element_size(), _stream(dev)))
+    _run(dev, lib.gdn_prefill_paged, C.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+         _ptr(cu_seqlens), B, T, _ptr(state_pool), stride, _ptr(page_indices), _ptr(page_indptr),
+         _ptr(last_page_len), int(page_size), sc, _ptr(o), _ptr(ws), ws.numel() * ws.element_size(),
+         _stream(dev))
     return o
 
 
@@ -502,11 +507,9 @@ def prefill_paged_noalloc(q, k, v, g, beta, cu_seqlens, state_pool, page_indices
         for t, nm in zip(slots, PrefillSlots._fields):
             _need(t, nm, torch.int32, dev)
         sc = C.byref(_PrefillSlotsC(*[t.data_ptr() for t in slots]))
-    _check(lib.gdn_prefill_paged_noalloc(C.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
-                                         _ptr(beta), _ptr(cu_seqlens), B, T, _ptr(state_pool),
-                                         stride, _ptr(page_indices), _ptr(page_indptr),
-                                         _ptr(last_page_len), int(page_size), sc, _ptr(o),
-                                         _stream(dev)))
+    _run(dev, lib.gdn_prefill_paged_noalloc, C.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
+         _ptr(beta), _ptr(cu_seqlens), B, T, _ptr(state_pool), stride, _ptr(page_indices),
+         _ptr(page_indptr), _ptr(last_page_len), int(page_size), sc, _ptr(o), _stream(dev))
     return o
 
 
@@ -531,10 +534,9 @@ def decode_paged(q, k, v, g, beta, state_pool, page_indices, page_indptr, page_s
         for t, nm in zip(slots, DecodeSlots._fields):
             _need(t, nm, torch.int32, dev)
         sc = C.byref(_DecodeSlotsC(*[t.data_ptr() for t in slots]))
-    _check(lib.gdn_decode_paged(C.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), B,
-                                _ptr(state_pool), stride, _ptr(page_indices),
-                                _ptr(page_indptr), _ptr(last_page_len), int(page_size), sc,
-                                _ptr(o), _stream(dev)))
+    _run(dev, lib.gdn_decode_paged, C.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), B,
+         _ptr(state_pool), stride, _ptr(page_indices), _ptr(page_indptr), _ptr(last_page_len),
+         int(page_size), sc, _ptr(o), _stream(dev))
     return o
 
 
@@ -571,14 +573,12 @@ def prefill(q, k, v, g, beta, cu_seqlens, *, initial_state=None, state_indices=N
     B = cu_seqlens.shape[0] - 1
     o = out if out is not None else torch.empty(T, H, V, dtype=torch.bfloat16, device=dev)
     ws = _workspace(workspace, lib.gdn_prefill_workspace_size(T, B, C.byref(d)), dev)
-    _check(lib.gdn_prefill(C.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
-                           _ptr(cu_seqlens), B, T, _ptr(initial_state), strides[0],
-                           _ptr(state_indices), _ptr(output_state), strides[1],
-                           _ptr(output_state_indices), int(bool(output_final_state)),
-                           _ptr(state_checkpoints), strides[2], _ptr(checkpoint_state_indices),
-                           _ptr(checkpoint_cu_starts), _ptr(prefix_lens),
-                           int(checkpoint_every_n_tokens), idt, _ptr(o), _ptr(ws),
-                           ws.numel() * ws.element_size(), _stream(dev)))
+    _run(dev, lib.gdn_prefill, C.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+         _ptr(cu_seqlens), B, T, _ptr(initial_state), strides[0], _ptr(state_indices),
+         _ptr(output_state), strides[1], _ptr(output_state_indices), int(bool(output_final_state)),
+         _ptr(state_checkpoints), strides[2], _ptr(checkpoint_state_indices),
+         _ptr(checkpoint_cu_starts), _ptr(prefix_lens), int(checkpoint_every_n_tokens), idt,
+         _ptr(o), _ptr(ws), ws.numel() * ws.element_size(), _stream(dev))
     return o
 
 
@@ -605,10 +605,9 @@ def decode(q, k, v, g, beta, *, initial_state=None, initial_state_indices=None,
     if output_state is not None:
         s_out = _pool_stride(output_state, "output_state", H, V, K)
     o = out if out is not None else torch.empty(B, H, V, dtype=torch.bfloat16, device=dev)
-    _check(lib.gdn_decode(C.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), B,
-                          _ptr(initial_state), s_in, _ptr(initial_state_indices),
-                          _ptr(output_state), s_out, _ptr(output_state_indices), idt, _ptr(o),
-                          _stream(dev)))
+    _run(dev, lib.gdn_decode, C.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), B,
+         _ptr(initial_state), s_in, _ptr(initial_state_indices), _ptr(output_state), s_out,
+         _ptr(output_state_indices), idt, _ptr(o), _stream(dev))
     return o
 
 
