@@ -219,10 +219,10 @@ typedef struct {
  * they are, and with norm or scales also rows of q_out behind the last sequence.
  * Errors as gdn_kv_append_paged and gdn_norm_rope (but that a null weight leaves
  * its heads as they are), GDN_EINVAL for null or unaligned scales, a bad block,
- * or a cache that is not 16-byte aligned in every stride and address;
+ * or an 8-bit cache that is not 16-byte aligned in every stride and address;
  * GDN_EUNSUPPORTED for an 8-bit cache of fp32 rows, of heads other than 64, 128
- * or 256, of rows that are not 4-byte aligned, or with a rot_dim that is not a
- * multiple of 4.
+ * or 256, with rows of k, v, q or q_out that are not 4-byte aligned, a rot_dim that
+ * is not a multiple of 4 or a rope table that is not 8-byte aligned.
  */
 int gdn_kv_append_paged_ext(const gdn_norm_t* norm, const gdn_rope_t* rope, int32_t dtype,
                             int32_t head_dim, int32_t num_q_heads, int32_t num_kv_heads,
@@ -238,7 +238,10 @@ int gdn_kv_append_paged_ext(const gdn_norm_t* norm, const gdn_rope_t* rope, int3
  * cu_seqlens[b] tokens of sequence b (cu_seqlens NULL: one each), exact in bf16 and
  * fp32 and rounded in fp16.  A row whose sequence holds fewer tokens is zeros, rows
  * behind the last sequence are left as they are.
- * Errors as gdn_kv_append_paged_ext.
+ * Errors: GDN_EINVAL (null pointers, negative sizes, num_kv_heads < 1, an unknown
+ * type, total_tokens other than num_seqs without cu_seqlens, null or unaligned
+ * scales, a bad block, a cache or rows of k and v that are not 16-byte aligned in every
+ * stride and address), GDN_EUNSUPPORTED (heads other than 64, 128 or 256), GDN_ELAUNCH.
  */
 int gdn_kv_read_paged(int32_t dtype, int32_t head_dim, int32_t num_kv_heads,
                       const int32_t* cu_seqlens, int64_t total_tokens, const gdn_kv_cache_t* cache,
