@@ -465,7 +465,7 @@ def _workspace_size(total_tokens: int, num_seqs: int, num_q_heads: int, num_kv_h
 def attention_workspace_size(total_tokens: int, num_seqs: int, num_q_heads: int, num_kv_heads: int,
                              head_dim: int, cache_dtype: Optional[torch.dtype] = None) -> int:
     """Bytes either attention call needs for at most that many query rows and sequences, over caches of any
-    type, or of ``cache_dtype`` alone (those of 8 bits need less for up to 8 q-heads on a kv-head, and more beyond)."""
+    type, or of ``cache_dtype`` alone (those of 8 bits need less for up to 7 q-heads on a kv-head, and more beyond)."""
     d = _AttentionC(num_q_heads, num_kv_heads, head_dim, 0, 0.0, 0.0, 0, 1)
     if cache_dtype is None:
         return int(load().gdn_attention_workspace_size(d, int(total_tokens), int(num_seqs)))

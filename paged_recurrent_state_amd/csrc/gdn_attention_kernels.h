@@ -1931,7 +1931,7 @@ int decode_shares() {
 }
 
 // Rows of a part in the workspace.  Over codes as many as a run has: they have 1.5 to 2 times the waves, and need
-// no more than 16-bit calls for groups of up to 8 q-heads (a caller's buffer serves both; 4 q-heads on one of 128
+// no more than 16-bit calls for groups of up to 7 q-heads (a caller's buffer serves both; 4 q-heads on one of 128
 // 12.8 MB, over 16 bits 34.1).
 template <bool Q8>
 int dec_part_rows(int64_t group) {

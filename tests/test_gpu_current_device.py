@@ -1,5 +1,5 @@
-"""Every call runs on its tensors' device when another one is current: it is made current for the call (there is one
-GPU here, so the current device's number is made up and the change of device recorded)."""
+"""Every call runs on its tensors' device when another one is current: it is made current for the call (one GPU
+suffices: the current device's number is made up, and the change of device recorded)."""
 
 import pytest
 import torch

@@ -10,7 +10,7 @@ from paged_recurrent_state_amd import _attention, _lib
 from paged_recurrent_state_amd._lib import _AttentionC
 
 BF, HF, E4M3 = torch.bfloat16, torch.float16, torch.float8_e4m3fn
-HEADS = [(1, 1), (8, 2), (32, 8), (24, 2), (16, 1), (64, 2)]
+HEADS = [(1, 1), (8, 2), (32, 8), (7, 1), (8, 1), (24, 2), (16, 1), (64, 2)]
 
 
 def parts(waves, rows, dim):
@@ -26,7 +26,7 @@ def test_needs(heads, dim):
         any_, codes = (gdn.attention_workspace_size(T, B, Hq, Hk, dim, *x) for x in ((), (E4M3,)))
         plain = gdn.attention_workspace_size(T, B, Hq, Hk, dim, BF)
         assert plain == gdn.attention_workspace_size(T, B, Hq, Hk, dim, HF) and any_ == max(plain, codes)
-        if Hq // Hk <= 8:
+        if Hq // Hk <= 7:
             assert codes <= plain
     # one token: the waves' parts, and nothing else, with the compute units of the first line
     cus = gdn.attention_workspace_size(1, 1, Hq, Hk, 64, BF) // parts(8, 16, 64)
